@@ -72,7 +72,13 @@ typedef enum { PKV_F16 = 0, PKV_BF16 = 1, PKV_F32 = 2 } pkv_dtype;
  * query rows (tcgen05 tensor cores).  MIXED: a batch holding both; requests with
  * one query row take the decode path, longer ones the prefill path, and one
  * persistent kernel serves both on disjoint SMs (see pkv_batch_mixed_paged). */
-typedef enum { PKV_PLAN_DECODE = 0, PKV_PLAN_PREFILL = 1, PKV_PLAN_MIXED = 2 } pkv_plan_kind;
+typedef enum {
+    PKV_PLAN_DECODE = 0,
+    PKV_PLAN_PREFILL = 1,
+    PKV_PLAN_MIXED = 2,
+    PKV_PLAN_DECODE_KV8 = 3,  /* pkv_batch_decode_paged_kv8: the same over the 8-bit cache */
+    PKV_PLAN_PREFILL_KV8 = 4  /* pkv_batch_prefill_paged_kv8 */
+} pkv_plan_kind;
 
 /* Problem description shared by plan and run calls. */
 typedef struct {
@@ -470,6 +476,110 @@ pkv_status pkv_append_paged_kv(const pkv_params* params, int batch, int64_t nnz,
                                const int32_t* kv_indices_d, const int32_t* kv_last_page_len_d,
                                const void* k_new, const void* v_new, void* kv_data, const void* q_in,
                                void* q_out, double rope_theta, int32_t* error_d, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions on several axes, and the 8-bit cache.
+ *
+ * The FlashInfer pages have no counterpart of either (they name RoPE only as a
+ * query/key transform that an attention variant fuses).
+ */
+
+/*
+ * A rotation by positions on num_axes axes (a picture's or a video's tokens
+ * have a time, a height and a width; a text token has one position, given on
+ * every axis).  The first rotary_dim elements of a head row are turned, the rest is
+ * copied: element i < rotary_dim/2 pairs with i + rotary_dim/2, and pair i turns by
+ * the angle position[axis(i)] * theta^(-2i/rotary_dim).
+ * sections[x] is the number of pairs of axis x.  interleaved = 0: axis 0 has the
+ * first sections[0] pairs, axis 1 the next sections[1], and so on.  interleaved = 1:
+ * the pairs are dealt to the axes in turn, an axis without pairs left passed over.
+ */
+typedef struct {
+    double theta;       /* > 0 */
+    int rotary_dim;     /* a multiple of 16 in [16, head_dim] */
+    int num_axes;       /* 1..4 */
+    int sections[4];    /* >= 0; the first num_axes of them sum to rotary_dim / 2 */
+    int interleaved;    /* 0 or 1 */
+} pkv_rope_axes;
+
+/*
+ * pkv_append_paged_kv with the positions given, on one axis or several: append
+ * new tokens' K and V into their pages, keys and queries turned on the way.
+ * Arguments as there, but for
+ * rope        : the rotation; NULL: keys and queries are copied unchanged.
+ * positions_d : [num_axes, nnz] int32 device, any int32 values; new token t's
+ *               position on axis x is entry x * nnz + t.  NULL: a token's place in its
+ *               request (kv_len_b - n_b + i) on every axis.  They turn the rows and
+ *               have no part in where a token is stored.
+ * q_in, q_out : both NULL or neither.
+ * Angles are computed modulo a turn in 64-bit fixed point, exactly for every int32
+ * position.  Errors: as pkv_append_paged_kv; PKV_ERR_INVALID_ARG also for a rotation
+ * out of the ranges above.  Tokens named wrongly by the device arrays are skipped
+ * and flagged in error_d as there.
+ */
+pkv_status pkv_append_paged_kv_axes(const pkv_params* params, const pkv_rope_axes* rope, int batch, int64_t nnz,
+                                    int64_t num_pages, const int32_t* append_indptr_d, const int32_t* kv_indptr_d,
+                                    const int32_t* kv_indices_d, const int32_t* kv_last_page_len_d,
+                                    const int32_t* positions_d, const void* k_new, const void* v_new, void* kv_data,
+                                    const void* q_in, void* q_out, int32_t* error_d, void* stream);
+
+/*
+ * The 8-bit cache: half the bytes of kv_data for the same tokens.
+ *   kv8        [num_pages, 2, num_kv_heads, page_size, head_dim] e4m3 codes, one byte each
+ *   kv8_scales [num_pages, 2, num_kv_heads, page_size] one byte s for each head row:
+ *              code c stands for e4m3(c) * 2^(s - 127)
+ * (K at index 0, V at index 1, as in kv_data.)
+ *
+ * pkv_append_paged_kv8 appends new tokens' K and V into it; arguments as for
+ * pkv_append_paged_kv_axes (k_new, v_new, q_in and q_out are of params->dtype).  For each
+ * head row s = max(E - 7, 1), E the exponent field (0..254) of the row's largest
+ * finite magnitude as a float32, taken before the rotation; the row, turned in float32
+ * if it is a key's, times 2^(127 - s) is rounded to the nearest e4m3, ties to even.
+ * The largest element of an unturned row lies in [128, 256) before that, and a
+ * turned one below 256 sqrt(2) < 448, the largest e4m3.  Infinite elements become
+ * +-448 of their row's scale (NaN where a rotation makes one of them), NaN stays NaN.
+ * kv8 must be 16-byte aligned, kv8_scales 4-byte.
+ * Errors: as pkv_append_paged_kv_axes.
+ */
+pkv_status pkv_append_paged_kv8(const pkv_params* params, const pkv_rope_axes* rope, int batch, int64_t nnz,
+                                int64_t num_pages, const int32_t* append_indptr_d, const int32_t* kv_indptr_d,
+                                const int32_t* kv_indices_d, const int32_t* kv_last_page_len_d,
+                                const int32_t* positions_d, const void* k_new, const void* v_new, void* kv8,
+                                uint8_t* kv8_scales, const void* q_in, void* q_out, int32_t* error_d, void* stream);
+
+/*
+ * Batch decode over the 8-bit cache, on a plan of kind PKV_PLAN_DECODE_KV8: what
+ * pkv_batch_decode_paged computes, with K and V the values that kv8 and kv8_scales
+ * stand for.  q and o are of params->dtype; page sizes, groups, head_dims,
+ * split-KV, the plan's workspaces, capture and the error word as there (every group
+ * runs the same kernel, and one-row pages need no tensor map).  Slots past
+ * kv_last_page_len are not read.  Products are exact in the tensor cores' fp16
+ * operands, with fp32 sums: queries keep 11 significant bits relative to their row's
+ * largest element, probabilities 11 bits.
+ * Errors: PKV_ERR_INVALID_ARG (a null or misaligned pointer, a plan of another kind or
+ * not planned), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const void* kv8, const uint8_t* kv8_scales,
+                                      const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
+                                      const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
+                                      void* stream);
+
+/*
+ * Batch prefill over the 8-bit cache, on a plan of kind PKV_PLAN_PREFILL_KV8: what
+ * pkv_batch_prefill_paged computes (ragged query rows, causal or not; with causal = 0
+ * also rows against states of another length, and the shared-prefix half of cascade
+ * attention), with K and V the values that kv8 and kv8_scales stand for.  Built for
+ * head_dim 128, groups 1/2/4/8 and every page size.  The keys and values that the batch
+ * names are first expanded, exactly, into 16-row pages of params->dtype in the device
+ * workspace (pkv_plan_workspace_bytes counts them: up to limits->max_kv_pages pages'
+ * keys), each once however many rows see it; the tensor-core kernel reads those.
+ * Values past fp16's range become infinite when dtype is PKV_F16.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, const int32_t* qo_indptr_d,
+                                       const void* kv8, const uint8_t* kv8_scales, const int32_t* kv_indices_d,
+                                       const int32_t* kv_indptr_d, const int32_t* kv_last_page_len_d, void* o,
+                                       float* lse, void* dev_ws, void* stream);
 
 /*
  * Read (and, with clear != 0, reset) the device error word a plan's kernels

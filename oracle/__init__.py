@@ -28,6 +28,9 @@ arguments through ctypes.  Every function follows the FlashInfer pages:
                        the rotary query/key transform (fdeinterviews
                        summary, "Customizable attention"), in plain numpy
                        fp64.
+* ``rope_axes``, ``e4m3_values``, ``e4m3_round``, ``kv8_exponents``, ``kv8_values`` -- rotary
+                       positions on several axes, and the 8-bit cache's codes and
+                       scales (no counterpart on the pages).
 * ``encode16``      -- fp64 -> fp16/bf16 storage, round to nearest even.
 
 Parity pins: see tests/test_oracle_pins.py.  Every function here is pinned.
@@ -301,6 +304,67 @@ def rope(x, positions, theta: float, dtype: Optional[str] = None) -> np.ndarray:
     s = np.sin(ang)[:, None, :]
     a, b = xv[..., :half], xv[..., half:]
     return np.concatenate([a * c - b * s, b * c + a * s], axis=-1)
+
+
+def rope_axes(x, positions, theta: float, rotary_dim: int, sections, interleaved: bool,
+              dtype: Optional[str] = None) -> np.ndarray:
+    """Rotary embedding with positions [axes, n] on several axes, in long double, returned as fp64.
+
+    The first rotary_dim elements of a row turn in pairs (i, i + rotary_dim/2), pair i by
+    positions[axis(i)] * theta^(-2i/rotary_dim); the rest is copied.  sections[a] pairs belong to axis
+    a: the first sections[0] pairs to axis 0 and so on, or (interleaved) dealt to the axes in turn,
+    an axis that has all of its pairs passed over.
+    """
+    xv = _as_f64(x, dtype)
+    half = rotary_dim // 2
+    if interleaved:
+        queue = [(k, a) for a, n in enumerate(sections) for k in range(n)]  # the k-th pair of axis a, by rounds
+        axis = [a for _, a in sorted(queue)]
+    else:
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    if len(axis) != half:
+        raise ValueError("the sections must sum to rotary_dim / 2")
+    pos = np.asarray(positions, dtype=np.longdouble)[np.array(axis)].T            # [n, half]
+    freq = np.longdouble(theta) ** (np.longdouble(-2) * np.arange(half) / np.longdouble(rotary_dim))
+    ang = pos * freq
+    c = np.cos(ang).astype(np.float64)[:, None, :]
+    s = np.sin(ang).astype(np.float64)[:, None, :]
+    a, b = xv[..., :half], xv[..., half:rotary_dim]
+    return np.concatenate([a * c - b * s, b * c + a * s, xv[..., rotary_dim:]], axis=-1)
+
+
+def e4m3_values() -> np.ndarray:
+    """The 256 e4m3 values by code: sign, 4 exponent bits (bias 7), 3 mantissa bits, subnormals at
+    exponent 0, no infinities, NaN at mantissa and exponent all ones."""
+    code = np.arange(256)
+    e, f = (code >> 3) & 15, code & 7
+    v = np.where(e == 0, f * 2.0 ** -9, (8 + f) * 2.0 ** (e - 10.0))
+    v = np.where(code & 128, -v, v)
+    v[(code & 127) == 127] = np.nan
+    return v
+
+
+def e4m3_round(x) -> np.ndarray:
+    """fp64 to the nearest e4m3 value, ties to the even mantissa, past +-448 to +-448, NaN kept."""
+    x = np.asarray(x, dtype=np.float64)
+    _, e = np.frexp(np.where(np.isfinite(x), x, 0.0))
+    step = 2.0 ** (np.maximum(e - 1, -6) - 3.0)
+    with np.errstate(invalid="ignore"):
+        return np.clip(np.rint(x / step) * step, -448.0, 448.0)
+
+
+def kv8_exponents(x, dtype: Optional[str] = None) -> np.ndarray:
+    """Exponent bytes of head rows x [..., d]: max(E - 7, 1), E the float32 exponent field of the
+    largest finite magnitude."""
+    xv = np.abs(_as_f64(x, dtype))
+    top = np.where(np.isfinite(xv), xv, 0.0).max(axis=-1).astype(np.float32)
+    return np.maximum((top.view(np.uint32) >> 23).astype(np.int64) - 7, 1)
+
+
+def kv8_values(codes, scales) -> np.ndarray:
+    """What an 8-bit cache's codes (uint8) and exponent bytes stand for, in fp64."""
+    c, s = np.asarray(codes, dtype=np.uint8), np.asarray(scales, dtype=np.uint8)
+    return e4m3_values()[c] * 2.0 ** (s.astype(np.float64) - 127.0)[..., None]
 
 
 def _as_f64(x, dtype: Optional[str]) -> np.ndarray:

@@ -23,6 +23,7 @@ from . import build as _build
 PKV_OK = 0
 PKV_F16, PKV_BF16, PKV_F32 = 0, 1, 2
 PLAN_DECODE, PLAN_PREFILL, PLAN_MIXED = 0, 1, 2
+PLAN_DECODE_KV8, PLAN_PREFILL_KV8 = 3, 4  # over the 8-bit cache
 
 _DTYPES = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
 
@@ -43,6 +44,11 @@ class Limits(ctypes.Structure):
     _fields_ = [("max_batch", ctypes.c_int), ("max_total_q", ctypes.c_int64), ("max_kv_pages", ctypes.c_int64)]
 
 
+class RopeAxes(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_double), ("rotary_dim", ctypes.c_int), ("num_axes", ctypes.c_int),
+                ("sections", ctypes.c_int * 4), ("interleaved", ctypes.c_int)]
+
+
 class PlanInfo(ctypes.Structure):
     _fields_ = [("grid_ctas", ctypes.c_int), ("workers", ctypes.c_int), ("active_workers", ctypes.c_int),
                 ("num_work", ctypes.c_int), ("num_merge", ctypes.c_int), ("num_slots", ctypes.c_int),
@@ -60,7 +66,8 @@ EXPORTS = [
     "pkv_get_device_error",
     "pkv_plan_set_timing_events", "pkv_batch_decode_paged_noalloc", "pkv_append_paged_kv",
     "pkv_batch_prefill_paged_masked", "pkv_batch_mixed_paged", "pkv_plan_set_pipelined",
-    "pkv_plan_set_split_kv",
+    "pkv_plan_set_split_kv", "pkv_append_paged_kv_axes", "pkv_append_paged_kv8", "pkv_batch_decode_paged_kv8",
+    "pkv_batch_prefill_paged_kv8",
 ]
 
 
@@ -103,6 +110,12 @@ def load(path: Optional[str] = None):
             "pkv_plan_set_split_kv": (i32, [vp, i32]),
             "pkv_append_paged_kv": (i32, [ctypes.POINTER(Params), i32, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp,
                                           vp, ctypes.c_double, vp, vp]),
+            "pkv_append_paged_kv_axes": (i32, [ctypes.POINTER(Params), ctypes.POINTER(RopeAxes), i32, i64, i64, vp, vp,
+                                               vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "pkv_append_paged_kv8": (i32, [ctypes.POINTER(Params), ctypes.POINTER(RopeAxes), i32, i64, i64, vp, vp, vp,
+                                           vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "pkv_batch_decode_paged_kv8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "pkv_batch_prefill_paged_kv8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -301,6 +314,115 @@ def append_paged_kv(params: Params, append_indptr, kv_indptr, kv_indices, kv_las
                                       _ptr(error), _stream(stream)), "pkv_append_paged_kv")
 
 
+def make_rope_axes(theta: float, rotary_dim: int, sections, interleaved: bool = False) -> RopeAxes:
+    """A rotation by positions on len(sections) axes (1 to 4), sections[x] pairs of elements to axis x;
+    the sections sum to rotary_dim / 2."""
+    s = [int(x) for x in sections]
+    if not 1 <= len(s) <= 4:
+        raise ValueError("sections must name 1 to 4 axes")
+    return RopeAxes(float(theta), int(rotary_dim), len(s), (ctypes.c_int * 4)(*s), int(bool(interleaved)))
+
+
+def _same_device(*tensors) -> None:
+    """Every tensor on the current CUDA device (the kernels are launched there)."""
+    if any(x is not None and not x.is_cuda for x in tensors):
+        raise ValueError("tensors must be on a CUDA device")
+    dev = torch.cuda.current_device()
+    if any(x is not None and x.device.index != dev for x in tensors):
+        raise ValueError(f"tensors must be on the current device cuda:{dev}")
+
+
+def _int32(**tensors) -> None:
+    for name, x in tensors.items():
+        if x is not None and x.dtype != torch.int32:
+            raise ValueError(f"{name} must be int32")
+
+
+def _kv8_tensors(params: Params, kv8, kv8_scales) -> None:
+    if kv8.element_size() != 1 or kv8_scales.dtype != torch.uint8:
+        raise ValueError("kv8 must hold one byte per element (float8_e4m3fn or uint8) and kv8_scales be uint8")
+    want = (2, params.num_kv_heads, params.page_size, params.head_dim)
+    if tuple(kv8.shape[1:]) != want or tuple(kv8_scales.shape) != tuple(kv8.shape[:-1]):
+        raise ValueError("kv8 must be [num_pages, 2, num_kv_heads, page_size, head_dim] and kv8_scales the same "
+                         "without head_dim")
+
+
+def _append_tensors(params: Params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
+                    v_new, q_in, q_out, error):
+    batch, nnz = int(append_indptr.numel()) - 1, int(k_new.shape[0])
+    _int32(append_indptr=append_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices, kv_last_page_len=kv_last_page_len,
+           positions=positions, error=error)
+    if batch < 0 or kv_indptr.numel() != batch + 1 or kv_last_page_len.numel() != batch:
+        raise ValueError("append_indptr and kv_indptr must have batch + 1 entries, kv_last_page_len batch")
+    dtype = next((t for t, c in _DTYPES.items() if c == params.dtype), None)
+    rows = [(k_new, params.num_kv_heads), (v_new, params.num_kv_heads), (q_in, params.num_qo_heads),
+            (q_out, params.num_qo_heads)]
+    for x, heads in rows:
+        if x is not None and (tuple(x.shape) != (nnz, heads, params.head_dim) or x.dtype != dtype):
+            raise ValueError("k_new, v_new, q_in and q_out must be [nnz, heads, head_dim] of the params' dtype")
+    if positions is not None:
+        if rope is None:
+            raise ValueError("positions without a rotation")
+        if tuple(positions.shape) != (rope.num_axes, nnz):
+            raise ValueError("positions must be [num_axes, nnz]")
+    return batch, nnz
+
+
+def append_paged_kv_axes(params: Params, rope: Optional[RopeAxes], append_indptr, kv_indptr, kv_indices,
+                         kv_last_page_len, positions, k_new, v_new, kv_data, q_in=None, q_out=None, error=None,
+                         stream=None) -> None:
+    """``append_paged_kv`` with the rotation's positions given ([num_axes, nnz] int32; None: each
+    token's place in its request); rope None copies keys and queries.  q_out may be q_in (the default)."""
+    if q_in is not None and q_out is None:
+        q_out = q_in
+    batch, nnz = _append_tensors(params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
+                                 v_new, q_in, q_out, error)
+    if tuple(kv_data.shape[1:]) != (2, params.num_kv_heads, params.page_size, params.head_dim) or \
+            kv_data.dtype != k_new.dtype:
+        raise ValueError("kv_data must be [num_pages, 2, num_kv_heads, page_size, head_dim] of the params' dtype")
+    _same_device(append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv_data, q_in, q_out,
+                 error)
+    _check(load().pkv_append_paged_kv_axes(
+        ctypes.byref(params), ctypes.byref(rope) if rope is not None else None, batch, nnz, int(kv_data.shape[0]),
+        _ptr(append_indptr), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(positions), _ptr(k_new),
+        _ptr(v_new), _ptr(kv_data), _ptr(q_in), _ptr(q_out), _ptr(error), _stream(stream)), "pkv_append_paged_kv_axes")
+
+
+def append_paged_kv8(params: Params, rope: Optional[RopeAxes], append_indptr, kv_indptr, kv_indices, kv_last_page_len,
+                     positions, k_new, v_new, kv8, kv8_scales, q_in=None, q_out=None, error=None, stream=None) -> None:
+    """``append_paged_kv_axes`` into the 8-bit cache: e4m3 codes ``kv8`` (float8_e4m3fn or uint8) and the
+    exponent bytes ``kv8_scales`` (uint8) of their rows' power-of-two scales."""
+    if q_in is not None and q_out is None:
+        q_out = q_in
+    batch, nnz = _append_tensors(params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
+                                 v_new, q_in, q_out, error)
+    _kv8_tensors(params, kv8, kv8_scales)
+    _same_device(append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv8, kv8_scales, q_in,
+                 q_out, error)
+    _check(load().pkv_append_paged_kv8(
+        ctypes.byref(params), ctypes.byref(rope) if rope is not None else None, batch, nnz, int(kv8.shape[0]),
+        _ptr(append_indptr), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(positions), _ptr(k_new),
+        _ptr(v_new), _ptr(kv8), _ptr(kv8_scales), _ptr(q_in), _ptr(q_out), _ptr(error), _stream(stream)),
+        "pkv_append_paged_kv8")
+
+
+def batch_decode_paged_kv8(h, q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws,
+                           stream=None) -> None:
+    """Decode over the 8-bit cache, on a plan of kind PLAN_DECODE_KV8."""
+    _check(load().pkv_batch_decode_paged_kv8(h, _ptr(q), _ptr(kv8), _ptr(kv8_scales), _ptr(kv_indices),
+                                             _ptr(kv_indptr), _ptr(kv_last_page_len), _ptr(o), _ptr(lse),
+                                             _ptr(dev_ws), _stream(stream)), "pkv_batch_decode_paged_kv8")
+
+
+def batch_prefill_paged_kv8(h, q, qo_indptr, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws,
+                            stream=None) -> None:
+    """Prefill over the 8-bit cache, on a plan of kind PLAN_PREFILL_KV8."""
+    _check(load().pkv_batch_prefill_paged_kv8(h, _ptr(q), _ptr(qo_indptr), _ptr(kv8), _ptr(kv8_scales),
+                                              _ptr(kv_indices), _ptr(kv_indptr), _ptr(kv_last_page_len), _ptr(o),
+                                              _ptr(lse), _ptr(dev_ws), _stream(stream)),
+           "pkv_batch_prefill_paged_kv8")
+
+
 def plan_set_timing_events(h, start=None, stop=None) -> None:
     """Record torch.cuda.Event ``start``/``stop`` around the main kernel of later run calls."""
     def handle(ev):
@@ -323,7 +445,8 @@ def get_device_error(h, dev_ws, clear: bool = False, stream=None) -> int:
 class Plan:
     """A plan handle plus the caller-side buffers it needs.
 
-    ``kind`` is PLAN_DECODE, PLAN_PREFILL or PLAN_MIXED.  The device workspace and the
+    ``kind`` is PLAN_DECODE, PLAN_PREFILL, PLAN_MIXED, or PLAN_DECODE_KV8 / PLAN_PREFILL_KV8
+    for the 8-bit cache (``run`` then takes its scales too).  The device workspace and the
     pinned host staging buffer are allocated once here, with torch, for the
     given limits; ``plan()`` re-plans a new batch into them and ``run()``
     launches the kernels.
@@ -344,6 +467,7 @@ class Plan:
         self.dev_ws = torch.empty(dev_bytes, dtype=torch.uint8, device=f"cuda:{self.device}")
         self.host_ws = torch.empty(host_bytes, dtype=torch.uint8, pin_memory=True)
         self.num_pages = 0
+        self.batch = self.total_q = self.kv_pages = 0
         if pipelined:
             _check(load().pkv_plan_set_pipelined(self.handle, 1), "pkv_plan_set_pipelined")
         if not split_kv:
@@ -364,10 +488,44 @@ class Plan:
         plan_run(self.handle, batch, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h, num_pages,
                  self.dev_ws, self.host_ws, stream)
         self.num_pages = int(num_pages)
+        self.batch = batch
+        self.total_q = batch if qo_indptr_h is None else int(torch.as_tensor(qo_indptr_h)[-1])
+        self.kv_pages = int(torch.as_tensor(kv_indptr_h)[-1])
+
+    def _check_kv8(self, q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, qo_indptr) -> None:
+        """The tensors of a run over the 8-bit cache against what the last plan() named."""
+        p = self.params
+        _kv8_tensors(p, kv8, kv8_scales)
+        _int32(kv_indices=kv_indices, kv_indptr=kv_indptr, kv_last_page_len=kv_last_page_len, qo_indptr=qo_indptr)
+        if kv8.shape[0] < self.num_pages or kv_indices.numel() < self.kv_pages:
+            raise ValueError("the pool or the page table is smaller than the plan's")
+        if kv_indptr.numel() != self.batch + 1 or kv_last_page_len.numel() != self.batch:
+            raise ValueError("kv_indptr must have batch + 1 entries, kv_last_page_len batch")
+        if self.kind == PLAN_PREFILL_KV8 and (qo_indptr is None or qo_indptr.numel() != self.batch + 1):
+            raise ValueError("a prefill takes qo_indptr with batch + 1 entries")
+        shape = (self.total_q, p.num_qo_heads, p.head_dim)
+        for x in (q, o):
+            if tuple(x.shape) != shape or _DTYPES.get(x.dtype) != p.dtype:
+                raise ValueError("q and o must be [rows of the plan, num_qo_heads, head_dim] of the plan's dtype")
+        if lse is not None and (tuple(lse.shape) != shape[:2] or lse.dtype != torch.float32):
+            raise ValueError("lse must be [rows of the plan, num_qo_heads] float32")
 
     def run(self, q, kv_data, kv_indices, kv_indptr, kv_last_page_len, o, lse=None, *, qo_indptr=None,
-            mask=None, stream=None) -> None:
-        if mask is not None:
+            mask=None, kv_scales=None, stream=None) -> None:
+        if (kv_scales is not None) != (self.kind in (PLAN_DECODE_KV8, PLAN_PREFILL_KV8)):
+            raise ValueError("kv_scales go with a plan for the 8-bit cache")
+        if kv_scales is not None:
+            if mask is not None:
+                raise ValueError("a custom mask needs a prefill plan over the 16-bit cache")
+            self._check_kv8(q, kv_data, kv_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, qo_indptr)
+            _same_device(q, kv_data, kv_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, qo_indptr)
+            if self.kind == PLAN_DECODE_KV8:
+                batch_decode_paged_kv8(self.handle, q, kv_data, kv_scales, kv_indices, kv_indptr, kv_last_page_len, o,
+                                       lse, self.dev_ws, stream)
+            else:
+                batch_prefill_paged_kv8(self.handle, q, qo_indptr, kv_data, kv_scales, kv_indices, kv_indptr,
+                                        kv_last_page_len, o, lse, self.dev_ws, stream)
+        elif mask is not None:
             if self.kind != PLAN_PREFILL:
                 raise ValueError("a custom mask needs a prefill plan")
             batch_prefill_paged_masked(self.handle, q, qo_indptr, kv_data, kv_indices, kv_indptr, kv_last_page_len,

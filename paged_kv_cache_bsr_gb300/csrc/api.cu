@@ -129,6 +129,28 @@ pkv::PrefillArgs prefill_args(const pkv_plan* plan, void* dev_ws, const void* q,
   return a;
 }
 
+// A packed plan: point the prefill kernel at the packed copy, in 16-row pages whose ids
+// are the plan's own table, and return the arguments of the kernel that makes it.
+pkv::PackArgs read_packed_copy(const pkv_plan* plan, pkv::PrefillArgs& a, void* dev_ws, const void* kv,
+                               const int32_t* kv_indices_d) {
+  auto* base = static_cast<uint8_t*>(dev_ws);
+  auto* tb = base + table_off(plan);
+  pkv::PackArgs pk{};
+  pk.kv = kv;
+  pk.kv_indices = kv_indices_d;
+  pk.src = reinterpret_cast<const pkv::PackedSrc*>(tb + plan->L.pk_src);
+  pk.hdr = a.hdr;
+  pk.packed = base + plan->L.pk_kv;
+  pk.err = a.err;
+  pk.num_kv_heads = plan->p.num_kv_heads;
+  pk.page_size = plan->p.page_size;
+  pk.num_pages = plan->num_pages;
+  a.kv = pk.packed;
+  a.kv_indices = reinterpret_cast<const int32_t*>(tb + plan->L.pk_ids);
+  a.page_size = 16;
+  return pk;
+}
+
 pkv_status launch_status(cudaError_t e) {
   if (e == cudaSuccess) return PKV_OK;
   cudaGetLastError();
@@ -138,13 +160,16 @@ pkv_status launch_status(cudaError_t e) {
 // The prefill kernel and its merge over a plan's prefill tables (a prefill plan,
 // or a decode plan whose work runs on the tensor cores); a packed plan's copy of
 // small pages (`pack`) is made first, inside the timed span.
+// With `scales` the copy expands the 8-bit cache's codes.
 cudaError_t launch_prefill_tables(const pkv_plan* plan, const pkv::PrefillArgs& a, cudaStream_t s,
-                                  const pkv::PackArgs* pack = nullptr) {
+                                  const pkv::PackArgs* pack = nullptr, const uint8_t* scales = nullptr) {
   const pkv_params& p = plan->p;
   const bool cap = p.logits_cap > 0.f;
   cudaError_t e = wait_tables(plan, s);
   if (plan->time_start && e == cudaSuccess) cudaEventRecord(plan->time_start, s);
-  if (pack && e == cudaSuccess) e = pkv::launch_pack_pages(*pack, p.head_dim, plan->num_sms * 8, s);
+  if (pack && e == cudaSuccess)
+    e = scales ? pkv::launch_expand_pages(*pack, scales, p.head_dim, p.dtype, plan->num_sms * 8, s)
+               : pkv::launch_pack_pages(*pack, p.head_dim, plan->num_sms * 8, s);
   if (e == cudaSuccess)
     e = pkv::launch_prefill(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->total_q,
                             plan->packed ? plan->max_packed : plan->num_pages, s);
@@ -177,7 +202,7 @@ pkv_status pkv_batch_decode_paged(const pkv_plan* plan, const void* q, const voi
                                   const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                                   const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                   void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_DECODE || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_DECODE || plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
   if (!q || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_data, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
@@ -206,7 +231,7 @@ static pkv_status prefill_run(const pkv_plan* plan, const void* q, const int32_t
                               const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                               const int32_t* kv_last_page_len_d, const uint8_t* mask, size_t mask_bytes, void* o,
                               float* lse, void* dev_ws, void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_PREFILL || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_PREFILL || plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
   if (mask) {
     // whole 32-bit words covering every request's [qo_len, kv_len] block
     if (!aligned(mask, 4) || mask_bytes / 4 < static_cast<size_t>((plan->mask_bits + 31) / 32))
@@ -221,23 +246,8 @@ static pkv_status prefill_run(const pkv_plan* plan, const void* q, const int32_t
   if (st != PKV_OK) return st;
   pkv::PrefillArgs a = prefill_args(plan, dev_ws, q, kv_data, kv_indices_d, mask, mask_bytes, o, lse);
   if (!plan->packed) return launch_status(launch_prefill_tables(plan, a, static_cast<cudaStream_t>(stream)));
-  // Pages of fewer than 8 rows: the kernel reads the packed copy, in 16-row pages
-  // whose ids are the plan's own table.
-  auto* base = static_cast<uint8_t*>(dev_ws);
-  auto* tb = base + table_off(plan);
-  pkv::PackArgs pk{};
-  pk.kv = kv_data;
-  pk.kv_indices = kv_indices_d;
-  pk.src = reinterpret_cast<const pkv::PackedSrc*>(tb + plan->L.pk_src);
-  pk.hdr = a.hdr;
-  pk.packed = base + plan->L.pk_kv;
-  pk.err = a.err;
-  pk.num_kv_heads = plan->p.num_kv_heads;
-  pk.page_size = plan->p.page_size;
-  pk.num_pages = plan->num_pages;
-  a.kv = pk.packed;
-  a.kv_indices = reinterpret_cast<const int32_t*>(tb + plan->L.pk_ids);
-  a.page_size = 16;
+  // Pages of fewer than 8 rows: the kernel reads the packed copy.
+  const pkv::PackArgs pk = read_packed_copy(plan, a, dev_ws, kv_data, kv_indices_d);
   return launch_status(launch_prefill_tables(plan, a, static_cast<cudaStream_t>(stream), &pk));
 }
 
@@ -257,6 +267,49 @@ pkv_status pkv_batch_prefill_paged_masked(const pkv_plan* plan, const void* q, c
   if (!packed_mask_d) return PKV_ERR_INVALID_ARG;
   return prefill_run(plan, q, qo_indptr_d, kv_data, kv_indices_d, kv_indptr_d, kv_last_page_len_d, packed_mask_d,
                      mask_bytes, o, lse, dev_ws, stream);
+}
+
+pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const void* kv8, const uint8_t* kv8_scales,
+                                      const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
+                                      const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
+                                      void* stream) {
+  if (!plan || plan->kind != PKV_PLAN_DECODE || !plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!q || !kv8 || !kv8_scales || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+    return PKV_ERR_INVALID_ARG;
+  // The exponent bytes are copied in fours.
+  if (!aligned(q, 16) || !aligned(kv8, 16) || !aligned(kv8_scales, 4) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
+      !aligned(kv_indices_d, 4) || !aligned(kv_indptr_d, 4) || (lse && !aligned(lse, 4)))
+    return PKV_ERR_INVALID_ARG;
+  pkv_status st = check_device(plan);
+  if (st != PKV_OK) return st;
+  auto s = static_cast<cudaStream_t>(stream);
+  const pkv_params& p = plan->p;
+  const pkv::DecodeArgs a = decode_args(plan, dev_ws, q, kv8, kv_indices_d, kv_indptr_d, o, lse);
+  cudaError_t e = wait_tables(plan, s);
+  if (plan->time_start && e == cudaSuccess) cudaEventRecord(plan->time_start, s);
+  if (e == cudaSuccess)
+    e = pkv::launch_decode8(a, kv8_scales, p.sm_scale, p.head_dim, p.dtype, p.logits_cap > 0.f, plan->grid_ctas, s);
+  if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
+  if (e == cudaSuccess) e = pkv::launch_decode_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
+  if (e == cudaSuccess) e = release_tables(plan, s);
+  return launch_status(e);
+}
+
+pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, const int32_t* qo_indptr_d,
+                                       const void* kv8, const uint8_t* kv8_scales, const int32_t* kv_indices_d,
+                                       const int32_t* kv_indptr_d, const int32_t* kv_last_page_len_d, void* o,
+                                       float* lse, void* dev_ws, void* stream) {
+  if (!plan || plan->kind != PKV_PLAN_PREFILL || !plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!q || !qo_indptr_d || !kv8 || !kv8_scales || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(kv8, 16) || !aligned(kv8_scales, 4) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
+      !aligned(kv_indices_d, 4) || (lse && !aligned(lse, 4)))
+    return PKV_ERR_INVALID_ARG;
+  pkv_status st = check_device(plan);
+  if (st != PKV_OK) return st;
+  pkv::PrefillArgs a = prefill_args(plan, dev_ws, q, kv8, kv_indices_d, nullptr, 0, o, lse);
+  const pkv::PackArgs pk = read_packed_copy(plan, a, dev_ws, kv8, kv_indices_d);
+  return launch_status(launch_prefill_tables(plan, a, static_cast<cudaStream_t>(stream), &pk, kv8_scales));
 }
 
 pkv_status pkv_batch_mixed_paged(const pkv_plan* plan, const void* q, const int32_t* qo_indptr_d,

@@ -99,7 +99,7 @@ extern "C" pkv_status pkv_batch_decode_paged_noalloc(const pkv_plan* plan, const
                                                      const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                                                      const int32_t* kv_last_page_len_d, void* o, float* lse,
                                                      void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_DECODE || !plan->planned || plan->device < 0 || plan->pipelined)
+  if (!plan || plan->kind != PKV_PLAN_DECODE || plan->kv8 || !plan->planned || plan->device < 0 || plan->pipelined)
     return PKV_ERR_INVALID_ARG;
   // Tensor-core decode plans keep prefill tables and 128-row partial states, far
   // more than the static array holds.

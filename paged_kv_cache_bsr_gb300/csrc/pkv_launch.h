@@ -91,6 +91,10 @@ cudaError_t launch_decode(const DecodeArgs& a, int head_dim, int group, int dtyp
 // Fill a.kv_rows / a.kv_rows_n for the gather instances: kv_data as rows of
 // head_dim elements, one-row boxes.
 cudaError_t set_kv_rows_map(DecodeArgs& a, int head_dim, int dtype, int64_t num_pages);
+// The same over the 8-bit cache (d.kv: e4m3 codes, scales: their exponent bytes; any
+// built group, no tensor map); its merge is launch_decode_merge over d.
+cudaError_t launch_decode8(const DecodeArgs& d, const uint8_t* scales, float sm_scale, int head_dim, int dtype, bool cap,
+                           int grid, cudaStream_t stream);
 // Launch the n-way merge of split decode sequences (fixed grid).
 cudaError_t launch_decode_merge(const DecodeArgs& a, int head_dim, int group, int dtype, int grid,
                                 cudaStream_t stream);
@@ -150,10 +154,14 @@ struct PackArgs {
   void* packed;                // [max_packed, 2, Hkv, 16, D]
   int32_t* err;
   int num_kv_heads;
-  int page_size;               // 1, 2 or 4
+  int page_size;               // 1, 2 or 4 (8-bit cache: any)
   int64_t num_pages;
 };
 cudaError_t launch_pack_pages(const PackArgs& a, int head_dim, int grid, cudaStream_t stream);
+// The packed copy of an 8-bit cache's pages: kv holds e4m3 codes, scales their exponent
+// bytes, any page size; the copy holds the values in dtype.
+cudaError_t launch_expand_pages(const PackArgs& a, const uint8_t* scales, int head_dim, int dtype, int grid,
+                                cudaStream_t stream);
 cudaError_t launch_prefill_merge(const PrefillArgs& a, int head_dim, int group, int dtype, int grid,
                                  cudaStream_t stream);
 

@@ -43,6 +43,9 @@ struct pkv_plan {
   int device = -1;          // -1: host-only plan (pkv_plan_create_host)
   int num_sms = 0;
   int group = 1;
+  // A plan of kind PKV_PLAN_DECODE_KV8 or PKV_PLAN_PREFILL_KV8: `kind` holds the decode or
+  // prefill kind whose tables it makes, and only the 8-bit cache's run calls take it.
+  bool kv8 = false;
   // Fixed grid and table capacities (depend on params and limits only).
   int grid_ctas = 0;
   int workers = 0;
@@ -57,9 +60,10 @@ struct pkv_plan {
   // prefill tables, planned over row_indptr = 0, 1, ..., batch.
   bool exec_prefill = false;
   std::vector<int32_t> row_indptr;
-  // Prefill plan on pages of fewer than 8 rows: each run first copies the
-  // requests' K/V rows into 16-row pages of its workspace (pack_pages_kernel),
-  // and the tables describe the prefill over that copy.
+  // Prefill plan on pages of fewer than 8 rows, or over the 8-bit cache: each run
+  // first copies the requests' K/V rows into 16-row pages of its workspace
+  // (pack_pages_kernel, expand_pages_kernel), and the tables describe the prefill
+  // over that copy.
   bool packed = false;
   int64_t max_packed = 0;
   pkv::WorkspaceLayout L{};

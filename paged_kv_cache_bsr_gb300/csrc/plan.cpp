@@ -63,7 +63,7 @@ bool decode_on_tensor_cores(const pkv_params* p) {
          pkv::prefill_supported(p->head_dim, g, p->dtype, p->page_size);
 }
 
-pkv_status check_params(int kind, const pkv_params* p, const pkv_limits* lim) {
+pkv_status check_params(int kind, bool kv8, const pkv_params* p, const pkv_limits* lim) {
   if (!p || !lim) return PKV_ERR_INVALID_ARG;
   if (kind != PKV_PLAN_DECODE && kind != PKV_PLAN_PREFILL && kind != PKV_PLAN_MIXED) return PKV_ERR_INVALID_ARG;
   if (p->num_qo_heads <= 0 || p->num_kv_heads <= 0 || p->num_qo_heads % p->num_kv_heads)
@@ -75,7 +75,8 @@ pkv_status check_params(int kind, const pkv_params* p, const pkv_limits* lim) {
   const int g = p->num_qo_heads / p->num_kv_heads;
   if (p->dtype != PKV_F16 && p->dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
   if (kind != PKV_PLAN_PREFILL && !pkv::decode_supported(p->head_dim, g, p->dtype)) return PKV_ERR_UNSUPPORTED;
-  if (kind != PKV_PLAN_DECODE && !pkv::prefill_supported(p->head_dim, g, p->dtype, p->page_size))
+  // A prefill over the 8-bit cache reads an expanded copy in 16-row pages.
+  if (kind != PKV_PLAN_DECODE && !pkv::prefill_supported(p->head_dim, g, p->dtype, kv8 ? 16 : p->page_size))
     return PKV_ERR_UNSUPPORTED;
   if (!is_pow2_group(g)) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
@@ -112,7 +113,9 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
                      int device, int num_sms, bool route_decode = true, bool allow_pack = true) {
   if (!out) return PKV_ERR_INVALID_ARG;
   *out = nullptr;
-  pkv_status st = check_params(kind, params, limits);
+  const bool kv8 = kind == PKV_PLAN_DECODE_KV8 || kind == PKV_PLAN_PREFILL_KV8;
+  if (kv8) kind = kind == PKV_PLAN_DECODE_KV8 ? PKV_PLAN_DECODE : PKV_PLAN_PREFILL;
+  pkv_status st = check_params(kind, kv8, params, limits);
   if (st != PKV_OK) return st;
   // Worker ids (num_sms x kDecodeWarps) fit the 24-bit field of the whole-list decode plan's heap keys.
   if (num_sms <= 0 || num_sms >= (1 << 20)) return PKV_ERR_INVALID_ARG;
@@ -120,6 +123,7 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
   pkv_plan* pl = new (std::nothrow) pkv_plan();
   if (!pl) return PKV_ERR_INVALID_ARG;
   pl->kind = kind;
+  pl->kv8 = kv8;
   pl->p = *params;
   pl->lim = *limits;
   pl->device = device;
@@ -150,7 +154,7 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
     *out = pl;
     return PKV_OK;
   }
-  pl->exec_prefill = kind == PKV_PLAN_DECODE && route_decode && decode_on_tensor_cores(params);
+  pl->exec_prefill = kind == PKV_PLAN_DECODE && !kv8 && route_decode && decode_on_tensor_cores(params);
   if (kind == PKV_PLAN_DECODE && !pl->exec_prefill) {
     pl->grid_ctas = num_sms;
     pl->workers = num_sms * pkv::kDecodeWarps;
@@ -185,9 +189,9 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
     pl->max_slots = 2 * num_sms + 2;
     pl->rows_per_slot = pkv::kPrefillRows;
     pl->merge_grid = num_sms * 4;
-    // Pages of fewer than 8 rows: the tensor-core prefill runs over a packed copy
-    // in 16-row pages (a request of L keys fills ceil(L / 16) of them).
-    pl->packed = kind == PKV_PLAN_PREFILL && allow_pack && params->page_size < 8;
+    // Pages of fewer than 8 rows, or of the 8-bit cache: the tensor-core prefill runs
+    // over a packed copy in 16-row pages (a request of L keys fills ceil(L / 16) of them).
+    pl->packed = kind == PKV_PLAN_PREFILL && allow_pack && (kv8 || params->page_size < 8);
     if (pl->packed) {
       pl->max_packed = ceil_div(static_cast<int64_t>(limits->max_kv_pages) * params->page_size, 16) + limits->max_batch;
       // Packed page ids and the packed copy's row coordinates are 32-bit.
@@ -800,7 +804,7 @@ pkv_status compute_prefill(pkv_plan* pl, int batch, const int32_t* qo_indptr, co
   return PKV_OK;
 }
 
-// A prefill plan on pages of fewer than 8 rows: request b's L keys become
+// A prefill plan on pages of fewer than 8 rows, or over the 8-bit cache: request b's L keys become
 // ceil(L / 16) pages of 16 rows in the workspace's packed copy (page ids 0, 1, ...
 // in request order), each with its source run of keys; the prefill tables are then
 // planned over the packed page table as for 16-row pages.

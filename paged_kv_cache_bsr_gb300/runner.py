@@ -45,9 +45,10 @@ def make_plan(b, kind: int, pipelined: bool = False, split_kv: bool = True, **li
                     causal=b.causal, pipelined=pipelined, split_kv=split_kv, **lim)
 
 
-def plan_batch(plan: api.Plan, b, stream=None) -> None:
-    plan.plan(b.kv_indptr, b.kv_last_page_len, b.num_pages,
-              qo_indptr_h=b.qo_indptr if plan.kind != api.PLAN_DECODE else None,
+def plan_batch(plan: api.Plan, b, stream=None, num_pages: Optional[int] = None) -> None:
+    """Plan the batch over a pool of ``num_pages`` pages (default: its own kv_data's)."""
+    plan.plan(b.kv_indptr, b.kv_last_page_len, b.num_pages if num_pages is None else num_pages,
+              qo_indptr_h=b.qo_indptr if plan.kind not in (api.PLAN_DECODE, api.PLAN_DECODE_KV8) else None,
               kv_indices_h=b.kv_indices, stream=stream)
 
 
@@ -103,6 +104,89 @@ def append_kv(db: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor, rope_th
                         db.kv_data, db.q if rotate_q else None, q_out if rotate_q else None, rope_theta,
                         error=error, stream=stream)
     return q_out if rotate_q else None
+
+
+def append_kv_axes(db: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor, rope: Optional[api.RopeAxes],
+                   positions: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None, rotate_q: bool = True,
+                   error: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
+    """``append_kv`` with positions on several axes: ``rope`` from ``api.make_rope_axes`` (None: no
+    rotation), ``positions`` [num_axes, new tokens] int32 on the device (None: each token's place in its
+    request).  Returns the rotated queries (None with rotate_q False)."""
+    b = db.host
+    params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
+    if rotate_q and q_out is None:
+        q_out = torch.empty_like(db.q)
+    api.append_paged_kv_axes(params, rope, db.qo_indptr, db.kv_indptr, db.kv_indices, db.kv_last_page_len, positions,
+                             k_new, v_new, db.kv_data, db.q if rotate_q else None, q_out if rotate_q else None,
+                             error=error, stream=stream)
+    return q_out if rotate_q else None
+
+
+@dataclasses.dataclass
+class Kv8Cache:
+    """The 8-bit paged cache: e4m3 codes [num_pages, 2, Hkv, P, d] and one exponent byte per head
+    row [num_pages, 2, Hkv, P] (a code c stands for e4m3(c) * 2^(byte - 127))."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+    @staticmethod
+    def zeros(num_pages: int, num_kv_heads: int, page_size: int, head_dim: int, device: str = "cuda") -> "Kv8Cache":
+        shape = (num_pages, 2, num_kv_heads, page_size)
+        return Kv8Cache(torch.zeros(*shape, head_dim, dtype=torch.uint8, device=device).view(torch.float8_e4m3fn),
+                        torch.ones(shape, dtype=torch.uint8, device=device))
+
+    @property
+    def num_pages(self) -> int:
+        return int(self.codes.shape[0])
+
+
+def append_kv8(db: DeviceBatch, cache: Kv8Cache, k_new: torch.Tensor, v_new: torch.Tensor,
+               rope: Optional[api.RopeAxes] = None, positions: Optional[torch.Tensor] = None,
+               q_out: Optional[torch.Tensor] = None, rotate_q: bool = True, error: Optional[torch.Tensor] = None,
+               stream=None) -> Optional[torch.Tensor]:
+    """``append_kv_axes`` into the 8-bit cache (``db.kv_data`` is not used)."""
+    b = db.host
+    params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
+    if rotate_q and q_out is None:
+        q_out = torch.empty_like(db.q)
+    api.append_paged_kv8(params, rope, db.qo_indptr, db.kv_indptr, db.kv_indices, db.kv_last_page_len, positions, k_new,
+                         v_new, cache.codes, cache.scales, db.q if rotate_q else None, q_out if rotate_q else None,
+                         error=error, stream=stream)
+    return q_out if rotate_q else None
+
+
+def _run_kv8(kind: int, db: DeviceBatch, cache: Kv8Cache, plan: Optional[api.Plan], stream
+             ) -> Tuple[torch.Tensor, torch.Tensor]:
+    if plan is None:
+        plan = make_plan(db.host, kind)
+        plan_batch(plan, db.host, stream, num_pages=cache.num_pages)
+    o = torch.empty_like(db.q)
+    lse = torch.empty(db.q.shape[:2], dtype=torch.float32, device=db.q.device)
+    plan.run(db.q, cache.codes, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o, lse,
+             qo_indptr=db.qo_indptr if kind == api.PLAN_PREFILL_KV8 else None, kv_scales=cache.scales, stream=stream)
+    return o, lse
+
+
+def decode_kv8(db: DeviceBatch, cache: Kv8Cache, plan: Optional[api.Plan] = None, stream=None
+               ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``decode`` over the 8-bit cache (a plan of kind PLAN_DECODE_KV8)."""
+    return _run_kv8(api.PLAN_DECODE_KV8, db, cache, plan, stream)
+
+
+def prefill_kv8(db: DeviceBatch, cache: Kv8Cache, plan: Optional[api.Plan] = None, stream=None
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``prefill`` over the 8-bit cache (a plan of kind PLAN_PREFILL_KV8)."""
+    return _run_kv8(api.PLAN_PREFILL_KV8, db, cache, plan, stream)
+
+
+def cascade_kv8(prefix: DeviceBatch, suffix: DeviceBatch, cache: Kv8Cache, prefix_plan: Optional[api.Plan] = None,
+                suffix_plan: Optional[api.Plan] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``cascade`` over the 8-bit cache: the shared prefix once for all rows, then the suffixes, merged."""
+    o_p, l_p = prefill_kv8(prefix, cache, prefix_plan, stream)
+    o_s, l_s = decode_kv8(suffix, cache, suffix_plan, stream)
+    api.merge_state(o_p, l_p, o_s, l_s, o_p, l_p, stream=stream)
+    return o_p, l_p
 
 
 def mixed(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
