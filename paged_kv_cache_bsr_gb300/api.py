@@ -26,6 +26,7 @@ PLAN_DECODE, PLAN_PREFILL, PLAN_MIXED = 0, 1, 2
 PLAN_DECODE_KV8, PLAN_PREFILL_KV8 = 3, 4  # over the 8-bit cache
 
 _DTYPES = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
+_STORED = {PKV_F16: torch.float16, PKV_BF16: torch.bfloat16}
 
 
 class PkvError(RuntimeError):
@@ -323,48 +324,55 @@ def make_rope_axes(theta: float, rotary_dim: int, sections, interleaved: bool = 
     return RopeAxes(float(theta), int(rotary_dim), len(s), (ctypes.c_int * 4)(*s), int(bool(interleaved)))
 
 
-def _same_device(*tensors) -> None:
-    """Every tensor on the current CUDA device (the kernels are launched there)."""
-    if any(x is not None and not x.is_cuda for x in tensors):
-        raise ValueError("tensors must be on a CUDA device")
-    dev = torch.cuda.current_device()
-    if any(x is not None and x.device.index != dev for x in tensors):
-        raise ValueError(f"tensors must be on the current device cuda:{dev}")
+def _ptrs(tensors):
+    """The tensors' addresses (None for None): contiguous, and on the current CUDA device, where the
+    kernels are launched."""
+    dev, out = -2, []
+    for x in tensors:
+        if x is None:
+            out.append(None)
+            continue
+        at = x.get_device()
+        if at != dev:
+            if dev != -2 or at < 0 or at != torch.cuda.current_device():
+                raise ValueError("tensors must be on the current CUDA device")
+            dev = at
+        if not x.is_contiguous():
+            raise ValueError("tensors passed to libpkvbsr must be contiguous")
+        out.append(x.data_ptr())
+    return out
 
 
-def _int32(**tensors) -> None:
-    for name, x in tensors.items():
-        if x is not None and x.dtype != torch.int32:
-            raise ValueError(f"{name} must be int32")
+def _int32(*tensors) -> None:
+    for x in tensors:
+        if x is not None and x.dtype is not torch.int32:
+            raise ValueError("page tables, row pointers, positions and error words must be int32")
 
 
 def _kv8_tensors(params: Params, kv8, kv8_scales) -> None:
-    if kv8.element_size() != 1 or kv8_scales.dtype != torch.uint8:
+    if kv8.element_size() != 1 or kv8_scales.dtype is not torch.uint8:
         raise ValueError("kv8 must hold one byte per element (float8_e4m3fn or uint8) and kv8_scales be uint8")
-    want = (2, params.num_kv_heads, params.page_size, params.head_dim)
-    if tuple(kv8.shape[1:]) != want or tuple(kv8_scales.shape) != tuple(kv8.shape[:-1]):
+    shape = kv8.shape
+    if shape[1:] != (2, params.num_kv_heads, params.page_size, params.head_dim) or kv8_scales.shape != shape[:-1]:
         raise ValueError("kv8 must be [num_pages, 2, num_kv_heads, page_size, head_dim] and kv8_scales the same "
                          "without head_dim")
 
 
 def _append_tensors(params: Params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
                     v_new, q_in, q_out, error):
-    batch, nnz = int(append_indptr.numel()) - 1, int(k_new.shape[0])
-    _int32(append_indptr=append_indptr, kv_indptr=kv_indptr, kv_indices=kv_indices, kv_last_page_len=kv_last_page_len,
-           positions=positions, error=error)
+    batch, nnz = append_indptr.numel() - 1, k_new.shape[0]
+    _int32(append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, error)
     if batch < 0 or kv_indptr.numel() != batch + 1 or kv_last_page_len.numel() != batch:
         raise ValueError("append_indptr and kv_indptr must have batch + 1 entries, kv_last_page_len batch")
-    dtype = next((t for t, c in _DTYPES.items() if c == params.dtype), None)
-    rows = [(k_new, params.num_kv_heads), (v_new, params.num_kv_heads), (q_in, params.num_qo_heads),
-            (q_out, params.num_qo_heads)]
-    for x, heads in rows:
-        if x is not None and (tuple(x.shape) != (nnz, heads, params.head_dim) or x.dtype != dtype):
-            raise ValueError("k_new, v_new, q_in and q_out must be [nnz, heads, head_dim] of the params' dtype")
-    if positions is not None:
-        if rope is None:
-            raise ValueError("positions without a rotation")
-        if tuple(positions.shape) != (rope.num_axes, nnz):
-            raise ValueError("positions must be [num_axes, nnz]")
+    dtype, kv_rows = _STORED.get(params.dtype), (nnz, params.num_kv_heads, params.head_dim)
+    fits = k_new.shape == kv_rows and v_new.shape == kv_rows and k_new.dtype is dtype and v_new.dtype is dtype
+    if q_in is not None:
+        q_rows = (nnz, params.num_qo_heads, params.head_dim)
+        fits = fits and q_in.shape == q_rows and q_out.shape == q_rows and q_in.dtype is dtype and q_out.dtype is dtype
+    if not fits:
+        raise ValueError("k_new, v_new, q_in and q_out must be [nnz, heads, head_dim] of the params' dtype")
+    if positions is not None and (rope is None or positions.shape != (rope.num_axes, nnz)):
+        raise ValueError("positions go with a rotation and must be [num_axes, nnz]")
     return batch, nnz
 
 
@@ -377,15 +385,13 @@ def append_paged_kv_axes(params: Params, rope: Optional[RopeAxes], append_indptr
         q_out = q_in
     batch, nnz = _append_tensors(params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
                                  v_new, q_in, q_out, error)
-    if tuple(kv_data.shape[1:]) != (2, params.num_kv_heads, params.page_size, params.head_dim) or \
-            kv_data.dtype != k_new.dtype:
+    if kv_data.shape[1:] != (2, params.num_kv_heads, params.page_size, params.head_dim) or \
+            kv_data.dtype is not k_new.dtype:
         raise ValueError("kv_data must be [num_pages, 2, num_kv_heads, page_size, head_dim] of the params' dtype")
-    _same_device(append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv_data, q_in, q_out,
-                 error)
     _check(load().pkv_append_paged_kv_axes(
-        ctypes.byref(params), ctypes.byref(rope) if rope is not None else None, batch, nnz, int(kv_data.shape[0]),
-        _ptr(append_indptr), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(positions), _ptr(k_new),
-        _ptr(v_new), _ptr(kv_data), _ptr(q_in), _ptr(q_out), _ptr(error), _stream(stream)), "pkv_append_paged_kv_axes")
+        ctypes.byref(params), None if rope is None else ctypes.byref(rope), batch, nnz, kv_data.shape[0],
+        *_ptrs((append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv_data, q_in, q_out,
+                error)), _stream(stream)), "pkv_append_paged_kv_axes")
 
 
 def append_paged_kv8(params: Params, rope: Optional[RopeAxes], append_indptr, kv_indptr, kv_indices, kv_last_page_len,
@@ -397,30 +403,26 @@ def append_paged_kv8(params: Params, rope: Optional[RopeAxes], append_indptr, kv
     batch, nnz = _append_tensors(params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
                                  v_new, q_in, q_out, error)
     _kv8_tensors(params, kv8, kv8_scales)
-    _same_device(append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv8, kv8_scales, q_in,
-                 q_out, error)
     _check(load().pkv_append_paged_kv8(
-        ctypes.byref(params), ctypes.byref(rope) if rope is not None else None, batch, nnz, int(kv8.shape[0]),
-        _ptr(append_indptr), _ptr(kv_indptr), _ptr(kv_indices), _ptr(kv_last_page_len), _ptr(positions), _ptr(k_new),
-        _ptr(v_new), _ptr(kv8), _ptr(kv8_scales), _ptr(q_in), _ptr(q_out), _ptr(error), _stream(stream)),
-        "pkv_append_paged_kv8")
+        ctypes.byref(params), None if rope is None else ctypes.byref(rope), batch, nnz, kv8.shape[0],
+        *_ptrs((append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv8, kv8_scales, q_in,
+                q_out, error)), _stream(stream)), "pkv_append_paged_kv8")
 
 
 def batch_decode_paged_kv8(h, q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws,
                            stream=None) -> None:
     """Decode over the 8-bit cache, on a plan of kind PLAN_DECODE_KV8."""
-    _check(load().pkv_batch_decode_paged_kv8(h, _ptr(q), _ptr(kv8), _ptr(kv8_scales), _ptr(kv_indices),
-                                             _ptr(kv_indptr), _ptr(kv_last_page_len), _ptr(o), _ptr(lse),
-                                             _ptr(dev_ws), _stream(stream)), "pkv_batch_decode_paged_kv8")
+    _check(load().pkv_batch_decode_paged_kv8(
+        h, *_ptrs((q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws)), _stream(stream)),
+        "pkv_batch_decode_paged_kv8")
 
 
 def batch_prefill_paged_kv8(h, q, qo_indptr, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws,
                             stream=None) -> None:
     """Prefill over the 8-bit cache, on a plan of kind PLAN_PREFILL_KV8."""
-    _check(load().pkv_batch_prefill_paged_kv8(h, _ptr(q), _ptr(qo_indptr), _ptr(kv8), _ptr(kv8_scales),
-                                              _ptr(kv_indices), _ptr(kv_indptr), _ptr(kv_last_page_len), _ptr(o),
-                                              _ptr(lse), _ptr(dev_ws), _stream(stream)),
-           "pkv_batch_prefill_paged_kv8")
+    _check(load().pkv_batch_prefill_paged_kv8(
+        h, *_ptrs((q, qo_indptr, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws)),
+        _stream(stream)), "pkv_batch_prefill_paged_kv8")
 
 
 def plan_set_timing_events(h, start=None, stop=None) -> None:
@@ -496,18 +498,17 @@ class Plan:
         """The tensors of a run over the 8-bit cache against what the last plan() named."""
         p = self.params
         _kv8_tensors(p, kv8, kv8_scales)
-        _int32(kv_indices=kv_indices, kv_indptr=kv_indptr, kv_last_page_len=kv_last_page_len, qo_indptr=qo_indptr)
+        _int32(kv_indices, kv_indptr, kv_last_page_len, qo_indptr)
         if kv8.shape[0] < self.num_pages or kv_indices.numel() < self.kv_pages:
             raise ValueError("the pool or the page table is smaller than the plan's")
         if kv_indptr.numel() != self.batch + 1 or kv_last_page_len.numel() != self.batch:
             raise ValueError("kv_indptr must have batch + 1 entries, kv_last_page_len batch")
         if self.kind == PLAN_PREFILL_KV8 and (qo_indptr is None or qo_indptr.numel() != self.batch + 1):
             raise ValueError("a prefill takes qo_indptr with batch + 1 entries")
-        shape = (self.total_q, p.num_qo_heads, p.head_dim)
-        for x in (q, o):
-            if tuple(x.shape) != shape or _DTYPES.get(x.dtype) != p.dtype:
-                raise ValueError("q and o must be [rows of the plan, num_qo_heads, head_dim] of the plan's dtype")
-        if lse is not None and (tuple(lse.shape) != shape[:2] or lse.dtype != torch.float32):
+        shape, dtype = (self.total_q, p.num_qo_heads, p.head_dim), _STORED[p.dtype]
+        if q.shape != shape or o.shape != shape or q.dtype is not dtype or o.dtype is not dtype:
+            raise ValueError("q and o must be [rows of the plan, num_qo_heads, head_dim] of the plan's dtype")
+        if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32):
             raise ValueError("lse must be [rows of the plan, num_qo_heads] float32")
 
     def run(self, q, kv_data, kv_indices, kv_indptr, kv_last_page_len, o, lse=None, *, qo_indptr=None,
@@ -518,7 +519,6 @@ class Plan:
             if mask is not None:
                 raise ValueError("a custom mask needs a prefill plan over the 16-bit cache")
             self._check_kv8(q, kv_data, kv_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, qo_indptr)
-            _same_device(q, kv_data, kv_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, qo_indptr)
             if self.kind == PLAN_DECODE_KV8:
                 batch_decode_paged_kv8(self.handle, q, kv_data, kv_scales, kv_indices, kv_indptr, kv_last_page_len, o,
                                        lse, self.dev_ws, stream)

@@ -12,7 +12,7 @@
 // positions come from the page table.
 //
 // Angles.  theta^(-2i/R) / (2 pi) is held as a 64-bit binary fraction F of a turn,
-// so pos * F modulo 2^64 is the angle modulo a turn, exactly, for every int32
+// so pos * F modulo 2^64 is the angle modulo a turn, with no rounding for any int32
 // position: two integer multiplications, no argument reduction in floating
 // point.  The top 32 bits (1.5e-9 rad) are split into a quadrant and a rest of at
 // most an eighth of a turn, whose sine and cosine come from their Taylor series
@@ -292,16 +292,15 @@ bool set_rotation(AxesArgs& a, const pkv_rope_axes* rope, int head_dim) {
   if (sum != pairs) return false;
   a.rot_chunks = rope->rotary_dim / 16;
   a.num_axes = rope->num_axes;
+  const double l2 = std::log2(rope->theta);
   for (int i = 0, x = 0; i < pairs; ++i) {
     while (left[x] == 0) x = (x + 1) % rope->num_axes;  // an axis without pairs left is passed over
     a.axis[i] = static_cast<uint8_t>(x);
     --left[x];
     if (rope->interleaved) x = (x + 1) % rope->num_axes;
-    const long double f = std::exp2(-(2.0L * i / rope->rotary_dim) * std::log2(static_cast<long double>(rope->theta)));
-    const long double turn = f / 6.283185307179586476925286766559005768L;
-    const long double frac = turn - std::floor(turn);  // theta < 1 turns faster than its position
-    const long double scaled = std::ldexp(frac, 64);
-    a.freq[i] = scaled >= 18446744073709551615.0L ? ~uint64_t{0} : static_cast<uint64_t>(scaled + 0.5L);
+    // Good to about 2^-50 of a turn a step, and the angle of position p to |p| times that.
+    const double turn = std::exp2(-(2.0 * i / rope->rotary_dim) * l2) / 6.283185307179586476925286766559;
+    a.freq[i] = static_cast<uint64_t>(std::ldexp(turn - std::floor(turn), 64));  // theta < 1: over a turn a step
   }
   return true;
 }

@@ -49,11 +49,17 @@ using decode_impl::SegInfo;
 
 constexpr int kRows = kDecodeTileRows;  // tokens of a tile
 
-template <int D>
+// How a tile lies in its pages: kOne, pages of a multiple of 16 rows, so that it lies in
+// one; kFours, pages of 4, 8 or 12 rows; kAny, the other sizes below 16.
+enum PageMode { kOne, kFours, kAny };
+
+template <int D, PageMode MODE>
 struct Shape8 {
   static constexpr int kTile = kRows * D;               // bytes of K (or V) of one tile
-  static constexpr int kStages = D == 128 ? 6 : 12;     // 24 KB of rows in flight per warp
-  static constexpr int kScales = 2 * kRows;             // exponent bytes of one tile
+  // Exponent bytes of one tile: 16 of K and 16 of V, or (kAny) the aligned word
+  // around each, with the byte's place in it behind the words.
+  static constexpr int kScales = MODE == kAny ? 32 * 5 : 32;
+  static constexpr int kStages = D == 128 ? (MODE == kAny ? 6 : 7) : (MODE == kAny ? 12 : 13);  // 24 - 28 KB of rows
   static constexpr int kWarpBytes = kStages * (2 * kTile + kScales);
 };
 
@@ -89,6 +95,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t a) {
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 r;
   asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
 __device__ __forceinline__ uint32_t lds8(uint32_t a) {
@@ -132,10 +143,14 @@ struct Feed {
   int tok, n_tok;
   int idx_begin, n_pages, kvh;
   int page, row;
-  int win_base, win;   // 32 page ids from entry win_base of the segment, one per lane
-  int issued;
-  int scale, scale_stage;  // this lane's exponent byte of the tile issued last, and its stage
+  int win_base;        // 64 page ids from entry win_base of the segment, two per lane; the
+  int win, win_next;   // second half is loaded half a window before its first use
+  int stage;
 };
+
+__device__ __forceinline__ int feed_ids(const Feed& p, const DecodeArgs& a, int at) {
+  return at < p.n_pages ? __ldg(a.kv_indices + p.idx_begin + at) : 0;
+}
 
 __device__ __forceinline__ void feed_enter(Feed& p, const DecodeArgs& a, int lane) {
   const SegInfo s = load_seg(a.segs, p.seg, lane);
@@ -144,31 +159,21 @@ __device__ __forceinline__ void feed_enter(Feed& p, const DecodeArgs& a, int lan
   p.n_tok = seg_tokens(s.n_pages, s.last_rows, a.page_size);
   p.kvh = s.kvh;
   p.tok = p.page = p.row = p.win_base = 0;
-  p.win = lane < s.n_pages ? __ldg(a.kv_indices + p.idx_begin + lane) : 0;
+  p.win = feed_ids(p, a, lane);
+  p.win_next = feed_ids(p, a, lane + 32);
 }
 
-// How a tile lies in its pages: kOne, pages of a multiple of 16 rows, so that it lies in
-// one; kFours, pages of 4, 8 or 12 rows; kAny, the other sizes below 16.
-enum PageMode { kOne, kFours, kAny };
-
 // Issue the next tile's copies as one cp.async group (an empty one when the list has
-// ended).  Its exponent bytes are copied in fours (which may take in slots past
-// kv_last_page_len: their scores are masked).  Where a page does not hold whole fours
-// (kAny) they come as one plain load per lane (K's tokens on lanes 0-15, V's on
-// 16-31), put into shared memory at the next call, when they have arrived: the
-// compute side reads a tile's bytes two calls later at the earliest.
+// ended).  Rows past the request, and of a page id outside the pool, arrive as zeros.
+// Exponent bytes are copied in aligned fours (which may take in slots past
+// kv_last_page_len: their scores are masked).
 template <int D, PageMode MODE>
 __device__ __forceinline__ void feed_issue(Feed& p, const DecodeArgs& a, const uint8_t* scales, uint32_t rows0,
                                            uint32_t scales0, int lane, int64_t num_pages, uint32_t small_div,
                                            uint64_t policy) {
-  using S = Shape8<D>;
-  constexpr bool ONE = MODE == kOne;
+  using S = Shape8<D, MODE>;
   constexpr int CPR = D / 16;          // 16-byte chunks per row
   constexpr int RPI = 32 / CPR;        // rows per copy instruction
-  if constexpr (MODE == kAny) {
-    if (p.scale_stage >= 0) sts8(scales0 + p.scale_stage * S::kScales + lane, p.scale);
-    p.scale_stage = -1;
-  }
   while (p.seg < p.seg_end && p.tok >= p.n_tok) {
     ++p.seg;
     if (p.seg < p.seg_end) feed_enter(p, a, lane);
@@ -176,63 +181,83 @@ __device__ __forceinline__ void feed_issue(Feed& p, const DecodeArgs& a, const u
   if (p.seg < p.seg_end) {
     const int P = a.page_size;
     const int rows = min(kRows, p.n_tok - p.tok);
-    const int stage = p.issued % S::kStages;
-    const uint32_t dst = rows0 + stage * 2 * S::kTile;
+    const uint32_t dst = rows0 + p.stage * 2 * S::kTile, dst_s = scales0 + p.stage * S::kScales;
+    p.stage = p.stage + 1 == S::kStages ? 0 : p.stage + 1;
     const uint8_t* kv = static_cast<const uint8_t*>(a.kv);
     const int64_t vdist = static_cast<int64_t>(a.num_kv_heads) * P;  // rows from a K row to its V row
-    const int span = ONE ? 1 : static_cast<int>((static_cast<uint32_t>(p.row + kRows - 1) * small_div) >> 12) + 1;
-    if (p.page + span - p.win_base > 32) {
-      p.win_base = p.page;
-      p.win = p.page + lane < p.n_pages ? __ldg(a.kv_indices + p.idx_begin + p.page + lane) : 0;
+    if (p.page - p.win_base >= 32) {
+      p.win_base += 32;
+      p.win = p.win_next;
+      p.win_next = feed_ids(p, a, p.win_base + 32 + lane);
     }
-    bool bad = false;
-    // Row (counted over the pool's (page, head) blocks of K) of row r of the tile, or
-    // -1 past the tile's rows or in a page outside the pool.
-    auto place = [&](int r) -> int64_t {
-      const int x = p.row + r;
-      const int k = ONE ? 0 : static_cast<int>((static_cast<uint32_t>(x) * small_div) >> 12);  // x / P
-      const int id = __shfl_sync(kFull, p.win, (p.page + k - p.win_base) & 31);
-      if (r >= rows) return -1;
-      if (id < 0 || id >= num_pages) {
-        bad = true;
-        return -1;
-      }
-      return (static_cast<int64_t>(id) * 2 * a.num_kv_heads + p.kvh) * P + (ONE ? x : x - k * P);
-    };
+    const int w0 = p.page - p.win_base;
+    if constexpr (MODE == kOne) {
+      const int id = __shfl_sync(kFull, p.win, w0);
+      const bool bad = id < 0 || id >= num_pages;
+      const int64_t at = bad ? 0 : (static_cast<int64_t>(id) * 2 * a.num_kv_heads + p.kvh) * P + p.row;
+      const int valid = bad ? 0 : rows;
+      // The tile's rows are contiguous: chunk it * 32 + lane of K, and of V.
+      const uint8_t* ks = kv + at * D + lane * 16;
+      const uint8_t* vs = ks + vdist * D;
 #pragma unroll
-    for (int it = 0; it < kRows / RPI; ++it) {
-      const int r = it * RPI + lane / CPR, c = lane % CPR;
-      const int64_t at = place(r);
-      const uint8_t* src = kv + (at < 0 ? 0 : at * D) + c * 16;
-      const uint32_t n = at < 0 ? 0u : 16u;
-      cp_async_16_hint(dst + k_off<D>(r, c), src, n, policy);
-      cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), at < 0 ? src : src + vdist * D, n, policy);
-    }
-    if constexpr (MODE == kAny) {
-      const int64_t at = place(lane & 15);
-      p.scale = 127;
-      if (at >= 0) p.scale = __ldg(scales + at + (lane < 16 ? 0 : vdist));
-      p.scale_stage = stage;
-    } else {
-      const int64_t at = place((lane & 3) * 4);
+      for (int it = 0; it < kRows / RPI; ++it) {
+        const int r = it * RPI + lane / CPR, c = lane % CPR;
+        const uint32_t n = r < valid ? 16u : 0u;
+        cp_async_16_hint(dst + k_off<D>(r, c), ks + it * 512, n, policy);
+        cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), vs + it * 512, n, policy);
+      }
       if (lane < 8)
-        cp_async_4(scales0 + stage * S::kScales + lane * 4, scales + (at < 0 ? 0 : at + (lane < 4 ? 0 : vdist)),
-                   at < 0 ? 0u : 4u);
-    }
-    if (bad) atomicOr(a.err, kErrPageIndex);
-    ++p.issued;
-    p.tok += rows;
-    p.row += kRows;
-    if constexpr (ONE) {
+        cp_async_4(dst_s + lane * 4, scales + at + (lane & 3) * 4 + (lane < 4 ? 0 : vdist), bad ? 0u : 4u);
+      if (bad && lane == 0) atomicOr(a.err, kErrPageIndex);
+      p.row += kRows;
       if (p.row == P) {
         p.row = 0;
         ++p.page;
       }
     } else {
+      bool bad = false;
+      // Row (counted over the pool's (page, head) blocks) of K row r of the tile, or -1
+      // past the tile's rows or in a page outside the pool.
+      auto place = [&](int r) -> int64_t {
+        const int x = p.row + r;
+        const int k = static_cast<int>((static_cast<uint32_t>(x) * small_div) >> 12);  // x / P
+        const int id0 = __shfl_sync(kFull, p.win, (w0 + k) & 31), id1 = __shfl_sync(kFull, p.win_next, (w0 + k) & 31);
+        const int id = w0 + k < 32 ? id0 : id1;
+        if (r >= rows) return -1;
+        if (id < 0 || id >= num_pages) {
+          bad = true;
+          return -1;
+        }
+        return (static_cast<int64_t>(id) * 2 * a.num_kv_heads + p.kvh) * P + (x - k * P);
+      };
+#pragma unroll
+      for (int it = 0; it < kRows / RPI; ++it) {
+        const int r = it * RPI + lane / CPR, c = lane % CPR;
+        const int64_t at = place(r);
+        const uint8_t* ks = kv + (at < 0 ? 0 : at * D) + c * 16;
+        const uint32_t n = at < 0 ? 0u : 16u;
+        cp_async_16_hint(dst + k_off<D>(r, c), ks, n, policy);
+        cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), at < 0 ? ks : ks + vdist * D, n, policy);
+      }
+      if constexpr (MODE == kFours) {
+        const int64_t at = place((lane & 3) * 4);
+        if (lane < 8)
+          cp_async_4(dst_s + lane * 4, scales + (at < 0 ? 0 : at + (lane < 4 ? 0 : vdist)), at < 0 ? 0u : 4u);
+      } else {
+        // Lane i < 16: K's byte of token i, lane 16 + i: V's.
+        const int64_t at = place(lane & 15);
+        const int64_t byte = at < 0 ? 0 : at + (lane < 16 ? 0 : vdist), word = byte & ~int64_t{3};
+        const int64_t left = num_pages * 2 * vdist - word;  // bytes of the pool from this word on
+        cp_async_4(dst_s + lane * 4, scales + word, at < 0 ? 0u : static_cast<uint32_t>(left < 4 ? left : 4));
+        sts8(dst_s + 128 + lane, static_cast<uint32_t>(byte - word) * 8);
+      }
+      if (bad) atomicOr(a.err, kErrPageIndex);
+      p.row += kRows;
       const int k = static_cast<int>((static_cast<uint32_t>(p.row) * small_div) >> 12);
       p.page += k;
       p.row -= k * P;
     }
+    p.tok += rows;
   }
   cp_async_commit();
 }
@@ -244,9 +269,153 @@ struct Decode8Args {
   uint32_t small_div;      // page_size < 16: ceil(4096 / page_size)
 };
 
+// A lane's running state of one segment: heads 2t and 2t + 1 of its quad position t.
+template <int KS>
+struct Acc8 {
+  float m[2], R[2], l[2];
+  float o[KS][4];  // o[i][h], o[i][2 + h]: dims D/8 g + 2i and + 2i + 1 of head 2t + h
+};
+
+// NT consecutive tiles in shared memory (the last of `rows` valid rows, 1 .. 16).
+template <int D, bool CAP, PageMode MODE, int NT>
+__device__ __forceinline__ void tiles_step(const DecodeArgs& a, const uint32_t (&sK)[NT], const uint32_t (&sS)[NT],
+                                           int rows, int g, int t, const uint32_t (&qf)[D / 16][2], float qs0,
+                                           float qs1, Acc8<D / 16>& st) {
+  using S = Shape8<D, MODE>;
+  constexpr int KC = D / 64, KS = D / 16;
+  float y[NT][4], b[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    // Exponent bytes of K and V, tokens g and g + 8.
+    uint32_t kb[2], vb[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if constexpr (MODE == kAny) {
+        const uint32_t i = g + 8 * h;
+        kb[h] = (lds32(sS[n] + 4 * i) >> lds8(sS[n] + 128 + i)) & 255u;
+        vb[h] = (lds32(sS[n] + 64 + 4 * i) >> lds8(sS[n] + 144 + i)) & 255u;
+      } else {
+        kb[h] = lds8(sS[n] + g + 8 * h);
+        vb[h] = lds8(sS[n] + 16 + g + 8 * h);
+      }
+      b[n][h] = static_cast<float>(vb[h]) - 127.f;
+    }
+    // S = K Q^T: rows g and g + 8 of the tile, heads 2t and 2t + 1.
+    float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < KC; ++c) {
+      const uint4 x = lds128(sK[n] + k_off<D>(g, t + 4 * c)), z = lds128(sK[n] + k_off<D>(g + 8, t + 4 * c));
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t a0, a1, a2, a3;
+        e4m3x4_to_half(xw[w], a0, a2);
+        e4m3x4_to_half(zw[w], a1, a3);
+        mma16816((w & 1) ? sb : sa, a0, a1, a2, a3, qf[c * 4 + w][0], qf[c * 4 + w][1]);
+      }
+    }
+    const float k0 = exp_byte(kb[0]), k1 = exp_byte(kb[1]);
+    y[n][0] = (sa[0] + sb[0]) * (qs0 * k0);
+    y[n][1] = (sa[1] + sb[1]) * (qs1 * k0);
+    y[n][2] = (sa[2] + sb[2]) * (qs0 * k1);
+    y[n][3] = (sa[3] + sb[3]) * (qs1 * k1);
+    if constexpr (CAP) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[n][i] = a.cap * kLog2e * tanh_from_log2(y[n][i] * (2.f * kLog2e / a.cap));
+    }
+  }
+  if (rows < kRows) {
+    if (g >= rows) y[NT - 1][0] = y[NT - 1][1] = -INFINITY;
+    if (g + 8 >= rows) y[NT - 1][2] = y[NT - 1][3] = -INFINITY;
+  }
+  // d = y - m and e = d + b, against the references (-inf before the first tile,
+  // whose first token is valid: d is then +inf and raises them).
+  float d[NT][4], e[NT][4];
+  bool up = false;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      d[n][i] = y[n][i] - st.m[i & 1];
+      e[n][i] = d[n][i] + b[n][i >> 1];
+      up |= d[n][i] > 8.f || e[n][i] > st.R[i & 1] + 8.f;
+    }
+  if (__any_sync(kFull, up)) {
+    float beta[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float my = fmaxf(y[0][h], y[0][2 + h]);
+#pragma unroll
+      for (int n = 1; n < NT; ++n) my = fmaxf(my, fmaxf(y[n][h], y[n][2 + h]));
+      my = warp_max(my, 16, 4);
+      const float m_new = my - st.m[h] > 8.f ? my : st.m[h];
+      const float shift = st.m[h] - m_new;  // 0, or by how much every earlier term falls
+      if (m_new != st.m[h]) st.l[h] *= fast_exp2(shift);
+      float me = -INFINITY;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          d[n][2 * k + h] = y[n][2 * k + h] - m_new;
+          e[n][2 * k + h] = d[n][2 * k + h] + b[n][k];
+          me = fmaxf(me, e[n][2 * k + h]);
+        }
+      me = warp_max(me, 16, 4);
+      const float r_old = m_new != st.m[h] ? st.R[h] + shift : st.R[h];
+      const float r_new = me > r_old + 8.f ? me : r_old;
+      beta[h] = r_new != r_old ? fast_exp2(r_old - r_new) : 1.f;
+      st.m[h] = m_new;
+      st.R[h] = r_new;
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) st.o[i][k] *= beta[k & 1];
+  }
+  const float r7[2] = {7.f - st.R[0], 7.f - st.R[1]};
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    float p[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      st.l[i & 1] += fast_exp2(d[n][i]);
+      p[i] = fast_exp2(e[n][i] + r7[i & 1]);
+    }
+    const uint32_t pb0 = movmatrix_trans(pack2<__half>(p[0], p[1])), pb1 = movmatrix_trans(pack2<__half>(p[2], p[3]));
+    // O += V^T P: lane (g, t) pairs tokens 2t, 2t + 1 (and + 8) of dims D/8 g ...
+    const uint32_t sV = sK[n] + S::kTile;
+    constexpr int W = KS / 2;  // 32-bit words of the lane's dims per row
+    uint32_t w0[W], w1[W], w2[W], w3[W];
+    if constexpr (D == 128) {
+      const uint4 v0 = lds128(sV + v_off<D>(2 * t, g)), v1 = lds128(sV + v_off<D>(2 * t + 1, g)),
+                  v2 = lds128(sV + v_off<D>(2 * t + 8, g)), v3 = lds128(sV + v_off<D>(2 * t + 9, g));
+      w0[0] = v0.x; w0[1] = v0.y; w0[2] = v0.z; w0[3] = v0.w;
+      w1[0] = v1.x; w1[1] = v1.y; w1[2] = v1.z; w1[3] = v1.w;
+      w2[0] = v2.x; w2[1] = v2.y; w2[2] = v2.z; w2[3] = v2.w;
+      w3[0] = v3.x; w3[1] = v3.y; w3[2] = v3.z; w3[3] = v3.w;
+    } else {
+      const uint32_t h8 = (g & 1) * 8;
+      const uint2 v0 = lds64(sV + v_off<D>(2 * t, g >> 1) + h8), v1 = lds64(sV + v_off<D>(2 * t + 1, g >> 1) + h8),
+                  v2 = lds64(sV + v_off<D>(2 * t + 8, g >> 1) + h8), v3 = lds64(sV + v_off<D>(2 * t + 9, g >> 1) + h8);
+      w0[0] = v0.x; w0[1] = v0.y;
+      w1[0] = v1.x; w1[1] = v1.y;
+      w2[0] = v2.x; w2[1] = v2.y;
+      w3[0] = v3.x; w3[1] = v3.y;
+    }
+#pragma unroll
+    for (int i = 0; i < KS; ++i) {
+      const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+      uint32_t a0, a1, a2, a3;
+      e4m3x4_to_half(__byte_perm(w0[i / 2], w1[i / 2], sel), a0, a1);
+      e4m3x4_to_half(__byte_perm(w2[i / 2], w3[i / 2], sel), a2, a3);
+      mma16816(st.o[i], a0, a1, a2, a3, pb0, pb1);
+    }
+  }
+}
+
 template <int D, typename T, bool CAP, PageMode MODE>
 __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker, uint32_t rows0, uint32_t scales0) {
-  using S = Shape8<D>;
+  using S = Shape8<D, MODE>;
   constexpr int ST = S::kStages;
   constexpr int KC = D / 64;     // 16-byte chunks of a K row per lane (and of a 16-bit Q row, pairs of them)
   constexpr int KS = D / 16;     // k steps of Q K^T, and 16-dim blocks of V^T P
@@ -263,8 +432,7 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
   Feed feed;
   feed.seg = seg_begin;
   feed.seg_end = seg_end;
-  feed.issued = 0;
-  feed.scale_stage = -1;
+  feed.stage = 0;
   feed_enter(feed, a, lane);
   auto issue = [&] {
     feed_issue<D, MODE>(feed, a, a8.scales, rows0, scales0, lane, num_pages, a8.small_div, policy);
@@ -272,7 +440,7 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
 #pragma unroll 1
   for (int i = 0; i < ST - 1; ++i) issue();
 
-  int consumed = 0;
+  int stage = 0;
   for (int si = seg_begin; si < seg_end; ++si) {
     const SegInfo sg = load_seg(a.segs, si, lane);
     const int hq0 = sg.kvh * G;
@@ -317,134 +485,58 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
     }
     // From here on a lane's two heads are 2t and 2t + 1.
     const float qs0 = __shfl_sync(kFull, qs, 8 * t), qs1 = __shfl_sync(kFull, qs, 8 * t + 4);
-    float m[2] = {-INFINITY, -INFINITY}, R[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    float acc[KS][4];
+    Acc8<KS> st;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      st.m[h] = st.R[h] = -INFINITY;
+      st.l[h] = 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < KS; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][e] = 0.f;
+      for (int k = 0; k < 4; ++k) st.o[i][k] = 0.f;
 
     const int n_tok = seg_tokens(sg.n_pages, sg.last_rows, a.page_size);
-    for (int tok0 = 0; tok0 < n_tok; tok0 += kRows) {
-      const int rows = min(kRows, n_tok - tok0);
-      const int stage = consumed % ST;
+    auto next_stage = [&](uint32_t& sK, uint32_t& sS) {
+      sK = rows0 + stage * 2 * S::kTile;
+      sS = scales0 + stage * S::kScales;
+      stage = stage + 1 == ST ? 0 : stage + 1;
+    };
+    // Two tiles a step (more independent work for the warp between its waits), and
+    // one where an odd tile is left.  Of the ST - 1 groups ahead of the compute side
+    // the first two (or one) must have landed.
+    int tok = 0;
+    for (; tok + kRows < n_tok; tok += 2 * kRows) {
+      cp_async_wait<ST - 3>();
+      __syncwarp();
+      uint32_t sK[2], sS[2];
+      next_stage(sK[0], sS[0]);
+      next_stage(sK[1], sS[1]);
+      tiles_step<D, CAP, MODE, 2>(a, sK, sS, min(kRows, n_tok - tok - kRows), g, t, qf, qs0, qs1, st);
+      __syncwarp();  // every lane has read the stages before they are filled again
+      issue();
+      issue();
+    }
+    if (tok < n_tok) {
       cp_async_wait<ST - 2>();
       __syncwarp();
-      const uint32_t sK = rows0 + stage * 2 * S::kTile, sV = sK + S::kTile, sS = scales0 + stage * S::kScales;
-      const uint32_t ka0 = lds8(sS + g), ka1 = lds8(sS + g + 8), vb0 = lds8(sS + 16 + g), vb1 = lds8(sS + 24 + g);
-
-      // S = K Q^T: rows g and g + 8 of the tile, heads 2t and 2t + 1.
-      float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < KC; ++c) {
-        const uint4 x = lds128(sK + k_off<D>(g, t + 4 * c)), y = lds128(sK + k_off<D>(g + 8, t + 4 * c));
-        const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_half(xw[w], a0, a2);
-          e4m3x4_to_half(yw[w], a1, a3);
-          mma16816((w & 1) ? sb : sa, a0, a1, a2, a3, qf[c * 4 + w][0], qf[c * 4 + w][1]);
-        }
-      }
-      const float k0 = exp_byte(ka0), k1 = exp_byte(ka1);
-      float y[4] = {(sa[0] + sb[0]) * (qs0 * k0), (sa[1] + sb[1]) * (qs1 * k0), (sa[2] + sb[2]) * (qs0 * k1),
-                    (sa[3] + sb[3]) * (qs1 * k1)};
-      if constexpr (CAP) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = a.cap * kLog2e * tanh_from_log2(y[e] * (2.f * kLog2e / a.cap));
-      }
-      if (rows < kRows) {
-        if (g >= rows) y[0] = y[1] = -INFINITY;
-        if (g + 8 >= rows) y[2] = y[3] = -INFINITY;
-      }
-      const float b0 = static_cast<float>(vb0) - 127.f, b1 = static_cast<float>(vb1) - 127.f;
-      // d = y - m and e = d + b, against the references (-inf before the first tile,
-      // whose first token is valid: d is then +inf and raises them).
-      float d[4], e[4];
-      bool up = false;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        d[i] = y[i] - m[i & 1];
-        e[i] = d[i] + (i < 2 ? b0 : b1);
-        up |= d[i] > 8.f || e[i] > R[i & 1] + 8.f;
-      }
-      if (__any_sync(kFull, up)) {
-        float beta[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float my = warp_max(fmaxf(y[h], y[2 + h]), 16, 4);
-          const float m_new = my - m[h] > 8.f ? my : m[h];
-          const float shift = m[h] - m_new;  // 0, or by how much every earlier term falls
-          if (m_new != m[h]) l[h] *= fast_exp2(shift);
-          d[h] = y[h] - m_new;
-          d[2 + h] = y[2 + h] - m_new;
-          e[h] = d[h] + b0;
-          e[2 + h] = d[2 + h] + b1;
-          const float r_old = m_new != m[h] ? R[h] + shift : R[h];
-          const float me = warp_max(fmaxf(e[h], e[2 + h]), 16, 4);
-          const float r_new = me > r_old + 8.f ? me : r_old;
-          beta[h] = r_new != r_old ? fast_exp2(r_old - r_new) : 1.f;
-          m[h] = m_new;
-          R[h] = r_new;
-        }
-#pragma unroll
-        for (int i = 0; i < KS; ++i)
-#pragma unroll
-          for (int k = 0; k < 4; ++k) acc[i][k] *= beta[k & 1];
-      }
-      float p[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        l[i & 1] += fast_exp2(d[i]);
-        p[i] = fast_exp2(e[i] - R[i & 1] + 7.f);
-      }
-      const uint32_t pb0 = movmatrix_trans(pack2<__half>(p[0], p[1])), pb1 = movmatrix_trans(pack2<__half>(p[2], p[3]));
-
-      // O += V^T P: lane (g, t) pairs tokens 2t, 2t + 1 (and + 8) of dims D/8 g ...
-      if constexpr (D == 128) {
-        const uint4 v0 = lds128(sV + v_off<D>(2 * t, g)), v1 = lds128(sV + v_off<D>(2 * t + 1, g)),
-                    v2 = lds128(sV + v_off<D>(2 * t + 8, g)), v3 = lds128(sV + v_off<D>(2 * t + 9, g));
-        const uint32_t w0[4] = {v0.x, v0.y, v0.z, v0.w}, w1[4] = {v1.x, v1.y, v1.z, v1.w},
-                       w2[4] = {v2.x, v2.y, v2.z, v2.w}, w3[4] = {v3.x, v3.y, v3.z, v3.w};
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_half(__byte_perm(w0[i / 2], w1[i / 2], sel), a0, a1);
-          e4m3x4_to_half(__byte_perm(w2[i / 2], w3[i / 2], sel), a2, a3);
-          mma16816(acc[i], a0, a1, a2, a3, pb0, pb1);
-        }
-      } else {
-        const uint32_t h8 = (g & 1) * 8;
-        const uint2 v0 = lds64(sV + v_off<D>(2 * t, g >> 1) + h8), v1 = lds64(sV + v_off<D>(2 * t + 1, g >> 1) + h8),
-                    v2 = lds64(sV + v_off<D>(2 * t + 8, g >> 1) + h8), v3 = lds64(sV + v_off<D>(2 * t + 9, g >> 1) + h8);
-        const uint32_t w0[2] = {v0.x, v0.y}, w1[2] = {v1.x, v1.y}, w2[2] = {v2.x, v2.y}, w3[2] = {v3.x, v3.y};
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-          uint32_t a0, a1, a2, a3;
-          e4m3x4_to_half(__byte_perm(w0[i / 2], w1[i / 2], sel), a0, a1);
-          e4m3x4_to_half(__byte_perm(w2[i / 2], w3[i / 2], sel), a2, a3);
-          mma16816(acc[i], a0, a1, a2, a3, pb0, pb1);
-        }
-      }
-      ++consumed;
-      __syncwarp();  // every lane has read the stage before it is filled again
+      uint32_t sK[1], sS[1];
+      next_stage(sK[0], sS[0]);
+      tiles_step<D, CAP, MODE, 1>(a, sK, sS, n_tok - tok, g, t, qf, qs0, qs1, st);
+      __syncwarp();
       issue();
     }
 
-    // acc[i][h] and acc[i][2 + h] are dims D/8 g + 2i and + 2i + 1 of head 2t + h.
     const bool empty = sg.n_pages == 0;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      float lh = l[h];
+      float lh = st.l[h];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) lh += __shfl_xor_sync(kFull, lh, o);
       const int head = 2 * t + h;
       if (head >= G) continue;
-      const float f = empty ? 0.f : exp2f(R[h] - 7.f) / lh;
-      const float lse_v = empty ? -INFINITY : (m[h] + log2f(lh)) * kLn2;
+      const float f = empty ? 0.f : exp2f(st.R[h] - 7.f) / lh;
+      const float lse_v = empty ? -INFINITY : (st.m[h] + log2f(lh)) * kLn2;
       if (sg.slot < 0) {
         const int64_t orow = static_cast<int64_t>(sg.q_row) * a.num_qo_heads + hq0 + head;
         T* dst = static_cast<T*>(a.o) + orow * D + g * (D / 8);
@@ -453,8 +545,8 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
           float v[8];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            v[2 * e] = acc[i + e][h] * f;
-            v[2 * e + 1] = acc[i + e][2 + h] * f;
+            v[2 * e] = st.o[i + e][h] * f;
+            v[2 * e + 1] = st.o[i + e][2 + h] * f;
           }
           *reinterpret_cast<uint4*>(dst + 2 * i) = from_float8<T>(v);
         }
@@ -465,7 +557,7 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
 #pragma unroll
         for (int i = 0; i < KS; i += 2)
           *reinterpret_cast<float4*>(dst + 2 * i) =
-              make_float4(acc[i][h] * f, acc[i][2 + h] * f, acc[i + 1][h] * f, acc[i + 1][2 + h] * f);
+              make_float4(st.o[i][h] * f, st.o[i][2 + h] * f, st.o[i + 1][h] * f, st.o[i + 1][2 + h] * f);
         if (g == 0) a.part_lse[prow] = lse_v;
       }
     }
@@ -474,7 +566,7 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
 
 template <int D, typename T, bool CAP, PageMode MODE>
 __global__ void __launch_bounds__(kDecodeWarps * 32, 1) decode8_kernel(const __grid_constant__ Decode8Args a) {
-  using S = Shape8<D>;
+  using S = Shape8<D, MODE>;
   extern __shared__ __align__(128) uint8_t smem[];
   // Launched as a programmatic dependent of the kernel before it on the stream:
   // nothing global is touched before that grid has finished.
@@ -489,14 +581,19 @@ template <int D, typename T>
 cudaError_t launch_t(const Decode8Args& a, bool cap, int grid, cudaStream_t s) {
   const int P = a.d.page_size;
   void (*kern)(Decode8Args) = nullptr;
-  if (P % kRows == 0)
+  int smem = kDecodeWarps * Shape8<D, kOne>::kWarpBytes;
+  static_assert(kDecodeWarps * Shape8<D, kOne>::kWarpBytes <= 232448 &&
+                    Shape8<D, kFours>::kWarpBytes == Shape8<D, kOne>::kWarpBytes &&
+                    Shape8<D, kAny>::kWarpBytes <= Shape8<D, kOne>::kWarpBytes,
+                "decode ring exceeds shared memory");
+  if (P % kRows == 0) {
     kern = cap ? decode8_kernel<D, T, true, kOne> : decode8_kernel<D, T, false, kOne>;
-  else if (P % 4 == 0)
+  } else if (P % 4 == 0) {
     kern = cap ? decode8_kernel<D, T, true, kFours> : decode8_kernel<D, T, false, kFours>;
-  else
+  } else {
     kern = cap ? decode8_kernel<D, T, true, kAny> : decode8_kernel<D, T, false, kAny>;
-  constexpr int smem = kDecodeWarps * Shape8<D>::kWarpBytes;
-  static_assert(smem <= 232448, "decode ring exceeds shared memory");
+    smem = kDecodeWarps * Shape8<D, kAny>::kWarpBytes;
+  }
   cudaError_t e = ensure_smem_limit(kern, smem);
   if (e != cudaSuccess) return e;
   return launch_dependent(kern, grid, kDecodeWarps * 32, smem, s, a);
