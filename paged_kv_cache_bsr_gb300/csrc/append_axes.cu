@@ -292,14 +292,20 @@ bool set_rotation(AxesArgs& a, const pkv_rope_axes* rope, int head_dim) {
   if (sum != pairs) return false;
   a.rot_chunks = rope->rotary_dim / 16;
   a.num_axes = rope->num_axes;
-  const double l2 = std::log2(rope->theta);
+  // theta^(-2i/R) as the product of a power by i / 8 and one by i % 8.
+  const double step = -2.0 / rope->rotary_dim * std::log2(rope->theta);
+  double by8[8], by1[8];
+  for (int i = 0; i < 8; ++i) {
+    by8[i] = std::exp2(step * (8 * i)) / 6.283185307179586476925286766559;
+    by1[i] = std::exp2(step * i);
+  }
   for (int i = 0, x = 0; i < pairs; ++i) {
     while (left[x] == 0) x = (x + 1) % rope->num_axes;  // an axis without pairs left is passed over
     a.axis[i] = static_cast<uint8_t>(x);
     --left[x];
     if (rope->interleaved) x = (x + 1) % rope->num_axes;
-    // Good to about 2^-50 of a turn a step, and the angle of position p to |p| times that.
-    const double turn = std::exp2(-(2.0 * i / rope->rotary_dim) * l2) / 6.283185307179586476925286766559;
+    // Good to about 2^-50 of its value: the angle of position p to |p| times that.
+    const double turn = by8[i / 8] * by1[i % 8];
     a.freq[i] = static_cast<uint64_t>(std::ldexp(turn - std::floor(turn), 64));  // theta < 1: over a turn a step
   }
   return true;
