@@ -28,7 +28,9 @@
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "pkv_bsr.h"
 #include "pkv_device.cuh"
@@ -43,6 +45,8 @@ constexpr int kAxThreads = kAxWarps * 32;
 constexpr int kAxPairs = 64;     // D / 2 for the largest head_dim built (128)
 constexpr int kAxIndptr = 1024;  // append_indptr entries staged in shared memory
 constexpr int kMaxAxes = 4;
+constexpr int kAhead = 6;        // passes in flight per warp
+constexpr int kAxSmem = kAxWarps * kAhead * 2048;
 
 struct AxesArgs {
   const int32_t* append_indptr;  // [batch + 1] new-token rows per request
@@ -66,17 +70,26 @@ struct AxesArgs {
   int rot_chunks;                // R / 16: lanes of a head row that rotate
   int num_axes;
   int parts;                     // warps that share a token
-  int part_passes;               // passes of head rows each of them takes
+  int part_passes;               // passes each of them takes
   uint64_t freq[kAxPairs];       // theta^(-2i/R) / (2 pi) * 2^64
   uint8_t axis[kAxPairs];
 };
 
+// pos * F modulo a turn: pos = u - 2^32 for a negative one.
+__device__ __forceinline__ uint32_t turn_hi(int32_t pos, uint64_t freq) {  // bits 32 .. 63
+  const uint32_t u = static_cast<uint32_t>(pos), flo = static_cast<uint32_t>(freq);
+  return u * static_cast<uint32_t>(freq >> 32) + __umulhi(u, flo) - (pos < 0 ? flo : 0u);
+}
+
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a) : "memory");
+  return r;
+}
+
 // Sine and cosine of pos * F turns.
 __device__ __forceinline__ void sincos_turn(int32_t pos, uint64_t freq, float& s, float& c) {
-  const uint32_t u = static_cast<uint32_t>(pos), fhi = static_cast<uint32_t>(freq >> 32),
-                 flo = static_cast<uint32_t>(freq);
-  // Bits 32..63 of pos * F: pos = u - 2^32 for a negative one.
-  const uint32_t turn = u * fhi + __umulhi(u, flo) - (pos < 0 ? flo : 0u);
+  const uint32_t turn = turn_hi(pos, freq);
   const uint32_t quad = (turn + 0x20000000u) >> 30;
   const float x = static_cast<float>(static_cast<int32_t>(turn - (quad << 30))) * 1.46291807926715968e-9f;  // 2 pi / 2^32
   const float z = x * x;
@@ -94,6 +107,29 @@ __device__ __forceinline__ void sincos_turn(int32_t pos, uint64_t freq, float& s
   c = ((quad + 1u) & 2u) ? -b : b;
 }
 
+// A pair turned in double precision, each element rounded to a float by truncation
+// with the lost part in its last bit, so that rounding the float to e4m3 rounds the
+// double's value correctly.
+__device__ __noinline__ float2 turn_pair_double(float x, float y, int32_t pos, uint64_t freq) {
+  const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq);
+  double s, c;
+  sincospi(static_cast<double>(turn) * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
+  const double v[2] = {x * c - y * s, y * c + x * s};
+  float r[2];
+  for (int i = 0; i < 2; ++i) {
+    r[i] = __double2float_rz(v[i]);
+    if (static_cast<double>(r[i]) != v[i]) r[i] = __uint_as_float(__float_as_uint(r[i]) | 1u);
+  }
+  return make_float2(r[0], r[1]);
+}
+
+// Whether a float changed by 16 units of its last place could round to another e4m3:
+// the 20 bits below e4m3's mantissa are that near to half.  (Below 2^-6, the smallest
+// normal e4m3, its steps are wider than this looks at.)
+__device__ __forceinline__ bool near_border(float x) {
+  return ((__float_as_uint(x) + (16u - 0x80000u)) & 0xfffffu) <= 32u;
+}
+
 // Two floats to two e4m3 codes, the first in the low byte: round to nearest even,
 // past +-448 to +-448, NaN to NaN.
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
@@ -102,52 +138,147 @@ __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint2 pack_e4m3x8(const float (&f)[8]) {
-  return make_uint2(pack_e4m3(f[0], f[1]) | (pack_e4m3(f[2], f[3]) << 16),
-                    pack_e4m3(f[4], f[5]) | (pack_e4m3(f[6], f[7]) << 16));
+__device__ __forceinline__ uint2 pack_e4m3x8(const float2 (&f)[4]) {
+  return make_uint2(pack_e4m3(f[0].x, f[0].y) | (pack_e4m3(f[1].x, f[1].y) << 16),
+                    pack_e4m3(f[2].x, f[2].y) | (pack_e4m3(f[3].x, f[3].y) << 16));
+}
+template <typename T>
+__device__ __forceinline__ uint4 pack_16x8(const float2 (&f)[4]) {
+  return make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y), pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y));
 }
 
-// One warp takes one token's head rows (keys, then queries, then values), or a
-// part of them when there are few tokens, D/16 lanes to a row.  A rotating lane
-// holds 8 pairs as 16 bytes of each half of the rotated part, any other lane 32
-// bytes in a row, so nothing is shuffled but the 8-bit rows' largest values.
+// The exponent byte of a head row of which each of LPH neighbouring lanes holds 16
+// elements: from the largest finite magnitude's float32 exponent field.  Magnitudes of
+// a 16-bit type are ordered like their bits, so the row is searched two elements an
+// instruction; a row with an infinity or a NaN is searched again without them.
+template <typename T, int LPH>
+__device__ __forceinline__ uint32_t row_exponent(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  constexpr bool kBf = std::is_same<T, __nv_bfloat16>::value;
+  constexpr uint32_t kInf = kBf ? 0x7f80u : 0x7c00u;
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7fff7fffu);
+#pragma unroll
+  for (int o = LPH / 2; o >= 1; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, o));
+  m = max(m & 0xffffu, m >> 16);
+  if (__any_sync(0xffffffffu, m >= kInf)) {
+    m = 0;
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = w[i] & 0x7fffu, hi = (w[i] >> 16) & 0x7fffu;
+      m = max(m, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+    }
+    for (int o = LPH / 2; o >= 1; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  }
+  const uint32_t field = kBf ? m >> 7 : __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(m)))) >> 23;
+  return static_cast<uint32_t>(max(static_cast<int>(field) - 7, 1));
+}
+
+// One warp takes one token, or some of its passes when there are few tokens.  A pass
+// is 4 16-byte loads per lane: RPP keys' and values' head rows, or 2 RPP queries',
+// D/16 lanes to a row.  A rotating lane holds 8 pairs as 16 bytes of each half of the
+// rotated part, any other lane 32 bytes in a row, so nothing is shuffled but the 8-bit
+// rows' largest magnitudes.  The rows arrive through a ring in shared memory of kAhead
+// passes (cp.async; a lane reads back only what it copied itself, so its own wait is the
+// only synchronisation), which runs across tokens and ahead of the page lookups.
+//
+// A key's code depends on which side of a border between two e4m3 values its turned
+// element falls.  A float turn is off by about 2^-23 of the pair's length; elements
+// within 16 units of their float's last place of a border (one in 30000) are turned
+// again in double precision, so elements of at least an eighth of their pair's length
+// get the code of the exact rotation.  (A smaller one may get its second nearest, when
+// the two are equally near to within 2^-21 of the pair's length.)
 template <int D, typename T, bool OUT8>
-__global__ void __launch_bounds__(kAxThreads) append_axes_kernel(const __grid_constant__ AxesArgs a) {
+__global__ void __launch_bounds__(kAxThreads, 2) append_axes_kernel(const __grid_constant__ AxesArgs a) {
   constexpr int LPH = D / 16;     // lanes per head row
-  constexpr int RPP = 32 / LPH;   // head rows per pass
-  constexpr int CHUNK = 2;        // passes loaded before the first is used
+  constexpr int RPP = 32 / LPH;   // head rows per load
   __shared__ int32_t s_indptr[kAxIndptr];
+  __shared__ uint64_t s_freq[kAxPairs];
+  extern __shared__ __align__(16) uint8_t s_ring[];
   // Launched as a programmatic dependent of the kernel before it on the stream:
   // nothing global is touched before that grid has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const bool staged = a.batch < kAxIndptr;
   if (staged)
     for (int i = threadIdx.x; i <= a.batch; i += blockDim.x) s_indptr[i] = a.append_indptr[i];
+  if (threadIdx.x < kAxPairs) s_freq[threadIdx.x] = a.freq[threadIdx.x];
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int sub = lane % LPH, hsub = lane / LPH;
   const bool turns = sub < a.rot_chunks;
-  // Element offsets of this lane's two 8-element chunks in a head row.
+  // Element offsets of this lane's two 8-element chunks in a turned head row.
   const int off_a = turns ? sub * 8 : a.rot_chunks * 16 + (sub - a.rot_chunks) * 16;
   const int off_b = turns ? a.rot_chunks * 8 + sub * 8 : off_a + 8;
-  uint64_t freq[8];
   uint32_t axes = 0;  // 4 bits per pair
+  if (turns)
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    freq[j] = turns ? a.freq[sub * 8 + j] : 0;
-    axes |= (turns ? static_cast<uint32_t>(a.axis[sub * 8 + j]) : 0u) << (4 * j);
-  }
+    for (int j = 0; j < 8; ++j) axes |= static_cast<uint32_t>(a.axis[sub * 8 + j]) << (4 * j);
   const int P = a.page_size, Hkv = a.num_kv_heads, Hq = a.q_in ? a.num_qo_heads : 0;
-  const int rows = 2 * Hkv + Hq;
+  const int kv_passes = (Hkv + RPP - 1) / RPP;
+  const int all_passes = kv_passes + (Hq + 2 * RPP - 1) / (2 * RPP);
+  const int part = static_cast<int>(blockIdx.x % a.parts);
+  const int pass0 = part * a.part_passes, pass1 = min(all_passes, pass0 + a.part_passes);
   const T* k_new = static_cast<const T*>(a.k_new);
   const T* v_new = static_cast<const T*>(a.v_new);
   const T* q_in = static_cast<const T*>(a.q_in);
+  const int64_t t_begin = static_cast<int64_t>(blockIdx.x / a.parts) * kAxWarps + warp;
+  const int64_t t_step = static_cast<int64_t>(gridDim.x / a.parts) * kAxWarps;
+  // The copy side: the next pass to issue, and its place in the ring.  A lane's four
+  // chunks of a pass are 512 bytes apart, so a warp's copies and reads are contiguous.
+  const uint32_t ring = smem_addr(s_ring) + warp * kAhead * 2048 + lane * 16;
+  int64_t next_t = t_begin;
+  int next_pass = pass0, next_at = 0;
+  auto issue = [&] {
+    if (next_t < a.nnz) {
+      const uint32_t dst = ring + next_at * 2048;
+      if (next_pass < kv_passes) {
+        const int r = next_pass * RPP + hsub;
+        if (r < Hkv) {
+          const int64_t row = (next_t * Hkv + r) * D;
+          cp_async_16(dst, k_new + row + off_a, 16);
+          cp_async_16(dst + 512, k_new + row + off_b, 16);
+          cp_async_16(dst + 1024, v_new + row + sub * 16, 16);
+          cp_async_16(dst + 1536, v_new + row + sub * 16 + 8, 16);
+        }
+      } else {
+        const int r = (next_pass - kv_passes) * 2 * RPP + hsub;
+        const T* src = q_in + (next_t * Hq + r) * D;
+        if (r < Hq) {
+          cp_async_16(dst, src + off_a, 16);
+          cp_async_16(dst + 512, src + off_b, 16);
+        }
+        if (r + RPP < Hq) {
+          cp_async_16(dst + 1024, src + RPP * D + off_a, 16);
+          cp_async_16(dst + 1536, src + RPP * D + off_b, 16);
+        }
+      }
+      next_at = next_at + 1 == kAhead ? 0 : next_at + 1;
+      if (++next_pass == pass1) {
+        next_pass = pass0;
+        next_t += t_step;
+      }
+    }
+    cp_async_commit();
+  };
+  for (int i = 0; i < kAhead - 1; ++i) issue();
+  int at = 0;
+  // The oldest pass in flight, arrived; its place is free again for the pass issued next.
+  auto take = [&](uint4 (&x)[4]) {
+    cp_async_wait<kAhead - 2>();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = ld_shared_v4(ring + at * 2048 + i * 512);
+    at = at + 1 == kAhead ? 0 : at + 1;
+    issue();
+  };
   int32_t err = 0;
-  const int64_t units = a.nnz * a.parts;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kAxWarps + warp; u < units;
-       u += static_cast<int64_t>(gridDim.x) * kAxWarps) {
-    const int64_t t = u / a.parts;
-    const int part = static_cast<int>(u - t * a.parts);
+  for (int64_t t = t_begin; t < a.nnz; t += t_step) {
+    // A token that is skipped leaves its passes in the ring.
+    auto skip = [&] {
+      uint4 x[4];
+      for (int pass = pass0; pass < pass1; ++pass) take(x);
+    };
+    int32_t pos = 0;  // lane i: the token's position on axis i
+    if (a.positions && lane < a.num_axes) pos = __ldg(a.positions + lane * a.nnz + t);
     // The request holding new row t: the last b with append_indptr[b] <= t.
     int lo = 0, hi = a.batch;
     while (hi - lo > 1) {
@@ -166,96 +297,135 @@ __global__ void __launch_bounds__(kAxThreads) append_axes_kernel(const __grid_co
     // counts, is skipped whole.
     if (t < a0 || t >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || (n_pages > 0 && (last < 1 || last > P))) {
       err |= kErrAppendLayout;
+      skip();
       continue;
     }
     const int place = static_cast<int>(kv_len - (a1 - a0) + (t - a0));
-    const int page = __ldg(a.kv_indices + p0 + place / P);
+    const int page_no = place / P, slot = place - page_no * P;
+    const int page = __ldg(a.kv_indices + p0 + page_no);
     if (page < 0 || page >= a.num_pages) {
       err |= kErrPageIndex;
+      skip();
       continue;
     }
-    const int slot = place % P;
-    float c[8], s[8];
+    if (!a.positions) pos = place;
+    float2 c[4], s[4], ns[4];  // cosines, sines and their negatives
     if (a.rot_chunks > 0) {
-      int32_t pos = place;  // lane x: the token's position on axis x
-      if (a.positions && lane < a.num_axes) pos = __ldg(a.positions + lane * a.nnz + t);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const int32_t pj = __shfl_sync(0xffffffffu, pos, (axes >> (4 * j)) & 15u);
-        sincos_turn(pj, freq[j], s[j], c[j]);
+        float sj, cj;
+        sincos_turn(pj, s_freq[turns ? sub * 8 + j : 0], sj, cj);
+        (j & 1 ? s[j >> 1].y : s[j >> 1].x) = sj;
+        (j & 1 ? ns[j >> 1].y : ns[j >> 1].x) = -sj;
+        (j & 1 ? c[j >> 1].y : c[j >> 1].x) = cj;
       }
     }
-    const int64_t head0 = static_cast<int64_t>(page) * 2 * Hkv;  // first (K|V, head) block of the page
-    const int r_end = min(rows, (part + 1) * a.part_passes * RPP);
-    for (int r0 = part * a.part_passes * RPP; r0 < r_end; r0 += CHUNK * RPP) {
-      uint4 xa[CHUNK], xb[CHUNK];
+    // The turned pair of chunks of a row.
+    auto turn = [&](float2 (&fa)[4], float2 (&fb)[4]) {
 #pragma unroll
-      for (int k = 0; k < CHUNK; ++k) {
-        const int r = r0 + k * RPP + hsub;
-        xa[k] = xb[k] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < r_end) {
-          const T* src = r < Hkv ? k_new + (t * Hkv + r) * D
-                                 : (r < Hkv + Hq ? q_in + (t * Hq + (r - Hkv)) * D
-                                                 : v_new + (t * Hkv + (r - Hkv - Hq)) * D);
-          xa[k] = *reinterpret_cast<const uint4*>(src + off_a);
-          xb[k] = *reinterpret_cast<const uint4*>(src + off_b);
-        }
+      for (int j = 0; j < 4; ++j) {
+        const float2 u = fa[j], v = fb[j];
+        fa[j] = ffma2(u, c[j], fmul2(v, ns[j]));
+        fb[j] = ffma2(v, c[j], fmul2(u, s[j]));
       }
-#pragma unroll
-      for (int k = 0; k < CHUNK; ++k) {
-        const int r = r0 + k * RPP + hsub;
-        const bool valid = r < r_end, is_q = r >= Hkv && r < Hkv + Hq, is_v = r >= Hkv + Hq;
-        float fa[8], fb[8];
-        to_float8<T>(xa[k], fa);
-        to_float8<T>(xb[k], fb);
-        uint32_t field = 0;
+    };
+    const int64_t head0 = static_cast<int64_t>(page) * 2 * Hkv;  // first (K|V, head) block of the page
+    for (int pass = pass0; pass < pass1; ++pass) {
+      uint4 x[4];
+      take(x);
+      if (pass < kv_passes) {
+        const int r = pass * RPP + hsub;
+        // K of head r is block r of the page, V of head r block Hkv + r.
+        const int64_t k_row = (head0 + r) * P + slot, v_row = k_row + static_cast<int64_t>(Hkv) * P;
+        uint32_t ks = 0, vs = 0;
         if constexpr (OUT8) {
-          // The row's largest finite |x|, as float bits (ordered like the values).
-          uint32_t mx = 0;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const uint32_t ba = __float_as_uint(fa[j]) & 0x7fffffffu, bb = __float_as_uint(fb[j]) & 0x7fffffffu;
-            if (ba < 0x7f800000u) mx = max(mx, ba);
-            if (bb < 0x7f800000u) mx = max(mx, bb);
-          }
-#pragma unroll
-          for (int o = LPH / 2; o >= 1; o >>= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-          field = mx >> 23;
+          ks = row_exponent<T, LPH>(x[0], x[1]);
+          vs = row_exponent<T, LPH>(x[2], x[3]);
         }
-        if (!valid) continue;
-        const uint32_t sc = max(static_cast<int>(field) - 7, 1);
-        if (OUT8 && !is_q) {
-          const float mul = __uint_as_float((254u - sc) << 23);  // 2^(127 - sc)
+        float2 fa[4], fb[4];
+        to_float2x4<T>(x[0], fa);
+        to_float2x4<T>(x[1], fb);
+        if constexpr (OUT8) {
+          const float km = __uint_as_float((254u - ks) << 23), vm = __uint_as_float((254u - vs) << 23);  // 2^(127 - s)
+          const float2 km2 = make_float2(km, km), vm2 = make_float2(vm, vm);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            fa[j] *= mul;
-            fb[j] *= mul;
+          for (int j = 0; j < 4; ++j) {
+            fa[j] = fmul2(fa[j], km2);
+            fb[j] = fmul2(fb[j], km2);
           }
-        }
-        if (turns && !is_v) {
+          if (turns) {
+            turn(fa, fb);
+            bool near = false;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float x = fa[j], y = fb[j];
-            fa[j] = fmaf(x, c[j], -y * s[j]);
-            fb[j] = fmaf(y, c[j], x * s[j]);
+            for (int j = 0; j < 4; ++j)
+              near |= near_border(fa[j].x) || near_border(fa[j].y) || near_border(fb[j].x) || near_border(fb[j].y);
+            if (near) {
+              float2 ua[4], ub[4];  // unturned
+              to_float2x4<T>(x[0], ua);
+              to_float2x4<T>(x[1], ub);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float& ra = j & 1 ? fa[j >> 1].y : fa[j >> 1].x;
+                float& rb = j & 1 ? fb[j >> 1].y : fb[j >> 1].x;
+                if (near_border(ra) || near_border(rb)) {
+                  const int axis = (axes >> (4 * j)) & 15u;
+                  const int32_t pj = a.positions ? __ldg(a.positions + axis * a.nnz + t) : place;
+                  const float2 d = turn_pair_double((j & 1 ? ua[j >> 1].y : ua[j >> 1].x) * km,
+                                                    (j & 1 ? ub[j >> 1].y : ub[j >> 1].x) * km, pj, s_freq[sub * 8 + j]);
+                  ra = d.x;
+                  rb = d.y;
+                }
+              }
+            }
           }
-        }
-        if (is_q) {
-          T* dst = static_cast<T*>(a.q_out) + (t * Hq + (r - Hkv)) * D;
-          *reinterpret_cast<uint4*>(dst + off_a) = from_float8<T>(fa);
-          *reinterpret_cast<uint4*>(dst + off_b) = from_float8<T>(fb);
-        } else {
-          // K of head h is block h of the page, V of head h block Hkv + h.
-          const int64_t row = (head0 + (is_v ? r - Hq : r)) * P + slot;
-          if constexpr (OUT8) {
-            uint8_t* dst = static_cast<uint8_t*>(a.kv) + row * D;
+          if (r < Hkv) {
+            uint8_t* dst = static_cast<uint8_t*>(a.kv) + k_row * D;
             *reinterpret_cast<uint2*>(dst + off_a) = pack_e4m3x8(fa);
             *reinterpret_cast<uint2*>(dst + off_b) = pack_e4m3x8(fb);
-            if (sub == 0) a.scales[row] = static_cast<uint8_t>(sc);
-          } else {
-            T* dst = static_cast<T*>(a.kv) + row * D;
-            *reinterpret_cast<uint4*>(dst + off_a) = from_float8<T>(fa);
-            *reinterpret_cast<uint4*>(dst + off_b) = from_float8<T>(fb);
+            to_float2x4<T>(x[2], fa);
+            to_float2x4<T>(x[3], fb);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              fa[j] = fmul2(fa[j], vm2);
+              fb[j] = fmul2(fb[j], vm2);
+            }
+            const uint2 ca = pack_e4m3x8(fa), cb = pack_e4m3x8(fb);
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.kv) + v_row * D + sub * 16) = make_uint4(ca.x, ca.y, cb.x, cb.y);
+            if (sub == 0) {
+              a.scales[k_row] = static_cast<uint8_t>(ks);
+              a.scales[v_row] = static_cast<uint8_t>(vs);
+            }
+          }
+        } else if (r < Hkv) {
+          T* kd = static_cast<T*>(a.kv) + k_row * D;
+          T* vd = static_cast<T*>(a.kv) + v_row * D;
+          if (turns) {
+            turn(fa, fb);
+            x[0] = pack_16x8<T>(fa);
+            x[1] = pack_16x8<T>(fb);
+          }
+          *reinterpret_cast<uint4*>(kd + off_a) = x[0];
+          *reinterpret_cast<uint4*>(kd + off_b) = x[1];
+          *reinterpret_cast<uint4*>(vd + sub * 16) = x[2];
+          *reinterpret_cast<uint4*>(vd + sub * 16 + 8) = x[3];
+        }
+      } else {
+        const int r = (pass - kv_passes) * 2 * RPP + hsub;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          if (turns) {
+            float2 fa[4], fb[4];
+            to_float2x4<T>(x[2 * h], fa);
+            to_float2x4<T>(x[2 * h + 1], fb);
+            turn(fa, fb);
+            x[2 * h] = pack_16x8<T>(fa);
+            x[2 * h + 1] = pack_16x8<T>(fb);
+          }
+          if (r + h * RPP < Hq) {
+            T* dst = static_cast<T*>(a.q_out) + (t * Hq + r + h * RPP) * D;
+            *reinterpret_cast<uint4*>(dst + off_a) = x[2 * h];
+            *reinterpret_cast<uint4*>(dst + off_b) = x[2 * h + 1];
           }
         }
       }
@@ -266,8 +436,10 @@ __global__ void __launch_bounds__(kAxThreads) append_axes_kernel(const __grid_co
 
 template <int D, typename T>
 cudaError_t launch_t(const AxesArgs& a, int grid, cudaStream_t s) {
-  return a.scales ? launch_dependent(append_axes_kernel<D, T, true>, grid, kAxThreads, 0, s, a)
-                  : launch_dependent(append_axes_kernel<D, T, false>, grid, kAxThreads, 0, s, a);
+  void (*kern)(AxesArgs) = a.scales ? append_axes_kernel<D, T, true> : append_axes_kernel<D, T, false>;
+  cudaError_t e = ensure_smem_limit(kern, kAxSmem);
+  if (e != cudaSuccess) return e;
+  return launch_dependent(kern, grid, kAxThreads, kAxSmem, s, a);
 }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -357,17 +529,17 @@ pkv_status append_axes(const pkv_params* p, const pkv_rope_axes* rope, int batch
     cudaGetLastError();
     return PKV_ERR_CUDA;
   }
-  // Few tokens are shared by several warps each, down to one pass of head rows a
-  // warp, until there are 16 warps for every SM.
+  // Few tokens are shared by several warps each, down to one pass a warp, until there
+  // are 16 warps for every SM.
   const int rpp = 32 / (p->head_dim / 16);
-  const int rows = 2 * p->num_kv_heads + (q_in ? p->num_qo_heads : 0);
-  const int passes = (rows + rpp - 1) / rpp;
+  const int hq = q_in ? p->num_qo_heads : 0;
+  const int passes = (p->num_kv_heads + rpp - 1) / rpp + (hq + 2 * rpp - 1) / (2 * rpp);
   const int64_t share = (static_cast<int64_t>(sms) * 16 + nnz - 1) / nnz;
   const int parts = static_cast<int>(share < passes ? share : passes);
   a.part_passes = (passes + parts - 1) / parts;
   a.parts = (passes + a.part_passes - 1) / a.part_passes;
-  const int64_t want = (nnz * a.parts + kAxWarps - 1) / kAxWarps;
-  const int grid = static_cast<int>(want < static_cast<int64_t>(sms) * 8 ? want : static_cast<int64_t>(sms) * 8);
+  const int64_t want = (nnz + kAxWarps - 1) / kAxWarps * a.parts, room = static_cast<int64_t>(sms) * 2 / a.parts * a.parts;
+  const int grid = static_cast<int>(want < room ? want : std::max<int64_t>(room, a.parts));
   auto s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (p->head_dim == 128)
