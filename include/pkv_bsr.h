@@ -557,7 +557,8 @@ pkv_status pkv_append_paged_kv8(const pkv_params* params, const pkv_rope_axes* r
  * operands, with fp32 sums: queries keep 11 significant bits relative to their row's
  * largest element, probabilities 11 bits.
  * Errors: PKV_ERR_INVALID_ARG (a null or misaligned pointer, a plan of another kind or
- * not planned), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ * not planned), PKV_ERR_UNSUPPORTED (a pool of 2^32 - 1 head rows or more),
+ * PKV_ERR_CUDA.
  */
 pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const void* kv8, const uint8_t* kv8_scales,
                                       const int32_t* kv_indices_d, const int32_t* kv_indptr_d,

@@ -184,7 +184,8 @@ __device__ __forceinline__ void feed_issue(Feed& p, const DecodeArgs& a, const u
     const uint32_t dst = rows0 + p.stage * 2 * S::kTile, dst_s = scales0 + p.stage * S::kScales;
     p.stage = p.stage + 1 == S::kStages ? 0 : p.stage + 1;
     const uint8_t* kv = static_cast<const uint8_t*>(a.kv);
-    const int64_t vdist = static_cast<int64_t>(a.num_kv_heads) * P;  // rows from a K row to its V row
+    const uint32_t vdist = static_cast<uint32_t>(a.num_kv_heads) * P;  // rows from a K row to its V row
+    const uint8_t* kv_v = kv + static_cast<uint64_t>(vdist) * D;
     if (p.page - p.win_base >= 32) {
       p.win_base += 32;
       p.win = p.win_next;
@@ -194,20 +195,19 @@ __device__ __forceinline__ void feed_issue(Feed& p, const DecodeArgs& a, const u
     if constexpr (MODE == kOne) {
       const int id = __shfl_sync(kFull, p.win, w0);
       const bool bad = id < 0 || id >= num_pages;
-      const int64_t at = bad ? 0 : (static_cast<int64_t>(id) * 2 * a.num_kv_heads + p.kvh) * P + p.row;
+      const uint32_t at = bad ? 0u : (static_cast<uint32_t>(id) * 2u * a.num_kv_heads + p.kvh) * P + p.row;
       const int valid = bad ? 0 : rows;
       // The tile's rows are contiguous: chunk it * 32 + lane of K, and of V.
-      const uint8_t* ks = kv + at * D + lane * 16;
-      const uint8_t* vs = ks + vdist * D;
+      const uint64_t off = static_cast<uint64_t>(at) * D + lane * 16;
 #pragma unroll
       for (int it = 0; it < kRows / RPI; ++it) {
         const int r = it * RPI + lane / CPR, c = lane % CPR;
         const uint32_t n = r < valid ? 16u : 0u;
-        cp_async_16_hint(dst + k_off<D>(r, c), ks + it * 512, n, policy);
-        cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), vs + it * 512, n, policy);
+        cp_async_16_hint(dst + k_off<D>(r, c), kv + off + it * 512, n, policy);
+        cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), kv_v + off + it * 512, n, policy);
       }
       if (lane < 8)
-        cp_async_4(dst_s + lane * 4, scales + at + (lane & 3) * 4 + (lane < 4 ? 0 : vdist), bad ? 0u : 4u);
+        cp_async_4(dst_s + lane * 4, scales + (at + (lane & 3) * 4 + (lane < 4 ? 0u : vdist)), bad ? 0u : 4u);
       if (bad && lane == 0) atomicOr(a.err, kErrPageIndex);
       p.row += kRows;
       if (p.row == P) {
@@ -215,47 +215,41 @@ __device__ __forceinline__ void feed_issue(Feed& p, const DecodeArgs& a, const u
         ++p.page;
       }
     } else {
-      bool bad = false;
-      // Row (counted over the pool's (page, head) blocks) of K row r of the tile, or -1
-      // past the tile's rows or in a page outside the pool.
-      auto place = [&](int r) -> int64_t {
-        const int x = p.row + r;
-        const int k = static_cast<int>((static_cast<uint32_t>(x) * small_div) >> 12);  // x / P
-        const int id0 = __shfl_sync(kFull, p.win, (w0 + k) & 31), id1 = __shfl_sync(kFull, p.win_next, (w0 + k) & 31);
-        const int id = w0 + k < 32 ? id0 : id1;
-        if (r >= rows) return -1;
-        if (id < 0 || id >= num_pages) {
-          bad = true;
-          return -1;
-        }
-        return (static_cast<int64_t>(id) * 2 * a.num_kv_heads + p.kvh) * P + (x - k * P);
-      };
+      // Lanes i and 16 + i find K row i of the tile: its row counted over the pool's
+      // (page, head) blocks, or kNone past the tile's rows or in a page outside the pool.
+      constexpr uint32_t kNone = 0xffffffffu;
+      const int i = lane & 15, x = p.row + i;
+      const int k = static_cast<int>((static_cast<uint32_t>(x) * small_div) >> 12);  // x / P
+      const int id0 = __shfl_sync(kFull, p.win, (w0 + k) & 31), id1 = __shfl_sync(kFull, p.win_next, (w0 + k) & 31);
+      const int id = w0 + k < 32 ? id0 : id1;
+      const bool bad = i < rows && (id < 0 || id >= num_pages);
+      uint32_t at = (static_cast<uint32_t>(id) * 2u * a.num_kv_heads + p.kvh) * P + (x - k * P);
+      if (bad || i >= rows) at = kNone;
+      if (bad) atomicOr(a.err, kErrPageIndex);
 #pragma unroll
       for (int it = 0; it < kRows / RPI; ++it) {
         const int r = it * RPI + lane / CPR, c = lane % CPR;
-        const int64_t at = place(r);
-        const uint8_t* ks = kv + (at < 0 ? 0 : at * D) + c * 16;
-        const uint32_t n = at < 0 ? 0u : 16u;
-        cp_async_16_hint(dst + k_off<D>(r, c), ks, n, policy);
-        cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), at < 0 ? ks : ks + vdist * D, n, policy);
+        const uint32_t row = __shfl_sync(kFull, at, r);
+        const uint64_t off = row == kNone ? 0u : static_cast<uint64_t>(row) * D + c * 16;
+        const uint32_t n = row == kNone ? 0u : 16u;
+        cp_async_16_hint(dst + k_off<D>(r, c), kv + off, n, policy);
+        cp_async_16_hint(dst + S::kTile + v_off<D>(r, c), row == kNone ? kv : kv_v + off, n, policy);
       }
       if constexpr (MODE == kFours) {
-        const int64_t at = place((lane & 3) * 4);
+        const uint32_t row = __shfl_sync(kFull, at, (lane & 3) * 4);
         if (lane < 8)
-          cp_async_4(dst_s + lane * 4, scales + (at < 0 ? 0 : at + (lane < 4 ? 0 : vdist)), at < 0 ? 0u : 4u);
+          cp_async_4(dst_s + lane * 4, scales + (row == kNone ? 0u : row + (lane < 4 ? 0u : vdist)), row == kNone ? 0u : 4u);
       } else {
         // Lane i < 16: K's byte of token i, lane 16 + i: V's.
-        const int64_t at = place(lane & 15);
-        const int64_t byte = at < 0 ? 0 : at + (lane < 16 ? 0 : vdist), word = byte & ~int64_t{3};
-        const int64_t left = num_pages * 2 * vdist - word;  // bytes of the pool from this word on
-        cp_async_4(dst_s + lane * 4, scales + word, at < 0 ? 0u : static_cast<uint32_t>(left < 4 ? left : 4));
-        sts8(dst_s + 128 + lane, static_cast<uint32_t>(byte - word) * 8);
+        const uint32_t byte = at == kNone ? 0u : at + (lane < 16 ? 0u : vdist), word = byte & ~3u;
+        const uint64_t left = static_cast<uint64_t>(num_pages) * 2 * vdist - word;  // bytes of the pool from this word on
+        cp_async_4(dst_s + lane * 4, scales + word, at == kNone ? 0u : static_cast<uint32_t>(left < 4 ? left : 4));
+        sts8(dst_s + 128 + lane, (byte - word) * 8);
       }
-      if (bad) atomicOr(a.err, kErrPageIndex);
       p.row += kRows;
-      const int k = static_cast<int>((static_cast<uint32_t>(p.row) * small_div) >> 12);
-      p.page += k;
-      p.row -= k * P;
+      const int full = static_cast<int>((static_cast<uint32_t>(p.row) * small_div) >> 12);
+      p.page += full;
+      p.row -= full * P;
     }
     p.tok += rows;
   }
@@ -602,7 +596,9 @@ cudaError_t launch_t(const Decode8Args& a, bool cap, int grid, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_decode8(const DecodeArgs& d, const uint8_t* scales, float sm_scale, int head_dim, int dtype, bool cap,
-                           int grid, cudaStream_t stream) {
+                           int grid, int64_t num_pages, cudaStream_t stream) {
+  // Rows of the pool are counted in 32 bits, with the last value for none.
+  if (static_cast<double>(num_pages) * 2 * d.num_kv_heads * d.page_size >= 4294967295.0) return cudaErrorInvalidValue;
   Decode8Args a{d, scales, sm_scale, 0};
   if (d.page_size < kRows) a.small_div = (4096 + d.page_size - 1) / d.page_size;
   if (head_dim == 128)

@@ -94,7 +94,7 @@ cudaError_t set_kv_rows_map(DecodeArgs& a, int head_dim, int dtype, int64_t num_
 // The same over the 8-bit cache (d.kv: e4m3 codes, scales: their exponent bytes; any
 // built group, no tensor map); its merge is launch_decode_merge over d.
 cudaError_t launch_decode8(const DecodeArgs& d, const uint8_t* scales, float sm_scale, int head_dim, int dtype, bool cap,
-                           int grid, cudaStream_t stream);
+                           int grid, int64_t num_pages, cudaStream_t stream);
 // Launch the n-way merge of split decode sequences (fixed grid).
 cudaError_t launch_decode_merge(const DecodeArgs& a, int head_dim, int group, int dtype, int grid,
                                 cudaStream_t stream);
