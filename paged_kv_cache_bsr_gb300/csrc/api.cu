@@ -291,7 +291,7 @@ pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const
     e = pkv::launch_decode8(a, kv8_scales, p.sm_scale, p.head_dim, p.dtype, p.logits_cap > 0.f, plan->grid_ctas,
                             plan->num_pages, s);
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
-  if (e == cudaSuccess) e = pkv::launch_decode_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
+  if (e == cudaSuccess) e = pkv::launch_decode8_merge(a, p.head_dim, p.dtype, plan->merge_grid, s);
   if (e == cudaSuccess) e = release_tables(plan, s);
   return launch_status(e);
 }

@@ -20,7 +20,7 @@
 // mma.sync m16n8k16 (fp16 operands, fp32 sums): 16 keys x 8 heads of the group
 // (padded), then 16 dims x 8 heads.  Keys and dims are the M axis, so a group of 8
 // wastes nothing, and the padding of a smaller one costs no bandwidth.
-//  - One CTA per SM holds kDecodeWarps independent warps, each with the plan's
+//  - One CTA per SM holds 8 (head_dim 64: 16) independent warps, each with the plan's
 //    list of (request, kv head, page range) segments and a ring of 16-token tiles in
 //    shared memory, filled by its own 16-byte cp.async copies kStages - 1 tiles
 //    ahead (any page size, zeros past the request: nothing unread is ever in a
@@ -59,7 +59,9 @@ struct Shape8 {
   // Exponent bytes of one tile: 16 of K and 16 of V, or (kAny) the aligned word
   // around each, with the byte's place in it behind the words.
   static constexpr int kScales = MODE == kAny ? 32 * 5 : 32;
-  static constexpr int kStages = D == 128 ? (MODE == kAny ? 6 : 7) : (MODE == kAny ? 12 : 13);  // 24 - 28 KB of rows
+  // 200 - 230 KB of rows and exponents per CTA.
+  static constexpr int kStages = D == 128 ? (MODE == kAny ? 6 : 7) : 6;
+  static constexpr int kWarps = decode8_warps(D);
   static constexpr int kWarpBytes = kStages * (2 * kTile + kScales);
 };
 
@@ -416,10 +418,11 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
   const DecodeArgs& a = a8.d;
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const PlanHeader* hdr = a.hdr;
-  if (worker >= hdr->num_workers) return;
-  const int64_t num_pages = hdr->num_pages;
+  // The table has an entry for every worker of the grid: read beside the header, used
+  // where the plan gave this worker work.
   const int seg_begin = a.worker_ptr[worker], seg_end = a.worker_ptr[worker + 1];
-  if (seg_begin >= seg_end) return;
+  const int64_t num_pages = hdr->num_pages;
+  if (worker >= hdr->num_workers || seg_begin >= seg_end) return;
   const uint64_t policy = l2_policy_evict_first();
   const int G = a.num_qo_heads / a.num_kv_heads;
 
@@ -496,27 +499,28 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
       sS = scales0 + stage * S::kScales;
       stage = stage + 1 == ST ? 0 : stage + 1;
     };
-    // Two tiles a step (more independent work for the warp between its waits), and
-    // one where an odd tile is left.  Of the ST - 1 groups ahead of the compute side
-    // the first two (or one) must have landed.
+    // NT tiles a step (more independent work for the warp between its waits), and one a
+    // step where fewer are left.  Of the ST - 1 groups ahead
+    // of the compute side the first NT (or one) must have landed.
+    constexpr int NT = 2;
     int tok = 0;
-    for (; tok + kRows < n_tok; tok += 2 * kRows) {
-      cp_async_wait<ST - 3>();
+    for (; tok + (NT - 1) * kRows < n_tok; tok += NT * kRows) {
+      cp_async_wait<ST - 1 - NT>();
       __syncwarp();
-      uint32_t sK[2], sS[2];
-      next_stage(sK[0], sS[0]);
-      next_stage(sK[1], sS[1]);
-      tiles_step<D, CAP, MODE, 2>(a, sK, sS, min(kRows, n_tok - tok - kRows), g, t, qf, qs0, qs1, st);
+      uint32_t sK[NT], sS[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) next_stage(sK[n], sS[n]);
+      tiles_step<D, CAP, MODE, NT>(a, sK, sS, min(kRows, n_tok - tok - (NT - 1) * kRows), g, t, qf, qs0, qs1, st);
       __syncwarp();  // every lane has read the stages before they are filled again
-      issue();
-      issue();
+#pragma unroll 1
+      for (int n = 0; n < NT; ++n) issue();
     }
-    if (tok < n_tok) {
+    for (; tok < n_tok; tok += kRows) {
       cp_async_wait<ST - 2>();
       __syncwarp();
       uint32_t sK[1], sS[1];
       next_stage(sK[0], sS[0]);
-      tiles_step<D, CAP, MODE, 1>(a, sK, sS, n_tok - tok, g, t, qf, qs0, qs1, st);
+      tiles_step<D, CAP, MODE, 1>(a, sK, sS, min(kRows, n_tok - tok), g, t, qf, qs0, qs1, st);
       __syncwarp();
       issue();
     }
@@ -559,7 +563,7 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
 }
 
 template <int D, typename T, bool CAP, PageMode MODE>
-__global__ void __launch_bounds__(kDecodeWarps * 32, 1) decode8_kernel(const __grid_constant__ Decode8Args a) {
+__global__ void __launch_bounds__(decode8_warps(D) * 32, 1) decode8_kernel(const __grid_constant__ Decode8Args a) {
   using S = Shape8<D, MODE>;
   extern __shared__ __align__(128) uint8_t smem[];
   // Launched as a programmatic dependent of the kernel before it on the stream:
@@ -567,18 +571,133 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) decode8_kernel(const __g
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5;
   const uint32_t base = smem_addr(smem);
-  decode8_worker<D, T, CAP, MODE>(a, blockIdx.x * kDecodeWarps + warp, base + warp * (S::kStages * 2 * S::kTile),
-                                 base + kDecodeWarps * (S::kStages * 2 * S::kTile) + warp * (S::kStages * S::kScales));
+  constexpr int W = S::kWarps;
+  decode8_worker<D, T, CAP, MODE>(a, blockIdx.x * W + warp, base + warp * (S::kStages * 2 * S::kTile),
+                                 base + W * (S::kStages * 2 * S::kTile) + warp * (S::kStages * S::kScales));
+}
+
+// The merge of split sequences, as decode_merge_pair computes it, with the slots of one
+// (item, head) dealt to as many warps of a CTA as the grid has to spare and the slots
+// fill (a power of two up to all of them): a request of 8192 tokens alone leaves 32 such
+// pairs of 152 slots, which take one warp each 10 us to read and eight warps 2.5 us; the
+// serving batch leaves 2016 pairs of 3 slots, a warp each.  The warps' states are
+// combined in their order, so the result does not depend on timing.
+template <int D, typename T>
+__global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const __grid_constant__ DecodeArgs a) {
+  constexpr int PER = D / 32;           // dims per lane
+  constexpr int W = kMergeThreads / 32;
+  constexpr int U = 8;                  // slots in flight per lane
+  __shared__ float s_o[W][D];
+  __shared__ float s_m[W], s_l[W];
+  // Launched as a programmatic dependent of the decode kernel: wait until that grid
+  // has finished and its partial states are visible.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.num_qo_heads / a.num_kv_heads;
+  const int n_items = a.hdr->num_merge, n_slots = a.hdr->num_slots;
+  const int pairs = n_items * G;
+  int wpp = W;  // warps per pair
+  while (wpp > 1 && (static_cast<int64_t>(pairs) * wpp > static_cast<int64_t>(gridDim.x) * W ||
+                     static_cast<int64_t>(n_items) * wpp * 4 > n_slots))
+    wpp >>= 1;
+  const int per_cta = W / wpp, part = warp % wpp;
+  for (int p0 = blockIdx.x * per_cta; p0 < pairs; p0 += gridDim.x * per_cta) {
+    const int pair = p0 + warp / wpp;
+    const bool have = pair < pairs;
+    float m = -INFINITY, l = 0.f, acc[PER];
+#pragma unroll
+    for (int v = 0; v < PER; ++v) acc[v] = 0.f;
+    MergeItem it{};
+    const int g = pair % G;
+    if (have) {
+      it = a.merge[pair / G];
+      const int lo = static_cast<int>(static_cast<int64_t>(it.n_slots) * part / wpp),
+                hi = static_cast<int>(static_cast<int64_t>(it.n_slots) * (part + 1) / wpp);
+      const float* lse_p = a.part_lse + static_cast<int64_t>(it.slot_begin) * G + g;
+      const float* o_p = a.part_o + (static_cast<int64_t>(it.slot_begin) * G + g) * D + lane * PER;
+      for (int i0 = lo; i0 < hi; i0 += U) {
+        // U slots' lse and rows together, then folded into the running state.
+        float vals[U][PER], lse[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          lse[u] = -INFINITY;
+#pragma unroll
+          for (int v = 0; v < PER; ++v) vals[u][v] = 0.f;
+          if (i0 + u < hi) {
+            const int64_t row = static_cast<int64_t>(i0 + u) * G;
+            lse[u] = lse_p[row];
+#pragma unroll
+            for (int v = 0; v < PER; v += 2) {
+              const float2 x = *reinterpret_cast<const float2*>(o_p + row * D + v);
+              vals[u][v] = x.x;
+              vals[u][v + 1] = x.y;
+            }
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int u = 0; u < U; ++u) top = fmaxf(top, lse[u]);
+        if (top == -INFINITY) continue;
+        const float w0 = fast_exp2((m - top) * kLog2e);  // 0 while m is -inf
+        l *= w0;
+#pragma unroll
+        for (int v = 0; v < PER; ++v) acc[v] *= w0;
+        m = top;
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const float w = fast_exp2((lse[u] - m) * kLog2e);  // 0 for a slot past hi
+          l += w;
+#pragma unroll
+          for (int v = 0; v < PER; ++v) acc[v] = fmaf(w, vals[u][v], acc[v]);
+        }
+      }
+    }
+    if (wpp > 1) {
+      __syncthreads();  // the round before has been read
+      if (lane == 0) {
+        s_m[warp] = m;
+        s_l[warp] = l;
+      }
+#pragma unroll
+      for (int v = 0; v < PER; ++v) s_o[warp][lane * PER + v] = acc[v];
+      __syncthreads();
+      if (part == 0) {
+        float top = m;
+        for (int k = 1; k < wpp; ++k) top = fmaxf(top, s_m[warp + k]);
+        const float w0 = m == -INFINITY ? 0.f : fast_exp2((m - top) * kLog2e);
+        l *= w0;
+#pragma unroll
+        for (int v = 0; v < PER; ++v) acc[v] *= w0;
+        for (int k = 1; k < wpp; ++k) {
+          if (s_m[warp + k] == -INFINITY) continue;
+          const float w = fast_exp2((s_m[warp + k] - top) * kLog2e);
+          l = fmaf(w, s_l[warp + k], l);
+#pragma unroll
+          for (int v = 0; v < PER; ++v) acc[v] = fmaf(w, s_o[warp + k][lane * PER + v], acc[v]);
+        }
+        m = top;
+      }
+    }
+    if (have && part == 0) {
+      const int64_t row = static_cast<int64_t>(it.row) * a.num_qo_heads + it.kvh * G + g;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      T* dst = static_cast<T*>(a.o) + row * D + lane * PER;
+#pragma unroll
+      for (int v = 0; v < PER; v += 2)
+        *reinterpret_cast<uint32_t*>(dst + v) = pack2<T>(acc[v] * inv, acc[v + 1] * inv);
+      if (lane == 0 && a.lse) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+    }
+  }
 }
 
 template <int D, typename T>
 cudaError_t launch_t(const Decode8Args& a, bool cap, int grid, cudaStream_t s) {
   const int P = a.d.page_size;
   void (*kern)(Decode8Args) = nullptr;
-  int smem = kDecodeWarps * Shape8<D, kOne>::kWarpBytes;
-  static_assert(kDecodeWarps * Shape8<D, kOne>::kWarpBytes <= 232448 &&
-                    Shape8<D, kFours>::kWarpBytes == Shape8<D, kOne>::kWarpBytes &&
-                    Shape8<D, kAny>::kWarpBytes <= Shape8<D, kOne>::kWarpBytes,
+  constexpr int W = decode8_warps(D);
+  int smem = W * Shape8<D, kOne>::kWarpBytes;
+  static_assert(W * Shape8<D, kOne>::kWarpBytes <= 232448 && W * Shape8<D, kAny>::kWarpBytes <= 232448 &&
+                    Shape8<D, kFours>::kWarpBytes == Shape8<D, kOne>::kWarpBytes,
                 "decode ring exceeds shared memory");
   if (P % kRows == 0) {
     kern = cap ? decode8_kernel<D, T, true, kOne> : decode8_kernel<D, T, false, kOne>;
@@ -586,11 +705,11 @@ cudaError_t launch_t(const Decode8Args& a, bool cap, int grid, cudaStream_t s) {
     kern = cap ? decode8_kernel<D, T, true, kFours> : decode8_kernel<D, T, false, kFours>;
   } else {
     kern = cap ? decode8_kernel<D, T, true, kAny> : decode8_kernel<D, T, false, kAny>;
-    smem = kDecodeWarps * Shape8<D, kAny>::kWarpBytes;
+    smem = W * Shape8<D, kAny>::kWarpBytes;
   }
   cudaError_t e = ensure_smem_limit(kern, smem);
   if (e != cudaSuccess) return e;
-  return launch_dependent(kern, grid, kDecodeWarps * 32, smem, s, a);
+  return launch_dependent(kern, grid, W * 32, smem, s, a);
 }
 
 }  // namespace
@@ -606,6 +725,16 @@ cudaError_t launch_decode8(const DecodeArgs& d, const uint8_t* scales, float sm_
   if (head_dim == 64)
     return dtype == PKV_BF16 ? launch_t<64, __nv_bfloat16>(a, cap, grid, stream) : launch_t<64, __half>(a, cap, grid, stream);
   return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode8_merge(const DecodeArgs& a, int head_dim, int dtype, int grid, cudaStream_t stream) {
+  void (*kern)(DecodeArgs) = nullptr;
+  if (head_dim == 128)
+    kern = dtype == PKV_BF16 ? decode8_merge_kernel<128, __nv_bfloat16> : decode8_merge_kernel<128, __half>;
+  else if (head_dim == 64)
+    kern = dtype == PKV_BF16 ? decode8_merge_kernel<64, __nv_bfloat16> : decode8_merge_kernel<64, __half>;
+  if (!kern) return cudaErrorInvalidValue;
+  return launch_dependent(kern, grid, kMergeThreads, 0, stream, a);
 }
 
 }  // namespace pkv

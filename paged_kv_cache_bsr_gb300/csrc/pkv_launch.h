@@ -91,10 +91,14 @@ cudaError_t launch_decode(const DecodeArgs& a, int head_dim, int group, int dtyp
 // Fill a.kv_rows / a.kv_rows_n for the gather instances: kv_data as rows of
 // head_dim elements, one-row boxes.
 cudaError_t set_kv_rows_map(DecodeArgs& a, int head_dim, int dtype, int64_t num_pages);
+// Warps per CTA of the 8-bit cache's decode kernel: a head_dim-64 tile is half the bytes
+// for the same steps around it, and its smaller state leaves registers for 16 warps.
+constexpr int decode8_warps(int head_dim) { return head_dim == 64 ? 16 : kDecodeWarps; }
 // The same over the 8-bit cache (d.kv: e4m3 codes, scales: their exponent bytes; any
-// built group, no tensor map); its merge is launch_decode_merge over d.
+// built group, no tensor map), and the merge of its split sequences (fixed grid).
 cudaError_t launch_decode8(const DecodeArgs& d, const uint8_t* scales, float sm_scale, int head_dim, int dtype, bool cap,
                            int grid, int64_t num_pages, cudaStream_t stream);
+cudaError_t launch_decode8_merge(const DecodeArgs& a, int head_dim, int dtype, int grid, cudaStream_t stream);
 // Launch the n-way merge of split decode sequences (fixed grid).
 cudaError_t launch_decode_merge(const DecodeArgs& a, int head_dim, int group, int dtype, int grid,
                                 cudaStream_t stream);

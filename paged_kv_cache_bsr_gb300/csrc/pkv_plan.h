@@ -49,6 +49,7 @@ struct pkv_plan {
   // Fixed grid and table capacities (depend on params and limits only).
   int grid_ctas = 0;
   int workers = 0;
+  int cta_warps = 0;        // decode tables: workers per CTA
   int max_work = 0;
   int max_merge = 0;
   int max_slots = 0;

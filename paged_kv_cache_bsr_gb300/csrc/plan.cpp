@@ -157,7 +157,8 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
   pl->exec_prefill = kind == PKV_PLAN_DECODE && !kv8 && route_decode && decode_on_tensor_cores(params);
   if (kind == PKV_PLAN_DECODE && !pl->exec_prefill) {
     pl->grid_ctas = num_sms;
-    pl->workers = num_sms * pkv::kDecodeWarps;
+    pl->cta_warps = kv8 ? pkv::decode8_warps(params->head_dim) : pkv::kDecodeWarps;
+    pl->workers = num_sms * pl->cta_warps;
     // Each worker's run cuts at most two page lists, and every list adds at
     // most one uncut entry; see the decode branch of compute_decode.
     const int64_t max_work = pl->workers + static_cast<int64_t>(limits->max_batch) * hkv + 1;
@@ -252,7 +253,7 @@ int64_t kv_len_of(const int32_t* kv_indptr, const int32_t* kv_last, int b, int P
 }
 
 // Decode work with the split turned off (pkv_plan_set_split_kv): every
-// (request, kv head) page list whole on one of `W` workers (warps of W / 8
+// (request, kv head) page list whole on one of `W` workers (warps of W / cta_warps
 // CTAs), longest first onto the least-loaded worker.  Ties go to the earlier
 // list, and between workers to the lower rank, rank r being warp r / C of CTA
 // r % C over C CTAs: so equal loads fill one warp on every SM before a second
@@ -263,8 +264,8 @@ pkv_status compute_decode_whole(pkv_plan* pl, int batch, const int32_t* kv_indpt
   const int hkv = pl->p.num_kv_heads;
   const int lists = batch * hkv;  // list i is request i / hkv, kv head i % hkv
   if (lists > pl->max_work) return PKV_ERR_WORKSPACE;
-  const int ctas = std::max(1, W / pkv::kDecodeWarps);
-  auto worker_of_rank = [&](int r) { return (r % ctas) * pkv::kDecodeWarps + r / ctas; };
+  const int cw = pl->cta_warps, ctas = std::max(1, W / cw);
+  auto worker_of_rank = [&](int r) { return (r % ctas) * cw + r / ctas; };
   auto pages = [&](int i) { return kv_indptr[i / hkv + 1] - kv_indptr[i / hkv]; };
   PlanScratch& sc = pl->scratch;
   std::vector<int>& order = sc.order;
@@ -354,6 +355,7 @@ pkv_status compute_decode_whole(pkv_plan* pl, int batch, const int32_t* kv_indpt
 // -> 167.7 us, the Llama-3-8B decode step 6160 -> 6178 GB/s.
 constexpr int64_t kPageCost = 8;
 constexpr int64_t kSegCost = 1 * kPageCost;
+constexpr int32_t kWholeSlack8 = 96;  // tokens
 pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, const int32_t* kv_last,
                           uint8_t* host, const int32_t* qo_indptr = nullptr, int W = 0) {
   const int P = pl->p.page_size;
@@ -380,7 +382,11 @@ pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, con
     // one page: 8.2 us against 16.4 us).
     int32_t longest = 0;
     for (int b = 0; b < batch; ++b) longest = std::max(longest, kv_indptr[b + 1] - kv_indptr[b]);
-    if (longest <= run) return compute_decode_whole(pl, batch, kv_indptr, kv_last, host, W);
+    // Over the 8-bit cache a warp streams 16 tokens in about 0.2 us and a split costs
+    // its pieces' setup and the merge's work, so lists up to 96 tokens longer than a run
+    // stay whole too (64 x 8 lists of 128 tokens: 9.1 us against 10.7 us).
+    const int32_t slack = pl->kv8 ? kWholeSlack8 / P : 0;
+    if (longest <= run + slack) return compute_decode_whole(pl, batch, kv_indptr, kv_last, host, W);
   }
 
   auto* hdr = reinterpret_cast<PlanHeader*>(host + pl->L.header);
@@ -472,7 +478,7 @@ pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, con
   // so a batch that fills only some of the workers still spreads them over every
   // SM instead of packing eight to an SM.  Segments are regrouped by worker.
   int n_workers = active;
-  const int C = W / pkv::kDecodeWarps;
+  const int C = W / pl->cta_warps;
   if (C > 1 && active > 0) {
     PlanScratch& sc = pl->scratch;
     sc.dsegs.assign(segs, segs + n_seg);
@@ -481,7 +487,7 @@ pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, con
     int k = 0;
     wptr[0] = 0;
     for (int w = 0; w < W; ++w) {
-      const int r = (w % pkv::kDecodeWarps) * C + w / pkv::kDecodeWarps;  // the run of worker w
+      const int r = (w % pl->cta_warps) * C + w / pl->cta_warps;  // the run of worker w
       if (r < active) {
         for (int i = sc.run_ptr[r]; i < sc.run_ptr[r + 1]; ++i) segs[k++] = sc.dsegs[i];
         n_workers = w + 1;
