@@ -513,7 +513,8 @@ typedef struct {
  *               have no part in where a token is stored.
  * q_in, q_out : both NULL or neither.
  * The frequencies are held in double precision and the angles computed modulo a turn
- * in 64-bit fixed point, without a rounding for any int32 position.  Errors: as pkv_append_paged_kv; PKV_ERR_INVALID_ARG also for a rotation
+ * in 64-bit fixed point, without a rounding for any int32 position.  As there, no two
+ * new tokens may have the same slot.  Errors: as pkv_append_paged_kv; PKV_ERR_INVALID_ARG also for a rotation
  * out of the ranges above.  Tokens named wrongly by the device arrays are skipped
  * and flagged in error_d as there.
  */

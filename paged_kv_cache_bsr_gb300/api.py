@@ -496,9 +496,10 @@ class Plan:
         plan_run(self.handle, batch, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h, num_pages,
                  self.dev_ws, self.host_ws, stream)
         self.num_pages = int(num_pages)
-        self.batch = batch
-        self.total_q = batch if qo_indptr_h is None else int(torch.as_tensor(qo_indptr_h)[-1])
-        self.kv_pages = int(torch.as_tensor(kv_indptr_h)[-1])
+        if self.kind in (PLAN_DECODE_KV8, PLAN_PREFILL_KV8):  # what run() checks its tensors against
+            self.batch = batch
+            self.total_q = batch if self.kind == PLAN_DECODE_KV8 else int(torch.as_tensor(qo_indptr_h)[-1])
+            self.kv_pages = int(torch.as_tensor(kv_indptr_h)[-1])
 
     def _check_kv8(self, q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, qo_indptr) -> None:
         """The tensors of a run over the 8-bit cache against what the last plan() named."""
