@@ -151,10 +151,10 @@ def _ptr(t: Optional[torch.Tensor]):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream(stream) -> ctypes.c_void_p:
+def _stream(stream):
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -394,7 +394,7 @@ def append_paged_kv_axes(params: Params, rope: Optional[RopeAxes], append_indptr
     if kv_data.shape[1:] != (2, params.num_kv_heads, params.page_size, params.head_dim) or \
             kv_data.dtype is not k_new.dtype:
         raise ValueError("kv_data must be [num_pages, 2, num_kv_heads, page_size, head_dim] of the params' dtype")
-    _check(load().pkv_append_paged_kv_axes(
+    _check((_lib or load()).pkv_append_paged_kv_axes(
         ctypes.byref(params), None if rope is None else ctypes.byref(rope), batch, nnz, kv_data.shape[0],
         *_ptrs((append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv_data, q_in, q_out,
                 error)), _stream(stream)), "pkv_append_paged_kv_axes")
@@ -409,7 +409,7 @@ def append_paged_kv8(params: Params, rope: Optional[RopeAxes], append_indptr, kv
     batch, nnz = _append_tensors(params, rope, append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new,
                                  v_new, q_in, q_out, error)
     _kv8_tensors(params, kv8, kv8_scales)
-    _check(load().pkv_append_paged_kv8(
+    _check((_lib or load()).pkv_append_paged_kv8(
         ctypes.byref(params), None if rope is None else ctypes.byref(rope), batch, nnz, kv8.shape[0],
         *_ptrs((append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, k_new, v_new, kv8, kv8_scales, q_in,
                 q_out, error)), _stream(stream)), "pkv_append_paged_kv8")
@@ -418,7 +418,7 @@ def append_paged_kv8(params: Params, rope: Optional[RopeAxes], append_indptr, kv
 def batch_decode_paged_kv8(h, q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws,
                            stream=None) -> None:
     """Decode over the 8-bit cache, on a plan of kind PLAN_DECODE_KV8."""
-    _check(load().pkv_batch_decode_paged_kv8(
+    _check((_lib or load()).pkv_batch_decode_paged_kv8(
         h, *_ptrs((q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws)), _stream(stream)),
         "pkv_batch_decode_paged_kv8")
 
@@ -426,7 +426,7 @@ def batch_decode_paged_kv8(h, q, kv8, kv8_scales, kv_indices, kv_indptr, kv_last
 def batch_prefill_paged_kv8(h, q, qo_indptr, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws,
                             stream=None) -> None:
     """Prefill over the 8-bit cache, on a plan of kind PLAN_PREFILL_KV8."""
-    _check(load().pkv_batch_prefill_paged_kv8(
+    _check((_lib or load()).pkv_batch_prefill_paged_kv8(
         h, *_ptrs((q, qo_indptr, kv8, kv8_scales, kv_indices, kv_indptr, kv_last_page_len, o, lse, dev_ws)),
         _stream(stream)), "pkv_batch_prefill_paged_kv8")
 

@@ -107,18 +107,39 @@ __device__ __forceinline__ void sincos_turn(int32_t pos, uint64_t freq, float& s
   c = ((quad + 1u) & 2u) ? -b : b;
 }
 
-// A pair turned in double precision, each element rounded to a float by truncation
-// with the lost part in its last bit, so that rounding the float to e4m3 rounds the
-// double's value correctly.
+// A pair turned in double precision (quadrant and rest of the 64-bit turn as above, the
+// Taylor series to x^17 and x^18: remainders below 2^-60), each element rounded to a
+// float by truncation with the lost part in its last bit, so that rounding the float to
+// e4m3 rounds the double's value correctly.
 __device__ __noinline__ float2 turn_pair_double(float x, float y, int32_t pos, uint64_t freq) {
-  const int64_t turn = static_cast<int64_t>(static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq);
-  double s, c;
-  sincospi(static_cast<double>(turn) * 1.0842021724855044e-19, &s, &c);  // 2^-63: half turns
-  const double v[2] = {x * c - y * s, y * c + x * s};
+  const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * freq;
+  const uint64_t quad = (turn + (uint64_t{1} << 61)) >> 62;
+  const double a = static_cast<double>(static_cast<int64_t>(turn - (quad << 62))) * 3.4061215800865545e-19;  // 2 pi / 2^64
+  const double z = a * a;
+  double ps = 1.0 / 355687428096000.0, pc = -1.0 / 6402373705728000.0;  // 1/17!, 1/18!
+  ps = fma(z, ps, -1.0 / 1307674368000.0);
+  pc = fma(z, pc, 1.0 / 20922789888000.0);
+  ps = fma(z, ps, 1.0 / 6227020800.0);
+  pc = fma(z, pc, -1.0 / 87178291200.0);
+  ps = fma(z, ps, -1.0 / 39916800.0);
+  pc = fma(z, pc, 1.0 / 479001600.0);
+  ps = fma(z, ps, 1.0 / 362880.0);
+  pc = fma(z, pc, -1.0 / 3628800.0);
+  ps = fma(z, ps, -1.0 / 5040.0);
+  pc = fma(z, pc, 1.0 / 40320.0);
+  ps = fma(z, ps, 1.0 / 120.0);
+  pc = fma(z, pc, -1.0 / 720.0);
+  ps = fma(z, ps, -1.0 / 6.0);
+  pc = fma(z, pc, 1.0 / 24.0);
+  pc = fma(z, pc, -0.5);
+  const double sa = fma(a * z, ps, a), ca = fma(z, pc, 1.0);
+  const double u = (quad & 1) ? ca : sa, v = (quad & 1) ? sa : ca;
+  const double s = (quad & 2) ? -u : u, c = ((quad + 1) & 2) ? -v : v;
+  const double w[2] = {x * c - y * s, y * c + x * s};
   float r[2];
   for (int i = 0; i < 2; ++i) {
-    r[i] = __double2float_rz(v[i]);
-    if (static_cast<double>(r[i]) != v[i]) r[i] = __uint_as_float(__float_as_uint(r[i]) | 1u);
+    r[i] = __double2float_rz(w[i]);
+    if (static_cast<double>(r[i]) != w[i]) r[i] = __uint_as_float(__float_as_uint(r[i]) | 1u);
   }
   return make_float2(r[0], r[1]);
 }
