@@ -356,6 +356,127 @@ pkv_status compute_decode_whole(pkv_plan* pl, int batch, const int32_t* kv_indpt
 constexpr int64_t kPageCost = 8;
 constexpr int64_t kSegCost = 1 * kPageCost;
 constexpr int32_t kWholeSlack8 = 96;  // tokens
+// The header, the counts and the inspection rows of a decode plan whose tables are
+// written: `n_workers` workers, `active` of them with work.
+void finish_decode(pkv_plan* pl, int batch, uint8_t* host, int n_workers, int active, int n_seg, int n_merge,
+                   int n_slot, int64_t total) {
+  auto* hdr = reinterpret_cast<PlanHeader*>(host + pl->L.header);
+  const auto* wptr = reinterpret_cast<const int32_t*>(host + pl->L.worker_ptr);
+  const auto* segs = reinterpret_cast<const DecodeSeg*>(host + pl->L.segs);
+  std::memset(hdr, 0, sizeof(PlanHeader));
+  hdr->kind = PKV_PLAN_DECODE;
+  hdr->batch = batch;
+  hdr->num_workers = n_workers;  // workers below this with no run return at once
+  hdr->num_segments = n_seg;
+  hdr->num_merge = n_merge;
+  hdr->num_slots = n_slot;
+
+  pl->active_workers = active;
+  pl->num_work = n_seg;
+  pl->num_merge = n_merge;
+  pl->num_slots = n_slot;
+  pl->total_cost = total;
+  pl->max_cost = 0;
+  pl->work_rows.assign((size_t)n_seg * 8, 0);
+  for (int w = 0; w < n_workers; ++w) {
+    int64_t cost = 0;
+    for (int i = wptr[w]; i < wptr[w + 1]; ++i) {
+      const DecodeSeg& s = segs[i];
+      int32_t* r = &pl->work_rows[(size_t)i * 8];
+      r[0] = w; r[1] = s.b; r[2] = s.kvh; r[3] = s.page_begin; r[4] = s.n_pages;
+      r[5] = s.last_rows; r[6] = s.slot; r[7] = 0;
+      cost += s.n_pages;
+    }
+    pl->max_cost = std::max(pl->max_cost, cost);
+  }
+  pl->used_bytes = pl->L.segs + sizeof(DecodeSeg) * (size_t)n_seg;
+}
+
+// Decode over the 8-bit cache with the heads in step: the requests' pages are cut into
+// W / Hkv runs of equal cost (as compute_decode cuts the lists), and run k is taken by
+// Hkv workers at the same time, one per kv head.  A page's heads are neighbours in
+// memory, and heads read far apart in time open its DRAM rows once each: with lists
+// cut head by head a batch on one-row pages (128 bytes a head) ran at 73 % of measured
+// HBM bandwidth.
+pkv_status compute_decode_heads(pkv_plan* pl, int batch, const int32_t* kv_indptr, const int32_t* kv_last,
+                                uint8_t* host, int W) {
+  const int hkv = pl->p.num_kv_heads, G = W / hkv;  // G runs
+  auto* wptr = reinterpret_cast<int32_t*>(host + pl->L.worker_ptr);
+  auto* merge = reinterpret_cast<MergeItem*>(host + pl->L.merge);
+  auto* segs = reinterpret_cast<DecodeSeg*>(host + pl->L.segs);
+  PlanScratch& sc = pl->scratch;
+  std::vector<DecodeSeg>& pieces = sc.dsegs;  // head 0's, in run order; slot: head 0's slot or -1
+  std::vector<int32_t>& run_of = sc.run_ptr;
+  std::vector<int>& stride = sc.start;        // slots from a head's piece to the next head's
+  pieces.clear();
+  run_of.clear();
+  stride.clear();
+  const int64_t total = kv_indptr[batch];
+  const int64_t T = std::max<int64_t>(kSegCost + kPageCost,
+                                      ceil_div(total * kPageCost + kSegCost * (batch + G - 1), G));
+  int64_t X = 0;
+  int n_merge = 0, n_slot = 0, runs = 0;
+  for (int b = 0; b < batch; ++b) {
+    const int32_t n = kv_indptr[b + 1] - kv_indptr[b];
+    const size_t first = pieces.size();
+    int32_t lo = 0;
+    do {
+      DecodeSeg s{};
+      s.b = b;
+      s.q_row = b;
+      s.page_begin = lo;
+      s.idx_begin = kv_indptr[b] + lo;
+      s.slot = -1;
+      int64_t r = std::min<int64_t>(X / T, G - 1);
+      if (n > 0) {
+        X += kSegCost;
+        r = std::min<int64_t>((X + kPageCost / 2) / T, G - 1);
+        const int64_t room = (r + 1) * T - X - kPageCost / 2;  // > 0: this page's midpoint is in run r
+        s.n_pages = r == G - 1 ? n - lo : static_cast<int32_t>(std::min<int64_t>(n - lo, ceil_div(room, kPageCost)));
+        X += static_cast<int64_t>(s.n_pages) * kPageCost;
+        lo += s.n_pages;
+        s.last_rows = lo == n ? kv_last[b] : pl->p.page_size;
+      }
+      pieces.push_back(s);
+      run_of.push_back(static_cast<int32_t>(r));
+      runs = std::max(runs, static_cast<int>(r) + 1);
+    } while (lo < n);
+    const int parts = static_cast<int>(pieces.size() - first);
+    stride.resize(pieces.size(), parts);
+    if (parts == 1) continue;
+    if (n_merge + hkv > pl->max_merge || n_slot + parts * hkv > pl->max_slots) return PKV_ERR_WORKSPACE;
+    for (int i = 0; i < parts; ++i) pieces[first + i].slot = n_slot + i;
+    for (int h = 0; h < hkv; ++h, n_slot += parts) merge[n_merge++] = MergeItem{b, h, n_slot, parts};
+  }
+  const int64_t n_seg64 = static_cast<int64_t>(pieces.size()) * hkv;
+  if (n_seg64 > pl->max_work) return PKV_ERR_WORKSPACE;
+  // First piece of each run (runs without pieces repeat the next one's).
+  std::vector<int>& from = sc.fill;
+  from.assign(static_cast<size_t>(runs) + 1, 0);
+  for (int32_t r : run_of) ++from[static_cast<size_t>(r) + 1];
+  for (int k = 0; k < runs; ++k) from[static_cast<size_t>(k) + 1] += from[k];
+  // (run, head) pair q goes to warp q / C of CTA q % C, over C CTAs.
+  const int cw = pl->cta_warps, C = std::max(1, W / cw), active = runs * hkv;
+  int k = 0, n_workers = 0;
+  wptr[0] = 0;
+  for (int w = 0; w < W && k < static_cast<int>(n_seg64); ++w) {
+    const int q = (w % cw) * C + w / cw;
+    if (q < active) {
+      const int run = q / hkv, h = q % hkv;
+      for (int i = from[run]; i < from[run + 1]; ++i) {
+        DecodeSeg s = pieces[i];
+        s.kvh = h;
+        if (s.slot >= 0) s.slot += h * stride[i];
+        segs[k++] = s;
+      }
+    }
+    wptr[w + 1] = k;
+    n_workers = w + 1;
+  }
+  finish_decode(pl, batch, host, n_workers, active, k, n_merge, n_slot, total * hkv);
+  return PKV_OK;
+}
+
 pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, const int32_t* kv_last,
                           uint8_t* host, const int32_t* qo_indptr = nullptr, int W = 0) {
   const int P = pl->p.page_size;
@@ -389,7 +510,9 @@ pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, con
     if (longest <= run + slack) return compute_decode_whole(pl, batch, kv_indptr, kv_last, host, W);
   }
 
-  auto* hdr = reinterpret_cast<PlanHeader*>(host + pl->L.header);
+  // In step as long as the runs' heads fill the workers to a twentieth.
+  if (pl->kv8 && (W % hkv) * 20 <= W) return compute_decode_heads(pl, batch, kv_indptr, kv_last, host, W);
+
   auto* wptr = reinterpret_cast<int32_t*>(host + pl->L.worker_ptr);
   auto* merge = reinterpret_cast<MergeItem*>(host + pl->L.merge);
   auto* segs = reinterpret_cast<DecodeSeg*>(host + pl->L.segs);
@@ -497,33 +620,7 @@ pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, con
     }
   }
 
-  std::memset(hdr, 0, sizeof(PlanHeader));
-  hdr->kind = PKV_PLAN_DECODE;
-  hdr->batch = batch;
-  hdr->num_workers = n_workers;  // workers below this with no run return at once
-  hdr->num_segments = n_seg;
-  hdr->num_merge = n_merge;
-  hdr->num_slots = n_slot;
-
-  pl->active_workers = active;
-  pl->num_work = n_seg;
-  pl->num_merge = n_merge;
-  pl->num_slots = n_slot;
-  pl->total_cost = total;
-  pl->max_cost = 0;
-  pl->work_rows.assign((size_t)n_seg * 8, 0);
-  for (int w = 0; w < n_workers; ++w) {
-    int64_t cost = 0;
-    for (int i = wptr[w]; i < wptr[w + 1]; ++i) {
-      const DecodeSeg& s = segs[i];
-      int32_t* r = &pl->work_rows[(size_t)i * 8];
-      r[0] = w; r[1] = s.b; r[2] = s.kvh; r[3] = s.page_begin; r[4] = s.n_pages;
-      r[5] = s.last_rows; r[6] = s.slot; r[7] = 0;
-      cost += s.n_pages;
-    }
-    pl->max_cost = std::max(pl->max_cost, cost);
-  }
-  pl->used_bytes = pl->L.segs + sizeof(DecodeSeg) * (size_t)n_seg;
+  finish_decode(pl, batch, host, n_workers, active, n_seg, n_merge, n_slot, total);
   return PKV_OK;
 }
 

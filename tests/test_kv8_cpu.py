@@ -219,3 +219,70 @@ def test_the_binding_refuses_tensors_that_do_not_fit(lib):
         api.append_paged_kv_axes(params, r, i(3), i(3), i(4), i(2), None, rows(5, 2), rows(5, 2), torch.zeros(4, 2, 2, 16, 128))
     with pytest.raises(ValueError):
         api.make_rope_axes(1e4, 128, [1, 2, 3, 4, 5])
+
+
+# --------------------------------------------------------------------------- decode plans with the heads in step
+def table(kv_lens, P):
+    counts = [(n + P - 1) // P for n in kv_lens]
+    indptr = torch.tensor([0] + list(np.cumsum(counts)), dtype=torch.int32)
+    last = torch.tensor([n - (c - 1) * P if c else 0 for n, c in zip(kv_lens, counts)], dtype=torch.int32)
+    return counts, indptr, last
+
+
+@pytest.mark.parametrize("hkv", [1, 2, 3, 5, 8, 16, 100, 700])
+@pytest.mark.parametrize("P,seed", [(1, 0), (16, 1), (5, 2), (64, 3)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_decode_kv8_plan(lib, hkv, P, seed, d):
+    gen = np.random.default_rng(seed)
+    top = 1200 if hkv <= 16 else 40
+    kv_lens = [0, 1] + [int(x) for x in gen.integers(1, top, size=20)] + [8 * top, 0, P, 17]
+    counts, indptr, last = table(kv_lens, P)
+    B = len(kv_lens)
+    params = api.make_params(2 * hkv, hkv, d, P, torch.bfloat16, 0.1)
+    h = make(api.PLAN_DECODE_KV8, params, api.Limits(B, B, int(indptr[-1])))
+    _, host = api.plan_workspace_bytes(h)
+    raw = torch.zeros(host + 64, dtype=torch.uint8)
+    ws = raw[(-raw.data_ptr()) % 64:][:host]
+    api.plan_compute(h, B, None, indptr, None, last, int(indptr[-1]) + 1, ws)
+    info, work = api.plan_get_info(h), api.plan_get_work(h).tolist()
+    W = info.workers
+    assert W == 152 * (16 if d == 64 else 8)
+    covered, slots, empty, load = set(), set(), {}, {}
+    for w, b, kvh, p0, n, rows, slot, _ in work:
+        assert 0 <= w < W and 0 <= kvh < hkv
+        for p in range(p0, p0 + n):
+            assert (b, kvh, p) not in covered
+            covered.add((b, kvh, p))
+        load[w] = load.get(w, 0) + n
+        if n:
+            assert rows == (int(last[b]) if p0 + n == counts[b] else P)
+        else:
+            empty[b] = empty.get(b, 0) + 1
+        if slot >= 0:
+            assert slot not in slots
+            slots.add(slot)
+    assert len(covered) == sum(counts) * hkv
+    assert empty == {b: hkv for b, c in enumerate(counts) if c == 0}
+    assert len(slots) == info.num_slots and slots == set(range(info.num_slots))
+    assert [r[0] for r in work] == sorted(r[0] for r in work)
+    # the slots of one (request, head) are neighbours in page order: the merge reads them as one range
+    by = {}
+    for w, b, kvh, p0, n, rows, slot, _ in work:
+        if slot >= 0:
+            by.setdefault((b, kvh), []).append((p0, slot))
+    for pieces in by.values():
+        s = [x for _, x in sorted(pieces)]
+        assert len(s) > 1 and s == list(range(s[0], s[0] + len(s)))
+    assert len(by) == info.num_merge
+    if (W % hkv) * 20 <= W:
+        # every head has the same pieces, a page's heads sit in consecutive runs, and no run is longer than its share
+        cw = W // 152
+        run = lambda w: (w % cw) * 152 + w // cw
+        cuts = [{(b, p0, n) for _, b, kvh, p0, n, _, _, _ in work if kvh == x} for x in range(hkv)]
+        assert all(c == cuts[0] for c in cuts)
+        at = {(b, p0, kvh): run(w) for w, b, kvh, p0, n, _, _, _ in work}
+        assert all(r == at[(b, p0, 0)] + kvh and at[(b, p0, 0)] % hkv == 0 for (b, p0, kvh), r in at.items())
+        G = W // hkv
+        T = max(16, -(-(8 * sum(counts) + 8 * (B + G - 1)) // G))
+        assert max(load.values()) <= -(-T // 8)
+    api.plan_destroy(h)
