@@ -275,9 +275,17 @@ def test_decode_kv8_plan(lib, hkv, P, seed, d):
         assert len(s) > 1 and s == list(range(s[0], s[0] + len(s)))
     assert len(by) == info.num_merge
     if (W % hkv) * 20 <= W:
-        # every head has the same pieces, a page's heads sit in consecutive runs, and no run is longer than its share
+        # every head has the same pieces, a run's heads are neighbours (small pages: warps of one CTA where they
+        # divide its warps), and no run is longer than its share
         cw = W // 152
-        run = lambda w: (w % cw) * 152 + w // cw
+        if P < 16 and cw % hkv == 0:
+            ctas = {}
+            for w, b, kvh, p0, n, _, _, _ in work:
+                ctas.setdefault((b, p0), set()).add(w // cw)
+            assert all(len(c) == 1 for c in ctas.values())
+            run = lambda w: ((w % cw) // hkv * 152 + w // cw) * hkv + w % cw % hkv
+        else:
+            run = lambda w: (w % cw) * 152 + w // cw
         cuts = [{(b, p0, n) for _, b, kvh, p0, n, _, _, _ in work if kvh == x} for x in range(hkv)]
         assert all(c == cuts[0] for c in cuts)
         at = {(b, p0, kvh): run(w) for w, b, kvh, p0, n, _, _, _ in work}
