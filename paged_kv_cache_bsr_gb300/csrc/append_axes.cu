@@ -531,7 +531,7 @@ pkv_status append_axes(const pkv_params* p, const pkv_rope_axes* rope, int batch
   a.kv_indptr = kv_indptr_d;
   a.kv_indices = kv_indices_d;
   a.kv_last = kv_last_page_len_d;
-  a.positions = positions_d;
+  a.positions = rope ? positions_d : nullptr;
   a.k_new = k_new;
   a.v_new = v_new;
   a.kv = kv;

@@ -472,3 +472,100 @@ def test_the_full_serving_batch():
     """The Llama-3-8B-shaped decode batch over the 8-bit cache (sampled rows against the oracle)."""
     b = W.llama3_decode(seed=1001, batch=24)
     check_attention(b, spread=1)
+
+
+def test_a_pool_past_4_gib():
+    """Pages at the end of a pool of more than 2^32 bytes: append, decode and prefill there."""
+    hq, hkv, P, D = 8, 8, 128, 128
+    n_pages = 17000                                  # 4.46 GB of codes
+    cache = runner.Kv8Cache.zeros(n_pages, hkv, P, D)
+    assert cache.codes.numel() > 1 << 32
+    b = batch([130, 40], [300, 40], hq=hq, hkv=hkv, P=P, seed=80, causal=True, extra=0)
+    far = n_pages - b.num_pages
+    k_new, v_new = W.new_kv_rows(b, seed=81)
+    small, twin = quantised(b, 1, poison=False)
+    cache.codes.view(torch.uint8)[far:].copy_(small.codes.view(torch.uint8))
+    cache.scales[far:].copy_(small.scales)
+    shifted = dataclasses.replace(b, kv_indices=b.kv_indices + far)
+    db = runner.DeviceBatch.from_host(shifted, kv_data=torch.empty(0))
+    rope = api.make_rope_axes(1e4, 128, [64])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    db.q = runner.append_kv8(db, cache, k_new.cuda(), v_new.cuda(), rope, error=err)
+    o, lse = runner.prefill_kv8(db, cache)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0 and int(cache.codes.view(torch.uint8)[:far].max()) == 0
+    tail = runner.Kv8Cache(cache.codes.view(torch.uint8)[far:].view(torch.float8_e4m3fn), cache.scales[far:])
+    ref = serving_reference(dataclasses.replace(b, q=db.q.cpu()), tail)
+    assert_attention(o, lse, ref, P_EPS["prefill"][BF], "prefill")
+    d = dataclasses.replace(shifted, qo_indptr=torch.tensor([0, 1, 2], dtype=torch.int32), qo_lens=[1, 1], q=b.q[:2], causal=False)
+    o, lse = runner.decode_kv8(runner.DeviceBatch.from_host(d, kv_data=torch.empty(0)), cache)
+    torch.cuda.synchronize()
+    assert_attention(o, lse, serving_reference(dataclasses.replace(d, kv_indices=b.kv_indices, kv_data=b.kv_data), tail),
+                     2.0 ** -11, "decode")
+    # the 16-bit append past 2^32 bytes
+    pool = torch.zeros(9000, 2, hkv, P, D, dtype=BF, device="cuda")
+    off = 9000 - b.num_pages
+    db16 = dataclasses.replace(db, kv_data=pool, kv_indices=(b.kv_indices + off).cuda(), q=b.q.cuda())
+    runner.append_kv_axes(db16, k_new.cuda(), v_new.cuda(), None, rotate_q=False)
+    page, slot = places(b)
+    torch.testing.assert_close(pool[off:][torch.from_numpy(page), 0, :, torch.from_numpy(slot)].cpu(), k_new, rtol=0, atol=0)
+    assert float(pool[:off].abs().max()) == 0
+
+
+def test_runs_refuse_tensors_that_do_not_fit_the_plan():
+    b = batch([1] * 3, [40, 100, 7], seed=82)
+    cache, _ = quantised(b)
+    c, db = to_cuda(cache), runner.DeviceBatch.from_host(b, kv_data=torch.empty(0))
+    plan = runner.make_plan(b, api.PLAN_DECODE_KV8)
+    runner.plan_batch(plan, b)
+    o, lse = torch.zeros_like(db.q), torch.zeros(3, 8, device="cuda")
+    good = dict(q=db.q, kv=c.codes, ix=db.kv_indices, ip=db.kv_indptr, la=db.kv_last_page_len, o=o, lse=lse, scales=c.scales)
+
+    def run(**kw):
+        a = {**good, **kw}
+        plan.run(a["q"], a["kv"], a["ix"], a["ip"], a["la"], a["o"], a["lse"], kv_scales=a["scales"])
+
+    for bad in (dict(scales=None), dict(q=db.q.half()), dict(q=db.q[:2]), dict(o=o[:, :4]), dict(lse=lse.half()),
+                dict(lse=lse[:2]), dict(kv=c.codes[:-1]), dict(kv=c.codes[:5], scales=c.scales[:5]), dict(scales=c.scales.int()),
+                dict(ix=db.kv_indices[:-1]), dict(ip=db.kv_indptr.long()), dict(la=db.kv_last_page_len[:2]),
+                dict(q=db.q.cpu()), dict(o=torch.zeros(3, 16, 128, dtype=BF, device="cuda")[:, ::2]), dict(lse=lse.cpu())):
+        with pytest.raises(ValueError):
+            run(**bad)
+    with pytest.raises(ValueError):
+        plan.run(db.q, c.codes, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o, lse, kv_scales=c.scales,
+                 mask=torch.zeros(4, dtype=torch.uint8, device="cuda"))
+    run(lse=None)
+    with pytest.raises(ValueError):   # the 16-bit cache's plan takes no scales
+        runner.make_plan(b, api.PLAN_DECODE).run(db.q, c.codes, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o,
+                                                 kv_scales=c.scales)
+    torch.cuda.synchronize()
+
+
+def test_two_streams_with_their_own_plans():
+    """Two steps of different batches on two streams at once, each with its plan and workspace."""
+    bs = [batch([1] * 8, list(np.random.default_rng(s).integers(1, 3000, size=8)), hq=16, hkv=4, seed=90 + s) for s in range(2)]
+    pairs = [quantised(b, 1, seed=s) for s, b in enumerate(bs)]
+    streams = [torch.cuda.Stream() for _ in bs]
+    jobs = []
+    for b, (cache, _), s in zip(bs, pairs, streams):
+        plan = runner.make_plan(b, api.PLAN_DECODE_KV8)
+        runner.plan_batch(plan, b, stream=s)
+        jobs.append((runner.DeviceBatch.from_host(b, kv_data=torch.empty(0)), to_cuda(cache), plan, s))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        outs = [runner.decode_kv8(db, c, plan, stream=s) for db, c, plan, s in jobs]
+    torch.cuda.synchronize()
+    for (o, lse), (_, twin) in zip(outs, pairs):
+        assert_attention(o, lse, twin, 2.0 ** -11)
+
+
+def test_the_same_call_twice_gives_the_same_bits():
+    b = batch([1] * 6, [9000, 3, 700, 64, 2000, 1], hq=8, hkv=1, seed=95)
+    cache, _ = quantised(b, 2)
+    c, db = to_cuda(cache), runner.DeviceBatch.from_host(b, kv_data=torch.empty(0))
+    plan = runner.make_plan(b, api.PLAN_DECODE_KV8)
+    runner.plan_batch(plan, b)
+    first = runner.decode_kv8(db, c, plan)
+    for _ in range(10):
+        again = runner.decode_kv8(db, c, plan)
+        assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
