@@ -198,7 +198,8 @@ pkv_status pkv_plan_get_info(const pkv_plan* plan, pkv_plan_info* info);
  * Copy the last computed work list, 8 int32 per entry, in worker order:
  *   decode:  {worker, b, kv_head, page_begin, n_pages, last_rows, slot, 0}
  *   prefill: {worker, b, kv_head, q_pos0, n_pos, kv_begin, kv_end, slot}
- * (slot = -1: the entry writes the final output itself).
+ * (slot = -1: the entry writes the final output itself; -2, on an 8-bit decode plan:
+ * it is joined with its list's other pieces, on the next warps of the same CTA).
  * *rows_written receives the number of entries (also when capacity is short,
  * in which case nothing is copied and PKV_ERR_WORKSPACE is returned).
  */

@@ -151,6 +151,16 @@ pkv::PackArgs read_packed_copy(const pkv_plan* plan, pkv::PrefillArgs& a, void* 
   return pk;
 }
 
+// Whether work on `s` may be going into a graph.
+bool maybe_capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusActive;
+  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+    cudaGetLastError();
+    return true;
+  }
+  return st != cudaStreamCaptureStatusNone;
+}
+
 pkv_status launch_status(cudaError_t e) {
   if (e == cudaSuccess) return PKV_OK;
   cudaGetLastError();
@@ -291,7 +301,10 @@ pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const
     e = pkv::launch_decode8(a, kv8_scales, p.sm_scale, p.head_dim, p.dtype, p.logits_cap > 0.f, plan->grid_ctas,
                             plan->num_pages, s);
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
-  if (e == cudaSuccess) e = pkv::launch_decode8_merge(a, p.head_dim, p.dtype, plan->merge_grid, s);
+  // A plan without split sequences leaves nothing to merge; a graph gets the launch all
+  // the same, for the plans it may be replayed with.
+  if (e == cudaSuccess && (plan->num_merge > 0 || maybe_capturing(s)))
+    e = pkv::launch_decode8_merge(a, p.head_dim, p.dtype, plan->merge_grid, s);
   if (e == cudaSuccess) e = release_tables(plan, s);
   return launch_status(e);
 }

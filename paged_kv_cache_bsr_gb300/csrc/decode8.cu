@@ -109,6 +109,9 @@ __device__ __forceinline__ uint32_t lds8(uint32_t a) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(a));
   return r;
 }
+__device__ __forceinline__ void sts128(uint32_t a, const float4& v) {
+  asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
 __device__ __forceinline__ void sts8(uint32_t a, uint32_t v) {
   asm volatile("st.shared.u8 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
@@ -409,8 +412,16 @@ __device__ __forceinline__ void tiles_step(const DecodeArgs& a, const uint32_t (
   }
 }
 
+// What a warp leaves for its CTA of a shared list's piece; its outputs are at the start
+// of its ring, [head][dim] in fp32.
+struct Shared8 {
+  float lse[8];  // -inf without a piece
+  int row, kvh;  // row: -1 without one
+};
+
 template <int D, typename T, bool CAP, PageMode MODE>
-__device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker, uint32_t rows0, uint32_t scales0) {
+__device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker, uint32_t rows0, uint32_t scales0,
+                                               Shared8& mine) {
   using S = Shape8<D, MODE>;
   constexpr int ST = S::kStages;
   constexpr int KC = D / 64;     // 16-byte chunks of a K row per lane (and of a 16-bit Q row, pairs of them)
@@ -535,7 +546,7 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
       if (head >= G) continue;
       const float f = empty ? 0.f : exp2f(st.R[h] - 7.f) / lh;
       const float lse_v = empty ? -INFINITY : (st.m[h] + log2f(lh)) * kLn2;
-      if (sg.slot < 0) {
+      if (sg.slot == -1) {
         const int64_t orow = static_cast<int64_t>(sg.q_row) * a.num_qo_heads + hq0 + head;
         T* dst = static_cast<T*>(a.o) + orow * D + g * (D / 8);
 #pragma unroll
@@ -549,6 +560,17 @@ __device__ __forceinline__ void decode8_worker(const Decode8Args& a8, int worker
           *reinterpret_cast<uint4*>(dst + 2 * i) = from_float8<T>(v);
         }
         if (g == 0 && a.lse) a.lse[orow] = lse_v;
+      } else if (sg.slot == kSharedSlot) {
+        // The warp's copies have all arrived and been read: its ring is free.
+        const uint32_t dst = rows0 + (head * D + g * (D / 8)) * 4;
+#pragma unroll
+        for (int i = 0; i < KS; i += 2)
+          sts128(dst + 8 * i, make_float4(st.o[i][h] * f, st.o[i][2 + h] * f, st.o[i + 1][h] * f, st.o[i + 1][2 + h] * f));
+        if (g == 0) mine.lse[head] = lse_v;
+        if (g == 0 && head == 0) {
+          mine.row = sg.q_row;
+          mine.kvh = sg.kvh;
+        }
       } else {
         const int64_t prow = static_cast<int64_t>(sg.slot) * G + head;
         float* dst = a.part_o + prow * D + g * (D / 8);
@@ -569,11 +591,46 @@ __global__ void __launch_bounds__(decode8_warps(D) * 32, 1) decode8_kernel(const
   // Launched as a programmatic dependent of the kernel before it on the stream:
   // nothing global is touched before that grid has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int warp = threadIdx.x >> 5;
-  const uint32_t base = smem_addr(smem);
   constexpr int W = S::kWarps;
-  decode8_worker<D, T, CAP, MODE>(a, blockIdx.x * W + warp, base + warp * (S::kStages * 2 * S::kTile),
-                                 base + W * (S::kStages * 2 * S::kTile) + warp * (S::kStages * S::kScales));
+  __shared__ Shared8 shared[W];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int share = a.d.hdr->share;
+  if (lane < 8) shared[warp].lse[lane] = -INFINITY;
+  if (lane == 0) shared[warp].row = -1;
+  __syncwarp();
+  const uint32_t base = smem_addr(smem);
+  constexpr uint32_t kRing = S::kStages * 2 * S::kTile;
+  decode8_worker<D, T, CAP, MODE>(a, blockIdx.x * W + warp, base + warp * kRing,
+                                  base + W * kRing + warp * (S::kStages * S::kScales), shared[warp]);
+  if (share <= 1) return;
+  // Lists shared by `share` neighbouring warps: each of them joins some of the heads.
+  __syncthreads();
+  constexpr int PER = D / 32;  // dims per lane
+  const int first = warp / share * share;
+  const int row = shared[first].row;  // the first piece exists where any does
+  if (row < 0) return;
+  const int G = a.d.num_qo_heads / a.d.num_kv_heads;
+  for (int head = warp - first; head < G; head += share) {
+    float m = -INFINITY;
+    for (int k = 0; k < share; ++k) m = fmaxf(m, shared[first + k].lse[head]);
+    float l = 0.f, acc[PER];
+#pragma unroll
+    for (int v = 0; v < PER; ++v) acc[v] = 0.f;
+    for (int k = 0; k < share; ++k) {
+      const float w = fast_exp2((shared[first + k].lse[head] - m) * kLog2e);
+      if (w == 0.f) continue;  // no piece (its ring holds anything), or nothing to add
+      l += w;
+      const float* o = reinterpret_cast<const float*>(smem + (first + k) * kRing) + head * D + lane * PER;
+#pragma unroll
+      for (int v = 0; v < PER; ++v) acc[v] = fmaf(w, o[v], acc[v]);
+    }
+    const int64_t orow = static_cast<int64_t>(row) * a.d.num_qo_heads + shared[first].kvh * G + head;
+    T* dst = static_cast<T*>(a.d.o) + orow * D + lane * PER;
+    const float inv = 1.f / l;
+#pragma unroll
+    for (int v = 0; v < PER; v += 2) *reinterpret_cast<uint32_t*>(dst + v) = pack2<T>(acc[v] * inv, acc[v + 1] * inv);
+    if (lane == 0 && a.d.lse) a.d.lse[orow] = m + logf(l);
+  }
 }
 
 // The merge of split sequences, as decode_merge_pair computes it, with the slots of one

@@ -35,9 +35,14 @@ struct alignas(64) PlanHeader {
                          // that serves it (CTAs below it serve the prefill half); 0 otherwise
   int32_t num_packed;    // prefill plans on pages of fewer than 8 rows: 16-row pages in the
                          // packed copy of the requests' K/V (0 otherwise)
-  int32_t pad[3];
+  int32_t share;         // 8-bit decode plans: warps of a CTA that share a page list (each list's
+                         // pieces on neighbouring warps, joined in the CTA); 0 or 1: none
+  int32_t pad[2];
 };
 static_assert(sizeof(PlanHeader) == 64, "PlanHeader layout");
+
+// A piece of a list that its CTA's warps share (PlanHeader::share).
+constexpr int32_t kSharedSlot = -2;
 
 // One contiguous run of one (request, kv head)'s pages, handled by one decode
 // worker.  slot < 0: the run is the whole sequence and writes the output
@@ -49,7 +54,7 @@ struct alignas(32) DecodeSeg {
   int32_t n_pages;     // pages in the run (0: empty request, write o = 0, lse = -inf)
   int32_t last_rows;   // valid slots of the run's final page
   int32_t page_begin;  // position of the run's first page in the request
-  int32_t slot;        // partial slot, or -1
+  int32_t slot;        // partial slot, -1, or (8-bit decode) kSharedSlot
   int32_t q_row;       // row of q / o / lse (the request itself in a decode batch; its
                        // qo_indptr entry in a mixed prefill + decode batch)
 };

@@ -355,7 +355,7 @@ pkv_status compute_decode_whole(pkv_plan* pl, int batch, const int32_t* kv_indpt
 // -> 167.7 us, the Llama-3-8B decode step 6160 -> 6178 GB/s.
 constexpr int64_t kPageCost = 8;
 constexpr int64_t kSegCost = 1 * kPageCost;
-constexpr int32_t kWholeSlack8 = 96;  // tokens
+constexpr int32_t kShareSlack8 = 96;  // tokens
 // The header, the counts and the inspection rows of a decode plan whose tables are
 // written: `n_workers` workers, `active` of them with work.
 void finish_decode(pkv_plan* pl, int batch, uint8_t* host, int n_workers, int active, int n_seg, int n_merge,
@@ -390,6 +390,47 @@ void finish_decode(pkv_plan* pl, int batch, uint8_t* host, int n_workers, int ac
     pl->max_cost = std::max(pl->max_cost, cost);
   }
   pl->used_bytes = pl->L.segs + sizeof(DecodeSeg) * (size_t)n_seg;
+}
+
+// Decode over the 8-bit cache with every page list shared by `share` (a power of two)
+// neighbouring warps of one CTA, which join their states themselves: nothing is left
+// for the merge.  List i takes warps (i / C) share .. of CTA i % C, over C CTAs.
+pkv_status compute_decode_shared(pkv_plan* pl, int batch, const int32_t* kv_indptr, const int32_t* kv_last,
+                                 uint8_t* host, int W, int share) {
+  const int hkv = pl->p.num_kv_heads, lists = batch * hkv, cw = pl->cta_warps, C = W / cw;
+  auto* wptr = reinterpret_cast<int32_t*>(host + pl->L.worker_ptr);
+  auto* segs = reinterpret_cast<DecodeSeg*>(host + pl->L.segs);
+  int k = 0, active = 0, n_workers = 0;
+  wptr[0] = 0;
+  for (int w = 0; w < W; ++w) {
+    const int64_t i = static_cast<int64_t>(w % cw / share) * C + w / cw;
+    const int part = w % cw % share;
+    if (i < lists) {
+      const int b = static_cast<int>(i / hkv);
+      const int32_t n = kv_indptr[b + 1] - kv_indptr[b];
+      const int parts = std::max(1, std::min<int>(share, n));
+      if (part < parts) {
+        const auto lo = static_cast<int32_t>(static_cast<int64_t>(n) * part / parts);
+        const auto hi = static_cast<int32_t>(static_cast<int64_t>(n) * (part + 1) / parts);
+        DecodeSeg s{};
+        s.b = b;
+        s.kvh = static_cast<int32_t>(i % hkv);
+        s.q_row = b;
+        s.idx_begin = kv_indptr[b] + lo;
+        s.n_pages = hi - lo;
+        s.last_rows = n == 0 ? 0 : (hi == n ? kv_last[b] : pl->p.page_size);
+        s.page_begin = lo;
+        s.slot = parts > 1 ? pkv::kSharedSlot : -1;
+        segs[k++] = s;
+        ++active;
+        n_workers = w + 1;
+      }
+    }
+    wptr[w + 1] = k;
+  }
+  finish_decode(pl, batch, host, n_workers, active, k, 0, 0, static_cast<int64_t>(kv_indptr[batch]) * hkv);
+  reinterpret_cast<PlanHeader*>(host + pl->L.header)->share = share;
+  return PKV_OK;
 }
 
 // Decode over the 8-bit cache with the heads in step: the requests' pages are cut into
@@ -510,11 +551,17 @@ pkv_status compute_decode(pkv_plan* pl, int batch, const int32_t* kv_indptr, con
     // one page: 8.2 us against 16.4 us).
     int32_t longest = 0;
     for (int b = 0; b < batch; ++b) longest = std::max(longest, kv_indptr[b + 1] - kv_indptr[b]);
-    // Over the 8-bit cache a warp streams 16 tokens in about 0.2 us and a split costs
-    // its pieces' setup and the merge's work, so lists up to 96 tokens longer than a run
-    // stay whole too (64 x 8 lists of 128 tokens: 9.1 us against 10.7 us).
-    const int32_t slack = pl->kv8 ? kWholeSlack8 / P : 0;
-    if (longest <= run + slack) return compute_decode_whole(pl, batch, kv_indptr, kv_last, host, W);
+    // Over the 8-bit cache a warp alone streams 16 tokens in about 0.3 us, and pieces on
+    // other SMs cost the merge's launch and reads.  Where the workers allow, a list is
+    // shared by up to 8 warps of one CTA instead, as long as its pieces are at most 96
+    // tokens longer than a run.
+    if (pl->kv8) {
+      int share = 8;
+      while (share > 1 && static_cast<int64_t>(batch) * hkv * share > W) share >>= 1;
+      if (ceil_div(longest, share) <= run + kShareSlack8 / P)
+        return compute_decode_shared(pl, batch, kv_indptr, kv_last, host, W, share);
+    }
+    if (longest <= run) return compute_decode_whole(pl, batch, kv_indptr, kv_last, host, W);
   }
 
   // In step as long as the runs' heads fill the workers to a twentieth.

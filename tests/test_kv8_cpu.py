@@ -294,3 +294,32 @@ def test_decode_kv8_plan(lib, hkv, P, seed, d):
         T = max(16, -(-(8 * sum(counts) + 8 * (B + G - 1)) // G))
         assert max(load.values()) <= -(-T // 8)
     api.plan_destroy(h)
+
+
+@pytest.mark.parametrize("kv_lens,hkv,P,share", [([1, 200, 0, 250], 2, 16, 8), ([128] * 64, 8, 16, 2), ([100] * 100, 8, 16, 1),
+                                                 ([500] * 19, 8, 1, 8), ([40] * 152, 1, 5, 8), ([3] * 300, 1, 1, 4)])
+def test_decode_kv8_plan_shares_short_lists_within_a_cta(lib, kv_lens, hkv, P, share):
+    counts, indptr, last = table(kv_lens, P)
+    B = len(kv_lens)
+    h = make(api.PLAN_DECODE_KV8, api.make_params(hkv, hkv, 128, P, torch.bfloat16, 0.1), api.Limits(B, B, int(indptr[-1])))
+    _, host = api.plan_workspace_bytes(h)
+    raw = torch.zeros(host + 64, dtype=torch.uint8)
+    ws = raw[(-raw.data_ptr()) % 64:][:host]
+    api.plan_compute(h, B, None, indptr, None, last, int(indptr[-1]) + 1, ws)
+    info, work = api.plan_get_info(h), api.plan_get_work(h).tolist()
+    assert info.num_merge == 0 and info.num_slots == 0
+    lists = {}
+    for w, b, kvh, p0, n, rows, slot, _ in work:
+        lists.setdefault((b, kvh), []).append((w, p0, n, slot))
+        if n:
+            assert rows == (int(last[b]) if p0 + n == counts[b] else P)
+    assert len({w for w, *_ in work}) == len(work) and len(lists) == B * hkv
+    for (b, kvh), pieces in lists.items():
+        parts = max(1, min(share, counts[b]))
+        assert len(pieces) == parts
+        w0 = pieces[0][0]
+        assert w0 % share == 0 and [w for w, *_ in pieces] == list(range(w0, w0 + parts))     # neighbours in one CTA
+        assert [p for _, p, _, _ in pieces] == [counts[b] * i // parts for i in range(parts)]
+        assert sum(n for _, _, n, _ in pieces) == counts[b]
+        assert {s for *_, s in pieces} == ({-2} if parts > 1 else {-1})
+    api.plan_destroy(h)

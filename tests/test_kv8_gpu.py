@@ -569,3 +569,59 @@ def test_the_same_call_twice_gives_the_same_bits():
     for _ in range(10):
         again = runner.decode_kv8(db, c, plan)
         assert torch.equal(first[0].view(torch.int16), again[0].view(torch.int16)) and torch.equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("g,d,dtype,cap", [(1, 128, BF, 0.0), (2, 64, FP, 4.0), (4, 128, FP, 0.0), (8, 64, BF, 0.0), (8, 128, BF, 6.0)])
+def test_decode_lists_shared_within_a_cta(g, d, dtype, cap):
+    lens = [1, 16, 17, 0, 33, 250, 128, 400, 2]
+    b = batch([1] * len(lens), lens, hq=2 * g, hkv=2, d=d, dtype=dtype, cap=cap, seed=g)
+    plan = runner.make_plan(b, api.PLAN_DECODE_KV8)
+    runner.plan_batch(plan, b)
+    assert plan.info().num_merge == 0 and (plan.work()[:, 6] == -2).any()
+    check_attention(b, spread=1)
+
+
+def test_a_graph_captured_without_splits_merges_after_replanning():
+    """Captured on a batch whose lists are shared within CTAs (nothing to merge), replayed on one whose
+    long lists are split over the card, and back."""
+    lens = [[20, 300], [30000, 17]]
+    bs = [batch([1, 1], n, hq=8, hkv=2, seed=110 + i, extra=0) for i, n in enumerate(lens)]
+    pool = max(b.num_pages for b in bs)
+    plan = api.Plan(api.PLAN_DECODE_KV8, num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=16, dtype=BF,
+                    sm_scale=128 ** -0.5, max_batch=2, max_kv_pages=pool)
+    cache = runner.Kv8Cache.zeros(pool, 2, 16, 128)
+    s = torch.cuda.Stream()
+    ix, ip, la = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (pool, 3, 2))
+    q = torch.zeros(2, 8, 128, dtype=BF, device="cuda")
+    o, lse = torch.zeros_like(q), torch.zeros(2, 8, device="cuda")
+    twins = []
+    for i, b in enumerate(bs):
+        c, twin = quantised(b, 1, seed=i, poison=False)
+        twins.append((c, twin))
+
+    def load(i):
+        b, (c, _) = bs[i], twins[i]
+        torch.cuda.synchronize()
+        ix[:b.kv_indices.numel()].copy_(b.kv_indices)
+        ip.copy_(b.kv_indptr), la.copy_(b.kv_last_page_len), q.copy_(b.q)
+        cache.codes.view(torch.uint8)[:b.num_pages].copy_(c.codes.view(torch.uint8))
+        cache.scales[:b.num_pages].copy_(c.scales)
+        torch.cuda.synchronize()
+        plan.plan(b.kv_indptr, b.kv_last_page_len, pool, kv_indices_h=b.kv_indices, stream=s)
+        return plan.info().num_merge
+
+    step = lambda: plan.run(q, cache.codes, ix, ip, la, o, lse, kv_scales=cache.scales, stream=s)
+    assert load(0) == 0
+    step()
+    s.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        step()
+    for i in (1, 0, 1):
+        assert (load(i) > 0) == (i == 1)
+        o.fill_(99.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            graph.replay()
+        s.synchronize()
+        assert_attention(o, lse, twins[i][1], 2.0 ** -11, f"replay {i}")
