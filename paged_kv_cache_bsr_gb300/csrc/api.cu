@@ -184,7 +184,9 @@ cudaError_t launch_prefill_tables(const pkv_plan* plan, const pkv::PrefillArgs& 
     e = pkv::launch_prefill(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->total_q,
                             plan->packed ? plan->max_packed : plan->num_pages, s);
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
-  if (e == cudaSuccess) e = pkv::launch_prefill_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
+  // Over the 8-bit cache: no merge launch without splits, as in its decode.
+  if (e == cudaSuccess && (!scales || plan->num_merge > 0 || maybe_capturing(s)))
+    e = pkv::launch_prefill_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
   if (e == cudaSuccess) e = release_tables(plan, s);
   return e;
 }
