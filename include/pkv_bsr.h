@@ -496,7 +496,7 @@ pkv_status pkv_append_paged_kv(const pkv_params* params, int batch, int64_t nnz,
  * the pairs are dealt to the axes in turn, an axis without pairs left passed over.
  */
 typedef struct {
-    double theta;       /* > 0 */
+    double theta;       /* > 0 (below 1 a pair may turn several times a step, at most 2^52) */
     int rotary_dim;     /* a multiple of 16 in [16, head_dim] */
     int num_axes;       /* 1..4 */
     int sections[4];    /* >= 0; the first num_axes of them sum to rotary_dim / 2 */
@@ -535,8 +535,9 @@ pkv_status pkv_append_paged_kv_axes(const pkv_params* params, const pkv_rope_axe
  * pkv_append_paged_kv8 appends new tokens' K and V into it; arguments as for
  * pkv_append_paged_kv_axes (k_new, v_new, q_in and q_out are of params->dtype).  For each
  * head row s = max(E - 7, 1), E the exponent field (0..254) of the row's largest
- * finite magnitude as a float32, taken before the rotation; the row, turned in float32
- * if it is a key's, times 2^(127 - s) is rounded to the nearest e4m3, ties to even.
+ * finite magnitude as a float32, taken before the rotation; the row, turned if it is a
+ * key's (in float32, and again in double precision where that may leave a code in
+ * doubt), times 2^(127 - s) is rounded to the nearest e4m3, ties to even.
  * The largest element of an unturned row lies in [128, 256) before that, and a
  * turned one below 256 sqrt(2) < 448, the largest e4m3.  Infinite elements become
  * +-448 of their row's scale (NaN where a rotation makes one of them), NaN stays NaN.

@@ -320,14 +320,15 @@ __global__ void __launch_bounds__(kAxThreads, 2) append_axes_kernel(const __grid
     const int n_pages = __ldg(a.kv_indptr + b + 1) - p0;
     const int last = __ldg(a.kv_last + b);
     const int64_t kv_len = n_pages > 0 ? static_cast<int64_t>(n_pages - 1) * P + last : 0;
+    const int64_t n_new = static_cast<int64_t>(a1) - a0;
     // A request claiming more new tokens than it holds, or more keys than an int
     // counts, is skipped whole.
-    if (t < a0 || t >= a1 || a1 - a0 > kv_len || kv_len > INT32_MAX || (n_pages > 0 && (last < 1 || last > P))) {
+    if (t < a0 || t >= a1 || n_new > kv_len || kv_len > INT32_MAX || (n_pages > 0 && (last < 1 || last > P))) {
       err |= kErrAppendLayout;
       skip();
       continue;
     }
-    const int place = static_cast<int>(kv_len - (a1 - a0) + (t - a0));
+    const int place = static_cast<int>(kv_len - n_new + (t - a0));
     const int page_no = place / P, slot = place - page_no * P;
     const int page = __ldg(a.kv_indices + p0 + page_no);
     if (page < 0 || page >= a.num_pages) {
@@ -506,6 +507,7 @@ bool set_rotation(AxesArgs& a, const pkv_rope_axes* rope, int head_dim) {
     if (rope->interleaved) x = (x + 1) % rope->num_axes;
     // Good to about 2^-50 of its value: the angle of position p to |p| times that.
     const double turn = by8[i / 8] * by1[i % 8];
+    if (!(turn < 4503599627370496.0)) return false;  // theta so small that a step's turns fill the double
     a.freq[i] = static_cast<uint64_t>(std::ldexp(turn - std::floor(turn), 64));  // theta < 1: over a turn a step
   }
   return true;

@@ -94,8 +94,9 @@ def test_appends_refuse_bad_arguments_before_any_cuda_call(lib, ptrs, kv8):
         return fn(*args, *([scales] if kv8 else []), q_in, q_out, None, None)
 
     assert append(params=None) == INVALID
-    for theta in (0.0, -1.0, float("nan"), float("inf")):
+    for theta in (0.0, -1.0, float("nan"), float("inf"), 1e-30, 1e-308, 5e-324):
         assert append(r=rope(theta=theta)) == INVALID
+    assert append(nnz=0, r=rope(theta=1e-9)) == api.PKV_OK
     for rotary, sections in ((0, (0,)), (8, (4,)), (24, (12,)), (144, (72,)), (128, (63,)), (128, (65, -1)), (128, (32, 32, 32))):
         assert append(r=rope(rotary=rotary, sections=sections)) == INVALID
     assert append(r=rope(axes=0)) == INVALID

@@ -625,3 +625,20 @@ def test_a_graph_captured_without_splits_merges_after_replanning():
             graph.replay()
         s.synchronize()
         assert_attention(o, lse, twins[i][1], 2.0 ** -11, f"replay {i}")
+
+
+def test_prefill_bad_page_is_flagged_and_the_rest_exact():
+    b = batch([20, 30, 5], [40, 100, 64], causal=True, seed=120)
+    cache, twin = quantised(b)
+    db = runner.DeviceBatch.from_host(b, kv_data=torch.empty(0))
+    plan = runner.make_plan(b, api.PLAN_PREFILL_KV8)
+    runner.plan_batch(plan, b)
+    db.kv_indices[int(b.kv_indptr[1])] = -3          # request 1's first page
+    o, lse = runner.prefill_kv8(db, to_cuda(cache), plan)
+    assert plan.device_error(clear=True) == 1 and plan.device_error() == 0
+    keep = list(range(20)) + list(range(50, 55))
+    ref_o, ref_lse = oracle.attention_of(twin, rows=keep)
+    got = oracle.decode16(o.cpu()[keep])
+    vmax = np.abs(np.nan_to_num(oracle.decode16(twin.kv_data)[:, 1])).max()
+    assert (np.abs(got - ref_o) <= EPS2[BF] * np.abs(ref_o) + (EPS2[BF] + 4e-4) * vmax).all()
+    assert (np.abs(lse.cpu().numpy()[keep] - ref_lse) <= 4e-4).all()
