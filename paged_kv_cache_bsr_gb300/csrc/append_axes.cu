@@ -559,12 +559,12 @@ pkv_status append_axes(const pkv_params* p, const pkv_rope_axes* rope, int batch
     cudaGetLastError();
     return PKV_ERR_CUDA;
   }
-  // Few tokens are shared by several warps each, down to one pass a warp, until there
-  // are 16 warps for every SM.
+  // Few tokens are shared by several warps each, down to one pass a warp, as long as all
+  // of them run at once (16 warps on every SM).
   const int rpp = 32 / (p->head_dim / 16);
   const int hq = q_in ? p->num_qo_heads : 0;
   const int passes = (p->num_kv_heads + rpp - 1) / rpp + (hq + 2 * rpp - 1) / (2 * rpp);
-  const int64_t share = (static_cast<int64_t>(sms) * 16 + nnz - 1) / nnz;
+  const int64_t share = std::max<int64_t>(static_cast<int64_t>(sms) * 16 / nnz, 1);
   const int parts = static_cast<int>(share < passes ? share : passes);
   a.part_passes = (passes + parts - 1) / parts;
   a.parts = (passes + a.part_passes - 1) / a.part_passes;
