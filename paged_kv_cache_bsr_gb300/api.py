@@ -349,9 +349,12 @@ def _ptrs(tensors):
     return out
 
 
+_I32 = torch.int32
+
+
 def _int32(*tensors) -> None:
     for x in tensors:
-        if x is not None and x.dtype is not torch.int32:
+        if x is not None and x.dtype is not _I32:
             raise ValueError("page tables, row pointers, positions and error words must be int32")
 
 
@@ -370,10 +373,11 @@ def _append_tensors(params: Params, rope, append_indptr, kv_indptr, kv_indices, 
     _int32(append_indptr, kv_indptr, kv_indices, kv_last_page_len, positions, error)
     if batch < 0 or kv_indptr.numel() != batch + 1 or kv_last_page_len.numel() != batch:
         raise ValueError("append_indptr and kv_indptr must have batch + 1 entries, kv_last_page_len batch")
-    dtype, kv_rows = _STORED.get(params.dtype), (nnz, params.num_kv_heads, params.head_dim)
+    dtype, dim = _STORED.get(params.dtype), params.head_dim
+    kv_rows = (nnz, params.num_kv_heads, dim)
     fits = k_new.shape == kv_rows and v_new.shape == kv_rows and k_new.dtype is dtype and v_new.dtype is dtype
     if q_in is not None:
-        q_rows = (nnz, params.num_qo_heads, params.head_dim)
+        q_rows = (nnz, params.num_qo_heads, dim)
         fits = fits and q_in.shape == q_rows and q_out.shape == q_rows and q_in.dtype is dtype and q_out.dtype is dtype
     if not fits:
         raise ValueError("k_new, v_new, q_in and q_out must be [nnz, heads, head_dim] of the params' dtype")

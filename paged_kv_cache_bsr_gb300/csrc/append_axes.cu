@@ -508,7 +508,7 @@ bool set_rotation(AxesArgs& a, const pkv_rope_axes* rope, int head_dim) {
     // Good to about 2^-50 of its value: the angle of position p to |p| times that.
     const double turn = by8[i / 8] * by1[i % 8];
     if (!(turn < 4503599627370496.0)) return false;  // theta so small that a step's turns fill the double
-    a.freq[i] = static_cast<uint64_t>(std::ldexp(turn - std::floor(turn), 64));  // theta < 1: over a turn a step
+    a.freq[i] = static_cast<uint64_t>((turn - std::floor(turn)) * 18446744073709551616.0);  // 2^64; theta < 1: over a turn a step
   }
   return true;
 }
