@@ -528,8 +528,8 @@ pkv_status pkv_append_paged_kv_axes(const pkv_params* params, const pkv_rope_axe
 /*
  * The 8-bit cache: half the bytes of kv_data for the same tokens.
  *   kv8        [num_pages, 2, num_kv_heads, page_size, head_dim] e4m3 codes, one byte each
- *   kv8_scales [num_pages, 2, num_kv_heads, page_size] one byte s for each head row:
- *              code c stands for e4m3(c) * 2^(s - 127)
+ *   kv8_scales [num_pages, 2, num_kv_heads, page_size] one byte s in 1..254 for each
+ *              head row: code c stands for e4m3(c) * 2^(s - 127)
  * (K at index 0, V at index 1, as in kv_data.)
  *
  * pkv_append_paged_kv8 appends new tokens' K and V into it; arguments as for

@@ -642,3 +642,10 @@ def test_prefill_bad_page_is_flagged_and_the_rest_exact():
     vmax = np.abs(np.nan_to_num(oracle.decode16(twin.kv_data)[:, 1])).max()
     assert (np.abs(got - ref_o) <= EPS2[BF] * np.abs(ref_o) + (EPS2[BF] + 4e-4) * vmax).all()
     assert (np.abs(lse.cpu().numpy()[keep] - ref_lse) <= 4e-4).all()
+
+
+@pytest.mark.parametrize("hkv,d,P", [(40, 128, 16), (150, 64, 4), (700, 64, 16), (2500, 64, 1)])
+def test_decode_many_kv_heads(hkv, d, P):
+    """Plans with many heads in step, and (700 heads fill 152 x 16 workers badly, 2500 are more than them) list by list."""
+    lens = [1, 33, 60, 7] if hkv > 200 else [1, 700, 33, 0, 1500, 64]
+    check_attention(batch([1] * len(lens), lens, hq=hkv, hkv=hkv, d=d, P=P, seed=hkv), spread=1)
