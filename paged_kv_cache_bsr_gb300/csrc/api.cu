@@ -180,9 +180,11 @@ cudaError_t launch_prefill_tables(const pkv_plan* plan, const pkv::PrefillArgs& 
   if (pack && e == cudaSuccess)
     e = scales ? pkv::launch_expand_pages(*pack, scales, p.head_dim, p.dtype, plan->num_sms * 8, s)
                : pkv::launch_pack_pages(*pack, p.head_dim, plan->num_sms * 8, s);
-  if (e == cudaSuccess)
-    e = pkv::launch_prefill(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->total_q,
-                            plan->packed ? plan->max_packed : plan->num_pages, s);
+  if (e == cudaSuccess) {
+    const int64_t pages = plan->packed ? plan->max_packed : plan->num_pages;
+    const auto launch = scales && plan->num_merge > 0 ? pkv::launch_prefill8 : pkv::launch_prefill;
+    e = launch(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->total_q, pages, s);
+  }
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
   // Over the 8-bit cache: no merge launch without splits, as in its decode.
   if (e == cudaSuccess && (!scales || plan->num_merge > 0 || maybe_capturing(s)))

@@ -166,6 +166,10 @@ cudaError_t launch_pack_pages(const PackArgs& a, int head_dim, int grid, cudaStr
 // bytes, any page size; the copy holds the values in dtype.
 cudaError_t launch_expand_pages(const PackArgs& a, const uint8_t* scales, int head_dim, int dtype, int grid,
                                 cudaStream_t stream);
+// launch_prefill without a mask, over 16-row pages, as a dependent of the expansion, with
+// split tiles' partial states staged through shared memory.
+cudaError_t launch_prefill8(const PrefillArgs& a, int head_dim, int group, int dtype, bool cap, int grid,
+                            int64_t total_q, int64_t num_pages, cudaStream_t stream);
 cudaError_t launch_prefill_merge(const PrefillArgs& a, int head_dim, int group, int dtype, int grid,
                                  cudaStream_t stream);
 
