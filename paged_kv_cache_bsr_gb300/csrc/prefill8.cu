@@ -7,7 +7,7 @@
 // programmatic dependent of the expansion, which hides the gap between the two.  Measured
 // against the plain instances: 64 rows over 8192 keys 39.2 -> 36.4 us, two short prompts
 // 16.1 -> 13.2 us, a 512-row chunk behind 8192 keys 113.7 -> 108.5 us.  Batches without
-// splits keep the plain instances, which they ran 1.6 % faster on when staging came in.
+// splits keep the plain instances (staging costs a ragged causal batch 1.6 %).
 #include "prefill_kernel.cuh"
 
 namespace pkv {
