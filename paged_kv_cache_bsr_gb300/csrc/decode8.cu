@@ -19,7 +19,9 @@
 // chip has, next to the conversions, so both products run on the tensor cores as
 // mma.sync m16n8k16 (fp16 operands, fp32 sums): 16 keys x 8 heads of the group
 // (padded), then 16 dims x 8 heads.  Keys and dims are the M axis, so a group of 8
-// wastes nothing, and the padding of a smaller one costs no bandwidth.
+// wastes nothing, and the padding of a smaller one costs no bandwidth.  (tcgen05 tiles
+// would tie a CTA's warps together over 128 keys, with the codes expanded into shared
+// memory first; here every warp streams on its own, and the tensor pipe is 16 % busy.)
 //  - One CTA per SM holds 8 (head_dim 64: 16) independent warps, each with the plan's
 //    list of (request, kv head, page range) segments and a ring of 16-token tiles in
 //    shared memory, filled by its own 16-byte cp.async copies kStages - 1 tiles
