@@ -626,8 +626,8 @@ __global__ void __launch_bounds__(decode8_warps(D) * 32, 1) decode8_kernel(const
 #pragma unroll
     for (int v = 0; v < PER; ++v) acc[v] = 0.f;
     for (int k = 0; k < share; ++k) {
+      if (shared[first + k].lse[head] == -INFINITY) continue;  // no piece: its ring holds anything
       const float w = fast_exp2((shared[first + k].lse[head] - m) * kLog2e);
-      if (w == 0.f) continue;  // no piece (its ring holds anything), or nothing to add
       l += w;
       const float* o = reinterpret_cast<const float*>(smem + (first + k) * kRing) + head * D + lane * PER;
 #pragma unroll
@@ -647,7 +647,9 @@ __global__ void __launch_bounds__(decode8_warps(D) * 32, 1) decode8_kernel(const
 // fill (a power of two up to all of them): a request of 8192 tokens alone leaves 32 such
 // pairs of 152 slots, which take one warp each 10 us to read and eight warps 2.5 us; the
 // serving batch leaves 2016 pairs of 3 slots, a warp each.  The warps' states are
-// combined in their order, so the result does not depend on timing.
+// combined in their order, so the result does not depend on timing.  A slot whose lse
+// is NaN counts like any other (fmaxf passes over a NaN, so m may stay -inf beside it):
+// its weight is NaN, and so are o and lse, as where one warp holds the whole list.
 template <int D, typename T>
 __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const __grid_constant__ DecodeArgs a) {
   constexpr int PER = D / 32;           // dims per lane
@@ -701,17 +703,21 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const __gr
           }
         }
         float top = m;
+        bool any = false;
 #pragma unroll
-        for (int u = 0; u < U; ++u) top = fmaxf(top, lse[u]);
-        if (top == -INFINITY) continue;
-        const float w0 = fast_exp2((m - top) * kLog2e);  // 0 while m is -inf
+        for (int u = 0; u < U; ++u) {
+          top = fmaxf(top, lse[u]);
+          any |= lse[u] != -INFINITY;
+        }
+        if (!any) continue;
+        const float w0 = m == top ? 1.f : fast_exp2((m - top) * kLog2e);  // 0 while m alone is -inf
         l *= w0;
 #pragma unroll
         for (int v = 0; v < PER; ++v) acc[v] *= w0;
         m = top;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          const float w = fast_exp2((lse[u] - m) * kLog2e);  // 0 for a slot past hi
+          const float w = lse[u] == -INFINITY ? 0.f : fast_exp2((lse[u] - m) * kLog2e);  // 0 for a slot past hi
           l += w;
 #pragma unroll
           for (int v = 0; v < PER; ++v) acc[v] = fmaf(w, vals[u][v], acc[v]);
@@ -730,12 +736,12 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const __gr
       if (part == 0) {
         float top = m;
         for (int k = 1; k < wpp; ++k) top = fmaxf(top, s_m[warp + k]);
-        const float w0 = m == -INFINITY ? 0.f : fast_exp2((m - top) * kLog2e);
+        const float w0 = m == top ? 1.f : fast_exp2((m - top) * kLog2e);
         l *= w0;
 #pragma unroll
         for (int v = 0; v < PER; ++v) acc[v] *= w0;
         for (int k = 1; k < wpp; ++k) {
-          if (s_m[warp + k] == -INFINITY) continue;
+          if (s_l[warp + k] == 0.f) continue;  // no slots
           const float w = fast_exp2((s_m[warp + k] - top) * kLog2e);
           l = fmaf(w, s_l[warp + k], l);
 #pragma unroll
@@ -746,12 +752,12 @@ __global__ void __launch_bounds__(kMergeThreads) decode8_merge_kernel(const __gr
     }
     if (have && part == 0) {
       const int64_t row = static_cast<int64_t>(it.row) * a.num_qo_heads + it.kvh * G + g;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       T* dst = static_cast<T*>(a.o) + row * D + lane * PER;
 #pragma unroll
       for (int v = 0; v < PER; v += 2)
         *reinterpret_cast<uint32_t*>(dst + v) = pack2<T>(acc[v] * inv, acc[v + 1] * inv);
-      if (lane == 0 && a.lse) a.lse[row] = l > 0.f ? m + logf(l) : -INFINITY;
+      if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
     }
   }
 }

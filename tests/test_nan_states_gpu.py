@@ -1,0 +1,150 @@
+"""NaN in what a batch reads: it reaches the outputs and lse of every row that sees it, and nothing else, however
+the plan splits the work.  Everything that does not see it keeps the bits of the call without it."""
+import dataclasses
+
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_bsr_gb300 import api, runner
+from kv8_util import batch
+
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from paged_kv_cache_bsr_gb300 import build
+    build.build()
+    api.load()
+    torch.cuda.set_device(0)
+
+
+def cache_of(b, seed=0):
+    """An 8-bit cache of finite codes for the batch's pool."""
+    gen = torch.Generator("cuda").manual_seed(seed)
+    shape = (b.num_pages, 2, b.num_kv_heads, b.page_size)
+    codes = torch.randint(0, 256, (*shape, b.head_dim), generator=gen, dtype=torch.uint8, device="cuda")
+    codes[(codes & 0x7F) == 0x7F] = 0x30
+    return runner.Kv8Cache(codes.view(torch.float8_e4m3fn),
+                           torch.randint(115, 120, shape, generator=gen, dtype=torch.uint8, device="cuda"))
+
+
+def at(b, r, token):
+    """(page, slot) of a request's token."""
+    return int(b.kv_indices[int(b.kv_indptr[r]) + token // b.page_size]), token % b.page_size
+
+
+def run(kind, b, plan, q, cache, kv):
+    db = runner.DeviceBatch.from_host(b, kv_data=kv)
+    db.q = q
+    o, lse = {"decode8": lambda: runner.decode_kv8(db, cache, plan), "prefill8": lambda: runner.prefill_kv8(db, cache, plan),
+              "decode16": lambda: runner.decode(db, plan), "prefill16": lambda: runner.prefill(db, plan),
+              "mixed16": lambda: runner.mixed(db, plan)}[kind]()
+    torch.cuda.synchronize()
+    return o.cpu(), lse.cpu()
+
+
+KINDS = {"decode8": api.PLAN_DECODE_KV8, "prefill8": api.PLAN_PREFILL_KV8, "decode16": api.PLAN_DECODE,
+         "prefill16": api.PLAN_PREFILL, "mixed16": api.PLAN_MIXED}
+
+
+def same_bits(x, y):
+    i = torch.int16 if x.element_size() == 2 else torch.int32
+    return x.view(i) == y.view(i)
+
+
+def check(kind, b, expect, keys, query_scale=1.0, dims=(5,), **plan_kw):
+    """A NaN in each listed key, value and query element: (request, token, kv head), in turn."""
+    g = b.num_qo_heads // b.num_kv_heads
+    plan = runner.make_plan(b, KINDS[kind], **plan_kw)
+    eight = kind.endswith("8")
+    cache = cache_of(b) if eight else None
+    kv = torch.empty(0) if eight else torch.nan_to_num(b.kv_data.float(), 0.0).to(b.dtype).cuda()
+    runner.plan_batch(plan, b, num_pages=b.num_pages)
+    expect(plan)
+    q = (b.q.float() * query_scale).to(b.dtype).cuda()
+    o, lse = run(kind, b, plan, q, cache, kv)
+    assert torch.isfinite(o.float()).all() and not torch.isnan(lse).any()
+    qo = b.qo_indptr.tolist()
+    for r, token, h in keys:
+        page, slot = at(b, r, token)
+        heads = slice(h * g, (h + 1) * g)
+        first = max(0, token - (b.kv_lens[r] - b.qo_lens[r])) if b.causal else 0   # the request's first row that sees it
+        rows = slice(qo[r] + first, qo[r + 1])
+        for which in (0, 1) if not b.causal else (0,):
+            for dim in dims:
+                if eight:
+                    c8 = runner.Kv8Cache(cache.codes.view(torch.uint8).clone(), cache.scales)
+                    c8.codes[page, which, h, slot, dim] = 0xFF
+                    got, got_lse = run(kind, b, plan, q, c8, kv)
+                else:
+                    k2 = kv.clone()
+                    k2[page, which, h, slot, dim] = NAN
+                    got, got_lse = run(kind, b, plan, q, cache, k2)
+                hit, hit_lse = torch.zeros(o.shape, dtype=torch.bool), torch.zeros(lse.shape, dtype=torch.bool)
+                if which == 0:
+                    hit[rows, heads], hit_lse[rows, heads] = True, True
+                else:
+                    hit[rows, heads, dim] = True
+                what = f"{'KV'[which]} of request {r}, token {token}, head {h}"
+                assert torch.isnan(got[hit]).all() and torch.isnan(got_lse[hit_lse]).all(), what
+                assert same_bits(got, o)[~hit].all() and same_bits(got_lse, lse)[~hit_lse].all(), what
+        row, head = qo[r + 1] - 1, h * g
+        q2 = q.clone()
+        q2[row, head, 7] = NAN
+        got, got_lse = run(kind, b, plan, q2, cache, kv)
+        hit = torch.zeros(lse.shape, dtype=torch.bool)
+        hit[row, head] = True
+        assert torch.isnan(got[hit]).all() and torch.isnan(got_lse[hit]).all(), f"query {row}, head {head}"
+        assert same_bits(got, o)[~hit].all() and same_bits(got_lse, lse)[~hit].all()
+
+
+def split(plan):
+    assert plan.info().num_merge > 0
+
+
+def whole(plan):
+    assert plan.info().num_merge == 0
+
+
+def shared(plan):
+    assert plan.info().num_merge == 0 and (plan.work()[:, 6] == -2).any()
+
+
+# --------------------------------------------------------------------------- decode over the 8-bit cache
+# Queries of 300 times the size put most pieces' weights at zero: a NaN value behind such a weight still counts.
+@pytest.mark.parametrize("scale", [1.0, 300.0])
+@pytest.mark.parametrize("g,d,dtype,cap", [(4, 128, BF, 0.0), (8, 64, FP, 0.0), (1, 128, BF, 9.0)])
+def test_decode8_few_lists_in_many_pieces(g, d, dtype, cap, scale):
+    """Several warps to a row of the merge, some with one piece or none."""
+    b = batch([1, 1], [30000, 600], hq=2 * g, hkv=2, d=d, dtype=dtype, cap=cap, seed=g, extra=0)
+    check("decode8", b, split, [(0, 17000, 0), (0, 29999, 1), (1, 0, 0), (1, 599, 1), (1, 300, 0)], scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 300.0])
+def test_decode8_many_lists_in_few_pieces(scale):
+    """One warp to a row of the merge."""
+    b = batch([1] * 71, [600] * 70 + [3000], hq=8, hkv=4, seed=3, extra=0)
+    check("decode8", b, split, [(0, 0, 0), (69, 599, 3), (70, 1500, 2)], scale)
+
+
+@pytest.mark.parametrize("scale", [1.0, 300.0])
+@pytest.mark.parametrize("d,P", [(128, 16), (64, 5)])
+def test_decode8_lists_shared_within_a_cta(d, P, scale):
+    b = batch([1] * 5, [1, 33, 250, 128, 400], hq=8, hkv=2, d=d, P=P, seed=4, extra=0)
+    check("decode8", b, shared, [(0, 0, 0), (2, 100, 1), (4, 399, 0), (4, 0, 1)], scale)
+
+
+def test_decode8_whole_lists():
+    b = batch([1] * 4, [1, 33, 250, 900], hq=8, hkv=2, seed=5, extra=0)
+    check("decode8", b, whole, [(0, 0, 0), (2, 100, 1), (3, 899, 0)], split_kv=False)
+
+
+def test_decode8_empty_requests_beside_a_nan():
+    """A request without keys keeps o = 0 and lse = -inf."""
+    b = batch([1] * 3, [0, 20000, 0], hq=8, hkv=2, seed=6, extra=0)
+    check("decode8", b, split, [(1, 19999, 1), (1, 3, 0)])
