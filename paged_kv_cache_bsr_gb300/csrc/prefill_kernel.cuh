@@ -655,8 +655,9 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
         ++odc;
         tc_fence_after();
       }
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      const float lse_v = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+      // l is 0 for a row that sees no key; a NaN key or query leaves it NaN, and o and lse with it.
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse_v = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
       const int64_t orow = static_cast<int64_t>(t.q_row0 + rpos) * a.num_qo_heads + t.kvh * G + (r % G);
       const int srow = x * kTM + r;  // row of the work tile, for a partial-state slot
       if (t.slot < 0) {

@@ -148,3 +148,17 @@ def test_decode8_empty_requests_beside_a_nan():
     """A request without keys keeps o = 0 and lse = -inf."""
     b = batch([1] * 3, [0, 20000, 0], hq=8, hkv=2, seed=6, extra=0)
     check("decode8", b, split, [(1, 19999, 1), (1, 3, 0)])
+
+
+# --------------------------------------------------------------------------- prefill
+@pytest.mark.parametrize("kind", ["prefill8", "prefill16"])
+@pytest.mark.parametrize("g,dtype,cap", [(4, BF, 0.0), (2, FP, 7.0)])
+def test_prefill_whole_tiles(kind, g, dtype, cap):
+    b = batch([30, 5], [100, 128], hq=2 * g, hkv=2, dtype=dtype, cap=cap, seed=g, extra=0)
+    check(kind, b, whole, [(0, 0, 0), (0, 99, 1), (1, 64, 0)])
+
+
+@pytest.mark.parametrize("kind", ["prefill8", "prefill16"])
+def test_prefill_causal_whole_tiles(kind):
+    """A NaN key reaches the rows from its own on (it is masked for those before)."""
+    check(kind, batch([128] * 20, [128] * 20, hq=16, hkv=8, causal=True, seed=9, extra=0), whole, [(0, 60, 1), (19, 127, 7)])
