@@ -768,17 +768,22 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
 
 // Log-sum-exp merge of the chunks' fp32 partial states of one packed row of a
 // query tile whose key range the plan split (pair = item * 256 + row), by the
-// calling warp, lanes over head_dim.  Shared by the prefill merge kernel and the
-// mixed batch's merge kernel.
+// calling warp, lanes over head_dim.  A NaN lse takes the maximum's place (fmaxf alone
+// would pass over it), so it makes every weight, o and lse NaN.  Shared by the prefill
+// merge kernel and the mixed batch's merge kernel.
 template <typename T>
 __device__ __forceinline__ void prefill_merge_row(const PrefillArgs& a, int pair, int lane, int G) {
   const PrefillMerge it = a.merge[pair / kWR];
   const int r = pair % kWR;
   if (r / G >= it.n_pos) return;
   float mx = -INFINITY;
-  for (int i = lane; i < it.n_slots; i += 32)
-    mx = fmaxf(mx, a.part_lse[static_cast<int64_t>(it.slot_begin + i) * kWR + r]);
-  mx = warp_max(mx);
+  bool nan = false;
+  for (int i = lane; i < it.n_slots; i += 32) {
+    const float l = a.part_lse[static_cast<int64_t>(it.slot_begin + i) * kWR + r];
+    mx = fmaxf(mx, l);
+    nan |= l != l;
+  }
+  mx = __any_sync(kFull, nan) ? NAN : warp_max(mx);
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float wsum = 0.f;
   if (mx != -INFINITY) {
@@ -789,7 +794,7 @@ __device__ __forceinline__ void prefill_merge_row(const PrefillArgs& a, int pair
       const int64_t row = static_cast<int64_t>(it.slot_begin + i) * kWR + r;
       const float4 v = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
       const float w = fast_exp2((a.part_lse[row] - mx) * kLog2e);
-      const bool use = w > 0.f;
+      const bool use = w != 0.f;
       acc[0] = use ? fmaf(w, v.x, acc[0]) : acc[0];
       acc[1] = use ? fmaf(w, v.y, acc[1]) : acc[1];
       acc[2] = use ? fmaf(w, v.z, acc[2]) : acc[2];
@@ -797,12 +802,12 @@ __device__ __forceinline__ void prefill_merge_row(const PrefillArgs& a, int pair
       wsum += use ? w : 0.f;
     }
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   const int64_t orow = static_cast<int64_t>(it.q_row0 + r / G) * a.num_qo_heads + it.kvh * G + (r % G);
   T* dst = static_cast<T*>(a.o) + orow * kD + lane * 4;
 #pragma unroll
   for (int v = 0; v < 4; ++v) dst[v] = from_float<T>(acc[v] * inv);
-  if (lane == 0 && a.lse) a.lse[orow] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
+  if (lane == 0 && a.lse) a.lse[orow] = wsum == 0.f ? -INFINITY : mx + logf(wsum);
 }
 
 template <int G, typename T, bool CAP, bool MASK, bool SMALL>

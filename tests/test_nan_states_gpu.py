@@ -162,3 +162,20 @@ def test_prefill_whole_tiles(kind, g, dtype, cap):
 def test_prefill_causal_whole_tiles(kind):
     """A NaN key reaches the rows from its own on (it is masked for those before)."""
     check(kind, batch([128] * 20, [128] * 20, hq=16, hkv=8, causal=True, seed=9, extra=0), whole, [(0, 60, 1), (19, 127, 7)])
+
+
+@pytest.mark.parametrize("kind", ["prefill8", "prefill16"])
+@pytest.mark.parametrize("g,dtype,cap", [(4, BF, 0.0), (1, FP, 7.0), (8, FP, 0.0)])
+def test_prefill_split_over_the_keys(kind, g, dtype, cap):
+    b = batch([40, 3], [3000, 700], hq=2 * g, hkv=2, dtype=dtype, cap=cap, seed=g, extra=0)
+    check(kind, b, split, [(0, 0, 0), (0, 2999, 1), (1, 350, 0)])
+
+
+@pytest.mark.parametrize("kind", ["prefill8", "prefill16"])
+def test_prefill_causal_split_over_the_keys(kind):
+    check(kind, batch([300, 70], [300, 200], hq=8, hkv=2, causal=True, seed=8, extra=0), split, [(0, 250, 1), (1, 150, 0)])
+
+
+def test_prefill_small_pages_and_a_mixed_batch():
+    check("prefill16", batch([40, 3], [900, 70], P=1, seed=10, extra=0), split, [(0, 5, 0), (1, 69, 1)])
+    check("mixed16", batch([1, 1, 40], [30000, 600, 3000], seed=11, extra=0), split, [(2, 5, 0), (2, 2999, 1)])
