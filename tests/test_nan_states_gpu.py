@@ -179,3 +179,10 @@ def test_prefill_causal_split_over_the_keys(kind):
 def test_prefill_small_pages_and_a_mixed_batch():
     check("prefill16", batch([40, 3], [900, 70], P=1, seed=10, extra=0), split, [(0, 5, 0), (1, 69, 1)])
     check("mixed16", batch([1, 1, 40], [30000, 600, 3000], seed=11, extra=0), split, [(2, 5, 0), (2, 2999, 1)])
+
+
+@pytest.mark.parametrize("kind", ["prefill8", "prefill16"])
+def test_prefill_nan_value_behind_a_weight_of_zero(kind):
+    """Queries of 300 times the size: most pieces of a split row weigh nothing beside its largest logits."""
+    b = batch([40, 3], [3000, 700], hq=8, hkv=2, seed=14, extra=0)
+    check(kind, b, split, [(0, t, 0) for t in (0, 700, 1500, 2300, 2999)] + [(1, 350, 1)], 300.0)
