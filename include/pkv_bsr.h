@@ -402,7 +402,8 @@ pkv_status pkv_batch_mixed_paged(const pkv_plan* plan, const void* q, const int3
  * num_heads rows with states (o_a, lse_a) and (o_b, lse_b) over disjoint key
  * sets:  m = max(lse_a, lse_b); w_x = exp(lse_x - m);
  *        o = (w_a o_a + w_b o_b) / (w_a + w_b); lse = m + ln(w_a + w_b).
- * Both lse = -inf gives o = 0, lse = -inf; a state with lse = -inf adds nothing.
+ * Both lse = -inf gives o = 0, lse = -inf; a state with lse = -inf adds nothing; a
+ * NaN lse gives NaN.
  * o_* : [n_rows, num_heads, head_dim] of `dtype` (PKV_F16, PKV_BF16 or PKV_F32;
  * inputs and output share it); lse_*: [n_rows, num_heads] fp32.  o_out and
  * lse_out may alias o_a and lse_a.  lse_out may be NULL.  The kernel is
@@ -420,7 +421,8 @@ pkv_status pkv_merge_state(const void* o_a, const float* lse_a, const void* o_b,
  * partial outputs, or the levels of a shared-prefix tree, guide section 3):
  * for each of n_rows * num_heads rows, m = max_k lse_k, w_k = exp(lse_k - m),
  * o = sum_k w_k o_k / sum_k w_k, lse = m + ln(sum_k w_k); every lse_k = -inf
- * gives o = 0, lse = -inf, and a state with lse = -inf adds nothing.
+ * gives o = 0, lse = -inf, a state with lse = -inf adds nothing, and a NaN lse
+ * gives NaN.
  * State k of row r is row k * state_stride_rows + r of o_states ([rows,
  * num_heads, head_dim] of `dtype`) and lse_states ([rows, num_heads] fp32), so
  * n states of n_rows rows laid out one after another have state_stride_rows =

@@ -7,6 +7,8 @@
 // "using online softmax correction"; FlashDecoding merges partial outputs the
 // same way):  m = max(lse_a, lse_b),  w_x = exp(lse_x - m),
 //             o = (w_a o_a + w_b o_b) / (w_a + w_b),  lse = m + ln(w_a + w_b).
+// A state with lse = -inf is empty and adds nothing, whatever its o holds; one whose
+// lse is NaN makes the result NaN.
 //
 // Elementwise and HBM-bound: one thread per 16-byte chunk of a row, the
 // chunks of one (row, head) inside one warp so that lse can be read by all of
@@ -70,7 +72,7 @@ __global__ void __launch_bounds__(256) merge_state_kernel(const uint8_t* o_a, co
       const int64_t off = (r * chunks + chunk) * 16;
       float out[C::N];
       float lse;
-      if (m == -INFINITY) {
+      if (la == -INFINITY && lb == -INFINITY) {  // (m is -inf too beside a NaN, which fmaxf passes over)
 #pragma unroll
         for (int i = 0; i < C::N; ++i) out[i] = 0.f;
         lse = -INFINITY;
@@ -82,8 +84,8 @@ __global__ void __launch_bounds__(256) merge_state_kernel(const uint8_t* o_a, co
         C::load(o_b + off, fb);
 #pragma unroll
         for (int i = 0; i < C::N; ++i) {
-          const float ta = wa > 0.f ? wa * fa[i] : 0.f;  // an empty state adds nothing
-          const float tb = wb > 0.f ? wb * fb[i] : 0.f;
+          const float ta = la != -INFINITY ? wa * fa[i] : 0.f;  // an empty state adds nothing
+          const float tb = lb != -INFINITY ? wb * fb[i] : 0.f;
           out[i] = (ta + tb) * inv;
         }
         lse = m + logf(s);
@@ -114,16 +116,24 @@ __global__ void __launch_bounds__(256) merge_states_kernel(const uint8_t* o_in, 
     const int64_t r = base + lane / chunks;
     const bool valid = r < rows;
     float m = -INFINITY;
-    if (valid)
-      for (int k = 0; k < n_states; ++k) m = fmaxf(m, lse_in[k * stride + r]);
+    if (valid) {
+      bool nan = false;
+      for (int k = 0; k < n_states; ++k) {
+        const float l = lse_in[k * stride + r];
+        m = fmaxf(m, l);
+        nan |= l != l;
+      }
+      if (nan) m = NAN;
+    }
     float out[C::N];
 #pragma unroll
     for (int i = 0; i < C::N; ++i) out[i] = 0.f;
     float s = 0.f;
     if (valid && m != -INFINITY) {
       for (int k = 0; k < n_states; ++k) {
-        const float w = expf(lse_in[k * stride + r] - m);
-        if (w > 0.f) {  // an empty state adds nothing (its o is not read)
+        const float l = lse_in[k * stride + r];
+        if (l != -INFINITY) {  // an empty state adds nothing (its o is not read)
+          const float w = expf(l - m);
           float f[C::N];
           C::load(o_in + ((k * stride + r) * chunks + chunk) * 16, f);
 #pragma unroll
@@ -134,11 +144,11 @@ __global__ void __launch_bounds__(256) merge_states_kernel(const uint8_t* o_in, 
     }
     __syncwarp();  // every lane has read the states' lse values
     if (valid) {
-      const float inv = s > 0.f ? 1.f / s : 0.f;
+      const float inv = s == 0.f ? 0.f : 1.f / s;
 #pragma unroll
       for (int i = 0; i < C::N; ++i) out[i] *= inv;
       C::store(o_out + (r * chunks + chunk) * 16, out);
-      if (chunk == 0 && lse_out) lse_out[r] = s > 0.f ? m + logf(s) : -INFINITY;
+      if (chunk == 0 && lse_out) lse_out[r] = s == 0.f ? -INFINITY : m + logf(s);
     }
   }
 }

@@ -186,3 +186,61 @@ def test_prefill_nan_value_behind_a_weight_of_zero(kind):
     """Queries of 300 times the size: most pieces of a split row weigh nothing beside its largest logits."""
     b = batch([40, 3], [3000, 700], hq=8, hkv=2, seed=14, extra=0)
     check(kind, b, split, [(0, t, 0) for t in (0, 700, 1500, 2300, 2999)] + [(1, 350, 1)], 300.0)
+
+
+# --------------------------------------------------------------------------- states merged by the caller
+@pytest.mark.parametrize("dtype", [BF, FP, torch.float32])
+def test_merged_states(dtype):
+    """Every pair, and every triple, of a finite, an empty and a NaN state: NaN where one is NaN."""
+    import itertools
+    vals = {"finite": (1.5, 0.25), "low": (-2.0, -400.0), "empty": (0.0, -np.inf), "nan": (NAN, NAN)}
+    for n in (2, 3):
+        combos = list(itertools.product(vals, repeat=n))
+        o = torch.tensor([[vals[c[k]][0] for c in combos] for k in range(n)])[:, :, None, None].expand(-1, -1, 2, 128)
+        o = o.to(dtype).contiguous().cuda()                        # [states, rows, heads, dim]
+        lse = torch.tensor([[vals[c[k]][1] for c in combos] for k in range(n)])[:, :, None].expand(-1, -1, 2).contiguous().cuda()
+        outs = []
+        o_n, l_n = torch.empty_like(o[0]), torch.empty_like(lse[0])
+        api.merge_states(o.flatten(0, 1), lse.flatten(0, 1), n, o_n, l_n)
+        outs.append((o_n, l_n))
+        if n == 2:
+            o_2, l_2 = torch.empty_like(o[0]), torch.empty_like(lse[0])
+            api.merge_state(o[0], lse[0], o[1], lse[1], o_2, l_2)
+            outs.append((o_2, l_2))
+        torch.cuda.synchronize()
+        for got, got_lse in outs:
+            got, got_lse = got.float().cpu(), got_lse.cpu()
+            for i, c in enumerate(combos):
+                if "nan" in c:
+                    assert torch.isnan(got[i]).all() and torch.isnan(got_lse[i]).all(), c
+                elif set(c) == {"empty"}:
+                    assert (got[i] == 0).all() and torch.isneginf(got_lse[i]).all(), c
+                else:
+                    top = "finite" if "finite" in c else "low"     # the other's weight is e^-400.25 = 0
+                    assert (got[i] == vals[top][0]).all(), c
+                    want = vals[top][1] + np.log(c.count(top))
+                    assert (got_lse[i] - want).abs().max() <= 2 * np.finfo(np.float32).eps * abs(want), c
+
+
+def test_cascade8_nan_query_beside_an_empty_suffix():
+    """The prefix's NaN state merged with the empty state of a request without a suffix."""
+    prefix = batch([4], [500], seed=12, extra=0)
+    suffix = batch([1] * 4, [0, 40, 0, 7], seed=13, extra=prefix.num_pages)
+    cache = cache_of(suffix)
+    q = prefix.q.cuda()
+    clean = None
+    for nan in (False, True):
+        if nan:
+            q[0, 3, 1], q[1, 2, 0] = NAN, NAN
+        dbs = [runner.DeviceBatch.from_host(x, kv_data=torch.empty(0)) for x in (prefix, suffix)]
+        for db in dbs:
+            db.q = q
+        o, lse = (x.cpu() for x in runner.cascade_kv8(*dbs, cache))
+        torch.cuda.synchronize()
+        if not nan:
+            clean = o, lse
+            assert torch.isfinite(o.float()).all() and torch.isfinite(lse).all()
+    hit = torch.zeros(lse.shape, dtype=torch.bool)
+    hit[0, 3] = hit[1, 2] = True
+    assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
+    assert same_bits(o, clean[0])[~hit].all() and same_bits(lse, clean[1])[~hit].all()
