@@ -524,7 +524,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) decode_kernel(const __gr
 // n-way merge of the partial states of one split (request, kv head) sequence for
 // one head of its group (pair = item * G + head), by the calling warp: lanes over
 // head_dim, the slot loop unrolled so that several partial rows are in flight per
-// lane.  Shared by the decode merge kernel and the mixed batch's merge kernel.
+// lane.  A NaN lse takes the maximum's place (fmaxf alone would pass over it), so it
+// makes every weight, o and lse NaN.  Shared by the decode merge kernel and the mixed
+// batch's merge kernel.
 template <int D, int G, typename T>
 __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair, int lane) {
   constexpr int PER = D / 32;  // dims per lane
@@ -559,8 +561,13 @@ __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair,
   load_rows(0, vals);
   const float l0 = lane < n ? lse_p[static_cast<int64_t>(lane) * G] : -INFINITY;
   float mx = l0;
-  for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, lse_p[static_cast<int64_t>(i) * G]);
-  mx = warp_max(mx);
+  bool nan = l0 != l0;
+  for (int i = lane + 32; i < n; i += 32) {
+    const float l = lse_p[static_cast<int64_t>(i) * G];
+    mx = fmaxf(mx, l);
+    nan |= l != l;
+  }
+  mx = __any_sync(kFull, nan) ? NAN : warp_max(mx);
   float acc[PER];
 #pragma unroll
   for (int v = 0; v < PER; ++v) acc[v] = 0.f;
@@ -587,11 +594,11 @@ __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair,
   }
   const int hq = it.kvh * G + g;
   T* orow = static_cast<T*>(a.o) + (static_cast<int64_t>(it.row) * a.num_qo_heads + hq) * D;
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
 #pragma unroll
   for (int v = 0; v < PER; ++v) orow[lane * PER + v] = from_float<T>(acc[v] * inv);
   if (lane == 0 && a.lse)
-    a.lse[static_cast<int64_t>(it.row) * a.num_qo_heads + hq] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
+    a.lse[static_cast<int64_t>(it.row) * a.num_qo_heads + hq] = wsum == 0.f ? -INFINITY : mx + logf(wsum);
 }
 
 // Launch one decode instance (head_dim, group size and cap chosen at run time).

@@ -244,3 +244,17 @@ def test_cascade8_nan_query_beside_an_empty_suffix():
     hit[0, 3] = hit[1, 2] = True
     assert torch.isnan(o[hit]).all() and torch.isnan(lse[hit]).all()
     assert same_bits(o, clean[0])[~hit].all() and same_bits(lse, clean[1])[~hit].all()
+
+
+# --------------------------------------------------------------------------- decode over the 16-bit cache
+@pytest.mark.parametrize("g,P", [(4, 16), (1, 8), (8, 16), (2, 1), (8, 4)])
+def test_decode16_split(g, P):
+    """Groups of 8 on pages of 8 rows or more run on the prefill kernel."""
+    b = batch([1, 1, 1], [20000, 600, 0], hq=2 * g, hkv=2, P=P, seed=g, extra=0)
+    check("decode16", b, split, [(0, 17000, 0), (1, 0, 1), (1, 599, 0)])
+
+
+def test_decode16_whole_lists_and_in_a_mixed_batch():
+    b = batch([1] * 3, [1, 250, 900], hq=8, hkv=2, seed=5, extra=0)
+    check("decode16", b, whole, [(0, 0, 0), (1, 100, 1), (2, 899, 0)], split_kv=False)
+    check("mixed16", batch([1, 1, 40], [30000, 600, 3000], seed=11, extra=0), split, [(0, 20000, 0), (1, 599, 1)])
