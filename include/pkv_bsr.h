@@ -169,6 +169,9 @@ pkv_status pkv_plan_run(pkv_plan* plan, int batch, const int32_t* qo_indptr_h,
  * The host half of pkv_plan_run: validate the host index arrays and write
  * the plan tables into `host_ws` (ordinary or pinned host memory), with no
  * CUDA call.  pkv_plan_run is this step followed by one asynchronous copy.
+ * The run calls go by the tables that the last pkv_plan_run copied: this call
+ * alone changes nothing for them (pkv_batch_decode_paged_noalloc, which takes the
+ * host tables, goes by it), and they refuse a plan that pkv_plan_run never copied.
  * Prefill and mixed plans keep their working arrays in the plan object and
  * reuse them from call to call (they grow with the largest batch planned).
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_BAD_INDEX, PKV_ERR_WORKSPACE.

@@ -144,7 +144,7 @@ pkv::PackArgs read_packed_copy(const pkv_plan* plan, pkv::PrefillArgs& a, void* 
   pk.err = a.err;
   pk.num_kv_heads = plan->p.num_kv_heads;
   pk.page_size = plan->p.page_size;
-  pk.num_pages = plan->num_pages;
+  pk.num_pages = plan->on_device.num_pages;
   a.kv = pk.packed;
   a.kv_indices = reinterpret_cast<const int32_t*>(tb + plan->L.pk_ids);
   a.page_size = 16;
@@ -181,13 +181,13 @@ cudaError_t launch_prefill_tables(const pkv_plan* plan, const pkv::PrefillArgs& 
     e = scales ? pkv::launch_expand_pages(*pack, scales, p.head_dim, p.dtype, plan->num_sms * 8, s)
                : pkv::launch_pack_pages(*pack, p.head_dim, plan->num_sms * 8, s);
   if (e == cudaSuccess) {
-    const int64_t pages = plan->packed ? plan->max_packed : plan->num_pages;
-    const auto launch = scales && plan->num_merge > 0 ? pkv::launch_prefill8 : pkv::launch_prefill;
-    e = launch(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->total_q, pages, s);
+    const int64_t pages = plan->packed ? plan->max_packed : plan->on_device.num_pages;
+    const auto launch = scales && plan->on_device.num_merge > 0 ? pkv::launch_prefill8 : pkv::launch_prefill;
+    e = launch(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->on_device.total_q, pages, s);
   }
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
   // Over the 8-bit cache: no merge launch without splits, as in its decode.
-  if (e == cudaSuccess && (!scales || plan->num_merge > 0 || maybe_capturing(s)))
+  if (e == cudaSuccess && (!scales || plan->on_device.num_merge > 0 || maybe_capturing(s)))
     e = pkv::launch_prefill_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
   if (e == cudaSuccess) e = release_tables(plan, s);
   return e;
@@ -216,7 +216,7 @@ pkv_status pkv_batch_decode_paged(const pkv_plan* plan, const void* q, const voi
                                   const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                                   const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                   void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_DECODE || plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_DECODE || plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
   if (!q || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_data, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
@@ -234,7 +234,7 @@ pkv_status pkv_batch_decode_paged(const pkv_plan* plan, const void* q, const voi
   cudaError_t e = wait_tables(plan, s);
   if (plan->time_start && e == cudaSuccess) cudaEventRecord(plan->time_start, s);
   if (e == cudaSuccess)
-    e = pkv::launch_decode(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->num_pages, s);
+    e = pkv::launch_decode(a, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->on_device.num_pages, s);
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
   if (e == cudaSuccess) e = pkv::launch_decode_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
   if (e == cudaSuccess) e = release_tables(plan, s);
@@ -245,10 +245,10 @@ static pkv_status prefill_run(const pkv_plan* plan, const void* q, const int32_t
                               const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                               const int32_t* kv_last_page_len_d, const uint8_t* mask, size_t mask_bytes, void* o,
                               float* lse, void* dev_ws, void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_PREFILL || plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_PREFILL || plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
   if (mask) {
     // whole 32-bit words covering every request's [qo_len, kv_len] block
-    if (!aligned(mask, 4) || mask_bytes / 4 < static_cast<size_t>((plan->mask_bits + 31) / 32))
+    if (!aligned(mask, 4) || mask_bytes / 4 < static_cast<size_t>((plan->on_device.mask_bits + 31) / 32))
       return PKV_ERR_INVALID_ARG;
   }
   if (!q || !qo_indptr_d || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
@@ -287,7 +287,7 @@ pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const
                                       const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                                       const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                       void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_DECODE || !plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_DECODE || !plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
   if (!q || !kv8 || !kv8_scales || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   // The exponent bytes are copied in fours.
@@ -303,11 +303,11 @@ pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const
   if (plan->time_start && e == cudaSuccess) cudaEventRecord(plan->time_start, s);
   if (e == cudaSuccess)
     e = pkv::launch_decode8(a, kv8_scales, p.sm_scale, p.head_dim, p.dtype, p.logits_cap > 0.f, plan->grid_ctas,
-                            plan->num_pages, s);
+                            plan->on_device.num_pages, s);
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
   // A plan without split sequences leaves nothing to merge; a graph gets the launch all
   // the same, for the plans it may be replayed with.
-  if (e == cudaSuccess && (plan->num_merge > 0 || maybe_capturing(s)))
+  if (e == cudaSuccess && (plan->on_device.num_merge > 0 || maybe_capturing(s)))
     e = pkv::launch_decode8_merge(a, p.head_dim, p.dtype, plan->merge_grid, s);
   if (e == cudaSuccess) e = release_tables(plan, s);
   return launch_status(e);
@@ -317,7 +317,7 @@ pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, cons
                                        const void* kv8, const uint8_t* kv8_scales, const int32_t* kv_indices_d,
                                        const int32_t* kv_indptr_d, const int32_t* kv_last_page_len_d, void* o,
                                        float* lse, void* dev_ws, void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_PREFILL || !plan->kv8 || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_PREFILL || !plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
   if (!q || !qo_indptr_d || !kv8 || !kv8_scales || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv8, 16) || !aligned(kv8_scales, 4) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
@@ -334,7 +334,7 @@ pkv_status pkv_batch_mixed_paged(const pkv_plan* plan, const void* q, const int3
                                  const void* kv_data, const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                                  const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                  void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_MIXED || !plan->planned) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_MIXED || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
   if (!q || !qo_indptr_d || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_data, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
@@ -357,7 +357,8 @@ pkv_status pkv_batch_mixed_paged(const pkv_plan* plan, const void* q, const int3
   // tables); then one launch merges both halves' split sequences.
   cudaError_t e = cudaSuccess;
   if (plan->time_start) cudaEventRecord(plan->time_start, s);
-  e = pkv::launch_mixed(pa, da, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, pp->total_q, pp->num_pages, s);
+  e = pkv::launch_mixed(pa, da, p.head_dim, plan->group, p.dtype, cap, plan->grid_ctas, plan->on_device.total_q,
+                        plan->on_device.num_pages, s);
   if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
   if (e == cudaSuccess)
     e = pkv::launch_mixed_merge(pa, da, plan->group, p.dtype, std::max(pp->merge_grid, dp->merge_grid), s);

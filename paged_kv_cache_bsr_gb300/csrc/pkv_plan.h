@@ -83,6 +83,15 @@ struct pkv_plan {
   int64_t total_cost = 0;
   size_t used_bytes = 0;
   std::vector<int32_t> work_rows;  // 8 int32 per work entry, for pkv_plan_get_work
+  // The plan whose tables the last pkv_plan_run copied to the device: the run calls go by
+  // it, since pkv_plan_compute alone replaces the fields above and not the tables.
+  struct OnDevice {
+    bool valid = false;
+    int64_t num_pages = 0;
+    int64_t total_q = 0;
+    int64_t mask_bits = 0;
+    int num_merge = 0;
+  } on_device;
   pkv::PlanScratch scratch;
   // The copy of the tables out of the pinned buffer.
   cudaEvent_t copy_done = nullptr;

@@ -1241,6 +1241,7 @@ pkv_status pkv_plan_run(pkv_plan* plan, int batch, const int32_t* qo_indptr_h, c
   if (st != PKV_OK) return st;
   auto s = static_cast<cudaStream_t>(stream);
   bool ok = true;
+  plan->on_device = {true, plan->num_pages, plan->total_q, plan->mask_bits, plan->num_merge};
   if (plan->pipelined) {
     const int r = plan->cur ^ 1;
     auto* dst = static_cast<uint8_t*>(dev_ws) + (r ? plan->L.alt : 0);
@@ -1250,7 +1251,7 @@ pkv_status pkv_plan_run(pkv_plan* plan, int batch, const int32_t* qo_indptr_h, c
          cudaEventRecord(plan->copy_ev[r], plan->copy_stream) == cudaSuccess;
     if (!ok) {
       cudaGetLastError();
-      plan->planned = false;
+      plan->planned = plan->on_device.valid = false;
       return PKV_ERR_CUDA;
     }
     plan->copy_pend[r] = true;
@@ -1269,7 +1270,7 @@ pkv_status pkv_plan_run(pkv_plan* plan, int batch, const int32_t* qo_indptr_h, c
   }
   if (!ok || cudaEventRecord(plan->copy_done, s) != cudaSuccess) {
     cudaGetLastError();
-    plan->planned = false;
+    plan->planned = plan->on_device.valid = false;
     return PKV_ERR_CUDA;
   }
   plan->copy_pending = true;
