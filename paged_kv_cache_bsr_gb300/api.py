@@ -358,9 +358,12 @@ def _int32(*tensors) -> None:
             raise ValueError("page tables, row pointers, positions and error words must be int32")
 
 
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
 def _kv8_tensors(params: Params, kv8, kv8_scales) -> None:
-    if kv8.element_size() != 1 or kv8_scales.dtype is not torch.uint8:
-        raise ValueError("kv8 must hold one byte per element (float8_e4m3fn or uint8) and kv8_scales be uint8")
+    if kv8.dtype not in _CODES or kv8_scales.dtype is not torch.uint8:
+        raise ValueError("kv8 must hold e4m3 codes (float8_e4m3fn or uint8) and kv8_scales be uint8")
     shape = kv8.shape
     if shape[1:] != (2, params.num_kv_heads, params.page_size, params.head_dim) or kv8_scales.shape != shape[:-1]:
         raise ValueError("kv8 must be [num_pages, 2, num_kv_heads, page_size, head_dim] and kv8_scales the same "
