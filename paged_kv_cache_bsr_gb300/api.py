@@ -464,7 +464,8 @@ class Plan:
     for the 8-bit cache (``run`` then takes its scales too).  The device workspace and the
     pinned host staging buffer are allocated once here, with torch, for the
     given limits; ``plan()`` re-plans a new batch into them and ``run()``
-    launches the kernels.
+    launches the kernels.  The workspace comes from the pool of the stream that is
+    current here: keep the plan until its runs on other streams are done.
     """
 
     def __init__(self, kind: int, *, num_qo_heads: int, num_kv_heads: int, head_dim: int, page_size: int,

@@ -3,9 +3,15 @@
 ``DeviceBatch`` moves one paged batch to the GPU; ``decode``, ``prefill``,
 ``cascade`` and ``multi_level_cascade`` plan and launch through ``api.Plan`` and
 return (o, lse) device tensors.  The arithmetic is all in libpkvbsr.so.
+
+A call given a stream allocates what it makes on that stream, as torch does for work on
+the current one: the outputs are good for the caller's current stream once that has
+waited for it, and may be freed there at any time.  The caller's own tensors have to be
+ready on the stream, and to outlive the call's work on it.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 from typing import Optional, Sequence, Tuple
 
@@ -32,6 +38,32 @@ class DeviceBatch:
                            kv_last_page_len=to(b.kv_last_page_len))
 
 
+def _on(stream):
+    """Allocations inside come from the pool of ``stream`` (None: the current one's).  Memory of another
+    stream's pool could still be in use by that stream's earlier work, and a plan made for one call and
+    dropped at its end be handed to that stream's next allocation while the call runs."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _handle(stream)
+        stream = torch.cuda.ExternalStream(handle) if handle else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _handle(stream) -> int:
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
+
+def _returned(stream, *tensors):
+    """Tensors made on ``stream``, kept from reuse until the caller's current stream is done with them too."""
+    if stream is not None:
+        now = torch.cuda.current_stream()
+        if now.cuda_stream != _handle(stream):
+            for t in tensors:
+                t.record_stream(now)
+    return tensors
+
+
 def _limits_of(b, max_batch=None, max_total_q=None, max_kv_pages=None):
     return dict(max_batch=max_batch or max(b.batch, 1),
                 max_total_q=max_total_q or max(b.total_q, 1),
@@ -52,15 +84,19 @@ def plan_batch(plan: api.Plan, b, stream=None, num_pages: Optional[int] = None) 
               kv_indices_h=b.kv_indices, stream=stream)
 
 
+def _outputs(q: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+    return torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+
+
 def decode(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     b = db.host
-    if plan is None:
-        plan = make_plan(b, api.PLAN_DECODE)
-        plan_batch(plan, b, stream)
-    o = torch.empty_like(db.q)
-    lse = torch.empty(db.q.shape[:2], dtype=torch.float32, device=db.q.device)
+    with _on(stream):
+        if plan is None:
+            plan = make_plan(b, api.PLAN_DECODE)
+            plan_batch(plan, b, stream)
+        o, lse = _outputs(db.q)
     plan.run(db.q, db.kv_data, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o, lse, stream=stream)
-    return o, lse
+    return _returned(stream, o, lse)
 
 
 def prefill(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None,
@@ -68,14 +104,14 @@ def prefill(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None,
     """Batch prefill; ``mask`` is an optional packed custom mask on the device
     (``workloads.pack_mask`` layout), applied on top of the batch's causal flag."""
     b = db.host
-    if plan is None:
-        plan = make_plan(b, api.PLAN_PREFILL)
-        plan_batch(plan, b, stream)
-    o = torch.empty_like(db.q)
-    lse = torch.empty(db.q.shape[:2], dtype=torch.float32, device=db.q.device)
+    with _on(stream):
+        if plan is None:
+            plan = make_plan(b, api.PLAN_PREFILL)
+            plan_batch(plan, b, stream)
+        o, lse = _outputs(db.q)
     plan.run(db.q, db.kv_data, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o, lse,
              qo_indptr=db.qo_indptr, mask=mask, stream=stream)
-    return o, lse
+    return _returned(stream, o, lse)
 
 
 def cascade(prefix: DeviceBatch, suffix: DeviceBatch, prefix_plan: Optional[api.Plan] = None,
@@ -99,7 +135,9 @@ def append_kv(db: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor, rope_th
     b = db.host
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
     if rotate_q and q_out is None:
-        q_out = torch.empty_like(db.q)
+        with _on(stream):
+            q_out = torch.empty_like(db.q)
+        _returned(stream, q_out)
     api.append_paged_kv(params, db.qo_indptr, db.kv_indptr, db.kv_indices, db.kv_last_page_len, k_new, v_new,
                         db.kv_data, db.q if rotate_q else None, q_out if rotate_q else None, rope_theta,
                         error=error, stream=stream)
@@ -115,7 +153,9 @@ def append_kv_axes(db: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor, ro
     b = db.host
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
     if rotate_q and q_out is None:
-        q_out = torch.empty_like(db.q)
+        with _on(stream):
+            q_out = torch.empty_like(db.q)
+        _returned(stream, q_out)
     api.append_paged_kv_axes(params, rope, db.qo_indptr, db.kv_indptr, db.kv_indices, db.kv_last_page_len, positions,
                              k_new, v_new, db.kv_data, db.q if rotate_q else None, q_out if rotate_q else None,
                              error=error, stream=stream)
@@ -149,7 +189,9 @@ def append_kv8(db: DeviceBatch, cache: Kv8Cache, k_new: torch.Tensor, v_new: tor
     b = db.host
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
     if rotate_q and q_out is None:
-        q_out = torch.empty_like(db.q)
+        with _on(stream):
+            q_out = torch.empty_like(db.q)
+        _returned(stream, q_out)
     api.append_paged_kv8(params, rope, db.qo_indptr, db.kv_indptr, db.kv_indices, db.kv_last_page_len, positions, k_new,
                          v_new, cache.codes, cache.scales, db.q if rotate_q else None, q_out if rotate_q else None,
                          error=error, stream=stream)
@@ -158,14 +200,14 @@ def append_kv8(db: DeviceBatch, cache: Kv8Cache, k_new: torch.Tensor, v_new: tor
 
 def _run_kv8(kind: int, db: DeviceBatch, cache: Kv8Cache, plan: Optional[api.Plan], stream
              ) -> Tuple[torch.Tensor, torch.Tensor]:
-    if plan is None:
-        plan = make_plan(db.host, kind)
-        plan_batch(plan, db.host, stream, num_pages=cache.num_pages)
-    o = torch.empty_like(db.q)
-    lse = torch.empty(db.q.shape[:2], dtype=torch.float32, device=db.q.device)
+    with _on(stream):
+        if plan is None:
+            plan = make_plan(db.host, kind)
+            plan_batch(plan, db.host, stream, num_pages=cache.num_pages)
+        o, lse = _outputs(db.q)
     plan.run(db.q, cache.codes, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o, lse,
              qo_indptr=db.qo_indptr if kind == api.PLAN_PREFILL_KV8 else None, kv_scales=cache.scales, stream=stream)
-    return o, lse
+    return _returned(stream, o, lse)
 
 
 def decode_kv8(db: DeviceBatch, cache: Kv8Cache, plan: Optional[api.Plan] = None, stream=None
@@ -194,14 +236,14 @@ def mixed(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None) -> Tupl
     call: the plan routes each request by its row count and splits the SMs, and one
     persistent launch runs both halves."""
     b = db.host
-    if plan is None:
-        plan = make_plan(b, api.PLAN_MIXED)
-        plan_batch(plan, b, stream)
-    o = torch.empty_like(db.q)
-    lse = torch.empty(db.q.shape[:2], dtype=torch.float32, device=db.q.device)
+    with _on(stream):
+        if plan is None:
+            plan = make_plan(b, api.PLAN_MIXED)
+            plan_batch(plan, b, stream)
+        o, lse = _outputs(db.q)
     plan.run(db.q, db.kv_data, db.kv_indices, db.kv_indptr, db.kv_last_page_len, o, lse,
              qo_indptr=db.qo_indptr, stream=stream)
-    return o, lse
+    return _returned(stream, o, lse)
 
 
 def levels_mixed(db: DeviceBatch, n_levels: int, plan: Optional[api.Plan] = None, stream=None
@@ -251,17 +293,18 @@ def multi_level_cascade(levels: Sequence[DeviceBatch], plans: Optional[Sequence[
         raise ValueError("multi_level_cascade needs at least one level")
     if plans is None:
         plans = []
-        for db in levels:
-            p = make_plan(db.host, level_kind(db.host))
-            plan_batch(p, db.host, stream)
-            plans.append(p)
+        with _on(stream):
+            for db in levels:
+                p = make_plan(db.host, level_kind(db.host))
+                plan_batch(p, db.host, stream)
+                plans.append(p)
     if len(plans) != len(levels):
         raise ValueError("one plan per level")
     if side_streams is not None and len(side_streams) < len(levels) - 1:
         raise ValueError("one side stream per level after the first")
     q = levels[0].q
-    outs = [(torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=q.device))
-            for _ in levels]
+    with _on(stream):
+        outs = [_outputs(q) for _ in levels]
     main = stream if stream is not None else torch.cuda.current_stream()
 
     def run(i, s):
@@ -290,4 +333,4 @@ def multi_level_cascade(levels: Sequence[DeviceBatch], plans: Optional[Sequence[
     o0, l0 = outs[0]
     for o, lse in outs[1:]:
         api.merge_state(o0, l0, o, lse, o0, l0, stream=main)
-    return o0, l0
+    return _returned(stream, o0, l0)
