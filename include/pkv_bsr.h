@@ -542,7 +542,9 @@ pkv_status pkv_append_paged_kv_axes(const pkv_params* params, const pkv_rope_axe
  * head row s = max(E - 7, 1), E the exponent field (0..254) of the row's largest
  * finite magnitude as a float32, taken before the rotation; the row, turned if it is a
  * key's (in float32, and again in double precision where that may leave a code in
- * doubt), times 2^(127 - s) is rounded to the nearest e4m3, ties to even.
+ * doubt), times 2^(127 - s) is rounded to the nearest e4m3, ties to even.  A turned
+ * element smaller than an eighth of its pair's length may become the second nearest
+ * instead, where the two are equally near to within 2^-21 of that length.
  * The largest element of an unturned row lies in [128, 256) before that, and a
  * turned one below 256 sqrt(2) < 448, the largest e4m3.  Infinite elements become
  * +-448 of their row's scale (NaN where a rotation makes one of them), NaN stays NaN.

@@ -16,7 +16,7 @@
 // position: two integer multiplications, no argument reduction in floating
 // point.  The top 32 bits (1.5e-9 rad) are split into a quadrant and a rest of at
 // most an eighth of a turn, whose sine and cosine come from their Taylor series
-// (remainders 1.8e-9 and 9e-11, below the rounding of the float result).
+// (remainders 1.8e-9 and 1.2e-10, below the rounding of the float result).
 //
 // 8-bit cache.  Each head row (token, kv head, K or V) is stored as e4m3 codes
 // and one power-of-two scale 2^(s - 127), s = max(E - 7, 1) with E the exponent
@@ -144,13 +144,6 @@ __device__ __noinline__ float2 turn_pair_double(float x, float y, int32_t pos, u
   return make_float2(r[0], r[1]);
 }
 
-// Whether a float changed by 16 units of its last place could round to another e4m3:
-// the 20 bits below e4m3's mantissa are that near to half.  (Below 2^-6, the smallest
-// normal e4m3, its steps are wider than this looks at.)
-__device__ __forceinline__ bool near_border(float x) {
-  return ((__float_as_uint(x) + (16u - 0x80000u)) & 0xfffffu) <= 32u;
-}
-
 // Two floats to two e4m3 codes, the first in the low byte: round to nearest even,
 // past +-448 to +-448, NaN to NaN.
 __device__ __forceinline__ uint32_t pack_e4m3(float lo, float hi) {
@@ -163,6 +156,24 @@ __device__ __forceinline__ uint2 pack_e4m3x8(const float2 (&f)[4]) {
   return make_uint2(pack_e4m3(f[0].x, f[0].y) | (pack_e4m3(f[1].x, f[1].y) << 16),
                     pack_e4m3(f[2].x, f[2].y) | (pack_e4m3(f[3].x, f[3].y) << 16));
 }
+
+// Codes of x (1 - 2^-19) and of x (1 + 2^-19).  Where the two are the same, so is that of
+// every value between them.
+__device__ __forceinline__ uint2 pack_e4m3x8_both(const float2 (&x)[4], bool& differ) {
+  float2 lo[4], hi[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    lo[j] = fmul2(x[j], make_float2(1.f - 0x1p-19f, 1.f - 0x1p-19f));
+    hi[j] = fmul2(x[j], make_float2(1.f + 0x1p-19f, 1.f + 0x1p-19f));
+  }
+  const uint2 a = pack_e4m3x8(lo), b = pack_e4m3x8(hi);
+  differ |= a.x != b.x || a.y != b.y;
+  return a;
+}
+__device__ __forceinline__ bool near_border(float x) {
+  return pack_e4m3(x * (1.f - 0x1p-19f), 0.f) != pack_e4m3(x * (1.f + 0x1p-19f), 0.f);
+}
+
 template <typename T>
 __device__ __forceinline__ uint4 pack_16x8(const float2 (&f)[4]) {
   return make_uint4(pack2<T>(f[0].x, f[0].y), pack2<T>(f[1].x, f[1].y), pack2<T>(f[2].x, f[2].y), pack2<T>(f[3].x, f[3].y));
@@ -205,10 +216,10 @@ __device__ __forceinline__ uint32_t row_exponent(const uint4& a, const uint4& b)
 //
 // A key's code depends on which side of a border between two e4m3 values its turned
 // element falls.  A float turn is off by about 2^-23 of the pair's length; elements
-// within 16 units of their float's last place of a border (one in 30000) are turned
-// again in double precision, so elements of at least an eighth of their pair's length
-// get the code of the exact rotation.  (A smaller one may get its second nearest, when
-// the two are equally near to within 2^-21 of the pair's length.)
+// within 2^-19 of their size of a border (one in some 20 000) are turned again in double
+// precision, so elements of at least an eighth of their pair's length get the code of the
+// exact rotation, e4m3's subnormals among them.  (A smaller one may get its second
+// nearest, when the two are equally near to within 2^-21 of the pair's length.)
 template <int D, typename T, bool OUT8>
 __global__ void __launch_bounds__(kAxThreads, 2) append_axes_kernel(const __grid_constant__ AxesArgs a) {
   constexpr int LPH = D / 16;     // lanes per head row
@@ -382,12 +393,15 @@ __global__ void __launch_bounds__(kAxThreads, 2) append_axes_kernel(const __grid
             fa[j] = fmul2(fa[j], km2);
             fb[j] = fmul2(fb[j], km2);
           }
-          if (turns) {
+          uint2 ca, cb;  // the key's codes
+          if (!turns) {
+            ca = pack_e4m3x8(fa);
+            cb = pack_e4m3x8(fb);
+          } else {
             turn(fa, fb);
             bool near = false;
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              near |= near_border(fa[j].x) || near_border(fa[j].y) || near_border(fb[j].x) || near_border(fb[j].y);
+            ca = pack_e4m3x8_both(fa, near);
+            cb = pack_e4m3x8_both(fb, near);
             if (near) {
               float2 ua[4], ub[4];  // unturned
               to_float2x4<T>(x[0], ua);
@@ -405,12 +419,14 @@ __global__ void __launch_bounds__(kAxThreads, 2) append_axes_kernel(const __grid
                   rb = d.y;
                 }
               }
+              ca = pack_e4m3x8(fa);
+              cb = pack_e4m3x8(fb);
             }
           }
           if (r < Hkv) {
             uint8_t* dst = static_cast<uint8_t*>(a.kv) + k_row * D;
-            *reinterpret_cast<uint2*>(dst + off_a) = pack_e4m3x8(fa);
-            *reinterpret_cast<uint2*>(dst + off_b) = pack_e4m3x8(fb);
+            *reinterpret_cast<uint2*>(dst + off_a) = ca;
+            *reinterpret_cast<uint2*>(dst + off_b) = cb;
             to_float2x4<T>(x[2], fa);
             to_float2x4<T>(x[3], fb);
 #pragma unroll
