@@ -524,9 +524,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) decode_kernel(const __gr
 // n-way merge of the partial states of one split (request, kv head) sequence for
 // one head of its group (pair = item * G + head), by the calling warp: lanes over
 // head_dim, the slot loop unrolled so that several partial rows are in flight per
-// lane.  A NaN lse takes the maximum's place (fmaxf alone would pass over it), so it
-// makes every weight, o and lse NaN.  Shared by the decode merge kernel and the mixed
-// batch's merge kernel.
+// lane.  A slot whose lse is NaN has the weight NaN and makes o and lse NaN; fmaxf
+// passes over it, so a pair without any other slot is looked at again.  Shared by the
+// decode merge kernel and the mixed batch's merge kernel.
 template <int D, int G, typename T>
 __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair, int lane) {
   constexpr int PER = D / 32;  // dims per lane
@@ -561,13 +561,8 @@ __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair,
   load_rows(0, vals);
   const float l0 = lane < n ? lse_p[static_cast<int64_t>(lane) * G] : -INFINITY;
   float mx = l0;
-  bool nan = l0 != l0;
-  for (int i = lane + 32; i < n; i += 32) {
-    const float l = lse_p[static_cast<int64_t>(i) * G];
-    mx = fmaxf(mx, l);
-    nan |= l != l;
-  }
-  mx = __any_sync(kFull, nan) ? NAN : warp_max(mx);
+  for (int i = lane + 32; i < n; i += 32) mx = fmaxf(mx, lse_p[static_cast<int64_t>(i) * G]);
+  mx = warp_max(mx);
   float acc[PER];
 #pragma unroll
   for (int v = 0; v < PER; ++v) acc[v] = 0.f;
@@ -591,6 +586,13 @@ __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair,
         }
       }
     }
+  } else {
+    for (int i = 0; i < n; ++i) {
+      const float l = lse_p[static_cast<int64_t>(i) * G];
+      wsum += l == l ? 0.f : l;
+    }
+#pragma unroll
+    for (int v = 0; v < PER; ++v) acc[v] = wsum;  // 0 or NaN
   }
   const int hq = it.kvh * G + g;
   T* orow = static_cast<T*>(a.o) + (static_cast<int64_t>(it.row) * a.num_qo_heads + hq) * D;
