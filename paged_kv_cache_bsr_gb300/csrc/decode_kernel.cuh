@@ -525,8 +525,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, 1) decode_kernel(const __gr
 // one head of its group (pair = item * G + head), by the calling warp: lanes over
 // head_dim, the slot loop unrolled so that several partial rows are in flight per
 // lane.  A slot whose lse is NaN has the weight NaN and makes o and lse NaN; fmaxf
-// passes over it, so a pair without any other slot is looked at again.  Shared by the
-// decode merge kernel and the mixed batch's merge kernel.
+// passes over it, so a pair may have one beside a maximum of -inf, and is summed all the
+// same (against 0).  Shared by the decode merge kernel and the mixed batch's merge kernel.
 template <int D, int G, typename T>
 __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair, int lane) {
   constexpr int PER = D / 32;  // dims per lane
@@ -567,32 +567,24 @@ __device__ __forceinline__ void decode_merge_pair(const DecodeArgs& a, int pair,
 #pragma unroll
   for (int v = 0; v < PER; ++v) acc[v] = 0.f;
   float wsum = 0.f;
-  if (mx != -INFINITY) {
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      // lane j holds the weight of slot i0 + j
-      const float l = i0 == 0 ? l0 : (i0 + lane < n ? lse_p[static_cast<int64_t>(i0 + lane) * G] : -INFINITY);
-      const float w_lane = i0 + lane < n ? fast_exp2((l - mx) * kLog2e) : 0.f;
-      const int cnt = min(32, n - i0);
-      for (int j0 = 0; j0 < cnt; j0 += U) {
-        if (i0 + j0 > 0) load_rows(i0 + j0, vals);
+  const float ref = mx == -INFINITY ? 0.f : mx;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    // lane j holds the weight of slot i0 + j
+    const float l = i0 == 0 ? l0 : (i0 + lane < n ? lse_p[static_cast<int64_t>(i0 + lane) * G] : -INFINITY);
+    const float w_lane = i0 + lane < n ? fast_exp2((l - ref) * kLog2e) : 0.f;
+    const int cnt = min(32, n - i0);
+    for (int j0 = 0; j0 < cnt; j0 += U) {
+      if (i0 + j0 > 0) load_rows(i0 + j0, vals);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const float w = __shfl_sync(kFull, w_lane, (j0 + u) & 31);
-          if (j0 + u < cnt) {
+      for (int u = 0; u < U; ++u) {
+        const float w = __shfl_sync(kFull, w_lane, (j0 + u) & 31);
+        if (j0 + u < cnt) {
 #pragma unroll
-            for (int v = 0; v < PER; ++v) acc[v] = fmaf(w, vals[u][v], acc[v]);
-            wsum += w;
-          }
+          for (int v = 0; v < PER; ++v) acc[v] = fmaf(w, vals[u][v], acc[v]);
+          wsum += w;
         }
       }
     }
-  } else {
-    for (int i = 0; i < n; ++i) {
-      const float l = lse_p[static_cast<int64_t>(i) * G];
-      wsum += l == l ? 0.f : l;
-    }
-#pragma unroll
-    for (int v = 0; v < PER; ++v) acc[v] = wsum;  // 0 or NaN
   }
   const int hq = it.kvh * G + g;
   T* orow = static_cast<T*>(a.o) + (static_cast<int64_t>(it.row) * a.num_qo_heads + hq) * D;

@@ -116,24 +116,18 @@ __global__ void __launch_bounds__(256) merge_states_kernel(const uint8_t* o_in, 
     const int64_t r = base + lane / chunks;
     const bool valid = r < rows;
     float m = -INFINITY;
-    if (valid) {
-      bool nan = false;
-      for (int k = 0; k < n_states; ++k) {
-        const float l = lse_in[k * stride + r];
-        m = fmaxf(m, l);
-        nan |= l != l;
-      }
-      if (nan) m = NAN;
-    }
+    if (valid)
+      for (int k = 0; k < n_states; ++k) m = fmaxf(m, lse_in[k * stride + r]);
+    const float ref = m == -INFINITY ? 0.f : m;  // (a NaN state may be beside it, which fmaxf passes over)
     float out[C::N];
 #pragma unroll
     for (int i = 0; i < C::N; ++i) out[i] = 0.f;
     float s = 0.f;
-    if (valid && m != -INFINITY) {
+    if (valid) {
       for (int k = 0; k < n_states; ++k) {
         const float l = lse_in[k * stride + r];
         if (l != -INFINITY) {  // an empty state adds nothing (its o is not read)
-          const float w = expf(l - m);
+          const float w = expf(l - ref);
           float f[C::N];
           C::load(o_in + ((k * stride + r) * chunks + chunk) * 16, f);
 #pragma unroll

@@ -769,9 +769,9 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
 // Log-sum-exp merge of the chunks' fp32 partial states of one packed row of a
 // query tile whose key range the plan split (pair = item * 256 + row), by the
 // calling warp, lanes over head_dim.  A slot whose lse is NaN has the weight NaN and
-// makes o and lse NaN; fmaxf passes over it, so a row without any other slot is looked
-// at again (a test in the maximum's own loop cost 1 us of 37 over 19 slots a row).
-// Shared by the prefill merge kernel and the mixed batch's merge kernel.
+// makes o and lse NaN; fmaxf passes over it, so a row may have one beside a maximum of
+// -inf, and is summed all the same (against 0).  Shared by the prefill merge kernel and
+// the mixed batch's merge kernel.
 template <typename T>
 __device__ __forceinline__ void prefill_merge_row(const PrefillArgs& a, int pair, int lane, int G) {
   const PrefillMerge it = a.merge[pair / kWR];
@@ -781,32 +781,24 @@ __device__ __forceinline__ void prefill_merge_row(const PrefillArgs& a, int pair
   for (int i = lane; i < it.n_slots; i += 32)
     mx = fmaxf(mx, a.part_lse[static_cast<int64_t>(it.slot_begin + i) * kWR + r]);
   mx = warp_max(mx);
+  const float ref = mx == -INFINITY ? 0.f : mx;
   float acc[4] = {0.f, 0.f, 0.f, 0.f};
   float wsum = 0.f;
-  if (mx != -INFINITY) {
-    // The row loads do not wait for the weights: a slot whose keys the row does not
-    // see (lse -inf; its o may be 0 times a NaN) is dropped by a select after its load,
-    // not by a branch before it.
+  // The row loads do not wait for the weights: a slot whose keys the row does not
+  // see (lse -inf; its o may be 0 times a NaN) is dropped by a select after its load,
+  // not by a branch before it.
 #pragma unroll 4
-    for (int i = 0; i < it.n_slots; ++i) {
-      const int64_t row = static_cast<int64_t>(it.slot_begin + i) * kWR + r;
-      const float4 v = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
-      const float l = a.part_lse[row];
-      const float w = fast_exp2((l - mx) * kLog2e);
-      const bool use = l != -INFINITY;
-      acc[0] = use ? fmaf(w, v.x, acc[0]) : acc[0];
-      acc[1] = use ? fmaf(w, v.y, acc[1]) : acc[1];
-      acc[2] = use ? fmaf(w, v.z, acc[2]) : acc[2];
-      acc[3] = use ? fmaf(w, v.w, acc[3]) : acc[3];
-      wsum += use ? w : 0.f;
-    }
-  } else {
-    for (int i = 0; i < it.n_slots; ++i) {
-      const float l = a.part_lse[static_cast<int64_t>(it.slot_begin + i) * kWR + r];
-      wsum += l == l ? 0.f : l;
-    }
-#pragma unroll
-    for (int v = 0; v < 4; ++v) acc[v] = wsum;  // 0 or NaN
+  for (int i = 0; i < it.n_slots; ++i) {
+    const int64_t row = static_cast<int64_t>(it.slot_begin + i) * kWR + r;
+    const float4 v = reinterpret_cast<const float4*>(a.part_o + row * kD)[lane];
+    const float l = a.part_lse[row];
+    const float w = fast_exp2((l - ref) * kLog2e);
+    const bool use = l != -INFINITY;
+    acc[0] = use ? fmaf(w, v.x, acc[0]) : acc[0];
+    acc[1] = use ? fmaf(w, v.y, acc[1]) : acc[1];
+    acc[2] = use ? fmaf(w, v.z, acc[2]) : acc[2];
+    acc[3] = use ? fmaf(w, v.w, acc[3]) : acc[3];
+    wsum += use ? w : 0.f;
   }
   const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   const int64_t orow = static_cast<int64_t>(it.q_row0 + r / G) * a.num_qo_heads + it.kvh * G + (r % G);
