@@ -135,8 +135,9 @@ pkv_status pkv_plan_create_host(pkv_plan** out, int kind, const pkv_params* para
 /*
  * Bytes of caller-provided memory the plan needs:
  *  - dev_bytes: device workspace (plan tables, fp32 partial states, error word;
- *    for a prefill plan on pages of fewer than 8 rows also the 16-row-page copy
- *    of up to limits->max_kv_pages pages' keys);
+ *    for a prefill plan on pages of fewer than 8 rows or over the 8-bit cache also
+ *    the 16-row-page copy of up to limits->max_kv_pages pages' keys: 4 * head_dim *
+ *    num_kv_heads bytes a key, each request's keys rounded up to a multiple of 16);
  *  - host_bytes: pinned host staging buffer for the plan tables.
  * Both depend only on params and limits.
  */
@@ -212,8 +213,8 @@ pkv_status pkv_plan_get_work(const pkv_plan* plan, int32_t* out, int64_t capacit
 /*
  * Profiling hook.  While set, every run call on this plan records `start` on
  * its stream just before the main kernel (decode or prefill; for a prefill
- * plan on pages of fewer than 8 rows, before the copy into 16-row pages that
- * precedes it) and `stop` just after it, before the merge kernel, so the caller
+ * plan on pages of fewer than 8 rows or over the 8-bit cache, before the copy into
+ * 16-row pages that precedes it) and `stop` just after it, before the merge kernel, so the caller
  * can time the main kernel alone with cudaEventElapsedTime.  The events (cudaEvent_t) stay the
  * caller's; pass NULL for both to clear.
  * Errors: PKV_ERR_INVALID_ARG.
@@ -229,7 +230,7 @@ pkv_status pkv_plan_set_timing_events(pkv_plan* plan, void* start, void* stop);
  * stream the plan owns, so that copy overlaps the previous call's kernels; the next
  * run call waits for it on its own stream.  Not for CUDA-graph capture of the run
  * calls (the image a run reads alternates).  Call before the first pkv_plan_run;
- * device plans of kind DECODE or PREFILL only.
+ * device plans of any kind but MIXED.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_CUDA.
  */
 pkv_status pkv_plan_set_pipelined(pkv_plan* plan, int on);
@@ -247,7 +248,7 @@ pkv_status pkv_plan_set_pipelined(pkv_plan* plan, int on);
  * Takes effect at the next plan step; the run call is unchanged.  The switch is
  * the CUDA-core decode schedule's: a decode plan on the tensor-core path (see
  * pkv_batch_decode_paged) refuses on = 0.
- * Errors: PKV_ERR_INVALID_ARG (NULL, or not a plan of kind DECODE),
+ * Errors: PKV_ERR_INVALID_ARG (NULL, or not a plan of kind DECODE or DECODE_KV8),
  * PKV_ERR_UNSUPPORTED (on = 0 for a tensor-core decode plan).
  */
 pkv_status pkv_plan_set_split_kv(pkv_plan* plan, int on);
@@ -562,10 +563,15 @@ pkv_status pkv_append_paged_kv8(const pkv_params* params, const pkv_rope_axes* r
  * pkv_batch_decode_paged computes, with K and V the values that kv8 and kv8_scales
  * stand for.  q and o are of params->dtype; page sizes, groups, head_dims,
  * split-KV, the plan's workspaces, capture and the error word as there (every group
- * runs the same kernel, and one-row pages need no tensor map).  Slots past
- * kv_last_page_len are not read.  Products are exact in the tensor cores' fp16
- * operands, with fp32 sums: queries keep 11 significant bits relative to their row's
- * largest element, probabilities 11 bits.
+ * runs the same kernel, and one-row pages need no tensor map).  Codes past
+ * kv_last_page_len are not read.  Exponent bytes are read sixteen at a time (pages of a
+ * multiple of 16 rows) or in the aligned groups of four that hold one that counts, so
+ * further bytes of kv8_scales are read with them, of whatever slot, head or page is next
+ * to them (not past the pool's end); they have no part in the result, but another stream
+ * that writes them meanwhile races with the read.  Products
+ * are exact in the tensor cores' fp16 operands, with fp32 sums: queries keep 11
+ * significant bits relative to their row's largest element, probabilities 11 bits.
+ * A NaN in a query, or in a key or value of the request, gives NaN.
  * Errors: PKV_ERR_INVALID_ARG (a null or misaligned pointer, a plan of another kind or
  * not planned), PKV_ERR_UNSUPPORTED (a pool of 2^32 - 1 head rows or more),
  * PKV_ERR_CUDA.
@@ -580,11 +586,18 @@ pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const
  * pkv_batch_prefill_paged computes (ragged query rows, causal or not; with causal = 0
  * also rows against states of another length, and the shared-prefix half of cascade
  * attention), with K and V the values that kv8 and kv8_scales stand for.  Built for
- * head_dim 128, groups 1/2/4/8 and every page size.  The keys and values that the batch
- * names are first expanded, exactly, into 16-row pages of params->dtype in the device
- * workspace (pkv_plan_workspace_bytes counts them: up to limits->max_kv_pages pages'
- * keys), each once however many rows see it; the tensor-core kernel reads those.
- * Values past fp16's range become infinite when dtype is PKV_F16.
+ * head_dim 128, groups 1/2/4/8 and every page size.  The keys and values of each
+ * request's page list are first expanded into 16-row pages of params->dtype in the device
+ * workspace, each once however many rows of the request see it (a page that several
+ * requests list, once for each); the tensor-core kernel reads those.  The copy takes 512 *
+ * num_kv_heads bytes a key, about twice the cache's own (pkv_plan_workspace_bytes).
+ * Expansion is exact within the type's range: values past it become infinite, and those
+ * below its subnormals' step (2^-24 for PKV_F16, 2^-133 for PKV_BF16) are rounded.
+ * Probabilities are rounded to params->dtype for the second product, as by
+ * pkv_batch_prefill_paged: 8 significant bits with PKV_BF16, 11 with PKV_F16; sums are
+ * fp32.  A NaN in a query or in a key or value that a row sees gives NaN.  A value that is
+ * NaN or infinite may make NaN also of rows of its 128-key block that do not see it (0
+ * times it); a key's does not.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
  */
 pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, const int32_t* qo_indptr_d,

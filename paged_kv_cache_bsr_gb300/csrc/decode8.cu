@@ -40,7 +40,7 @@
 //    through shared memory; longer ones are split over the card and merged by a second
 //    kernel (the plan decides, see compute_decode_shared and compute_decode_heads).
 // Measured (head_dim 128, 8 kv heads, page 16, call with its merge): 64 requests of 8192
-// tokens 164 - 168 us, 96 - 98 % of measured HBM bandwidth at groups 1, 4 and 8 alike;
+// tokens 163, 165 and 169 us at groups 1, 4 and 8, 99, 98 and 96 % of measured HBM bandwidth;
 // of 512 to 4096 tokens 48.5 us, 82 %, where about 8 us go to the launches, the chain of
 // table reads before the first tile and the merge.
 #include <cuda_runtime.h>

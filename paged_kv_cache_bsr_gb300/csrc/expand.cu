@@ -2,8 +2,8 @@
 // into 16-row pages of a plan's workspace for the tensor-core prefill kernel.
 //
 // value = e4m3(code) * 2^(s - 127): 4 significant bits and a power of two, so the
-// bf16 (or, within its range, fp16) value is exact and the prefill over the copy
-// computes with the cache's own values.  One pass over the batch's keys, whatever the
+// 16-bit value is exact within the type's range (past it infinite, below its subnormals'
+// step rounded) and the prefill over the copy computes with the cache's own values.  One pass over the batch's keys, whatever the
 // number of query rows: 1 byte read and 2 written per element.  32-byte stores matter
 // most: with two 16-byte stores per lane, each of which fills half of every sector, a
 // batch of 15 000 tokens x 8 kv heads took 25 us, with whole sectors 16 us.
