@@ -55,6 +55,26 @@ pkv_status check_device(const pkv_plan* plan) {
   return cur == plan->device ? PKV_OK : PKV_ERR_INVALID_ARG;
 }
 
+// Whether work on `s` may be going into a graph.
+bool maybe_capturing(cudaStream_t s) {
+  cudaStreamCaptureStatus st = cudaStreamCaptureStatusActive;
+  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
+    cudaGetLastError();
+    return true;
+  }
+  return st != cudaStreamCaptureStatusNone;
+}
+
+// Tensors without elements have no address: a batch without query rows may come without
+// q and o (nothing is launched), and one without keys without kv_indices.  Not into a
+// graph, which may be replayed with other batches.
+bool no_rows(const pkv_plan* plan, const void* q, const void* o, void* stream) {
+  return plan->on_device.total_q == 0 && !q && !o && !maybe_capturing(static_cast<cudaStream_t>(stream));
+}
+bool no_table(const pkv_plan* plan, const int32_t* kv_indices_d, void* stream) {
+  return !kv_indices_d && (plan->on_device.kv_pages > 0 || maybe_capturing(static_cast<cudaStream_t>(stream)));
+}
+
 // Offset of the table image the next run reads (pipelined plans alternate two).
 size_t table_off(const pkv_plan* plan) { return (plan->pipelined && plan->cur) ? plan->L.alt : 0; }
 
@@ -151,16 +171,6 @@ pkv::PackArgs read_packed_copy(const pkv_plan* plan, pkv::PrefillArgs& a, void* 
   return pk;
 }
 
-// Whether work on `s` may be going into a graph.
-bool maybe_capturing(cudaStream_t s) {
-  cudaStreamCaptureStatus st = cudaStreamCaptureStatusActive;
-  if (cudaStreamIsCapturing(s, &st) != cudaSuccess) {
-    cudaGetLastError();
-    return true;
-  }
-  return st != cudaStreamCaptureStatusNone;
-}
-
 pkv_status launch_status(cudaError_t e) {
   if (e == cudaSuccess) return PKV_OK;
   cudaGetLastError();
@@ -217,7 +227,8 @@ pkv_status pkv_batch_decode_paged(const pkv_plan* plan, const void* q, const voi
                                   const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                   void* stream) {
   if (!plan || plan->kind != PKV_PLAN_DECODE || plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
-  if (!q || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+  if (no_rows(plan, q, o, stream)) return PKV_OK;
+  if (!q || !kv_data || no_table(plan, kv_indices_d, stream) || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_data, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
       !aligned(kv_indices_d, 4) || !aligned(kv_indptr_d, 4) || (lse && !aligned(lse, 4)))
@@ -246,12 +257,14 @@ static pkv_status prefill_run(const pkv_plan* plan, const void* q, const int32_t
                               const int32_t* kv_last_page_len_d, const uint8_t* mask, size_t mask_bytes, void* o,
                               float* lse, void* dev_ws, void* stream) {
   if (!plan || plan->kind != PKV_PLAN_PREFILL || plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
+  if (no_rows(plan, q, o, stream)) return PKV_OK;
   if (mask) {
     // whole 32-bit words covering every request's [qo_len, kv_len] block
     if (!aligned(mask, 4) || mask_bytes / 4 < static_cast<size_t>((plan->on_device.mask_bits + 31) / 32))
       return PKV_ERR_INVALID_ARG;
   }
-  if (!q || !qo_indptr_d || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+  if (!q || !qo_indptr_d || !kv_data || no_table(plan, kv_indices_d, stream) || !kv_indptr_d ||
+      !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_data, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
       !aligned(kv_indices_d, 4) || (lse && !aligned(lse, 4)))
@@ -288,7 +301,9 @@ pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const
                                       const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                       void* stream) {
   if (!plan || plan->kind != PKV_PLAN_DECODE || !plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
-  if (!q || !kv8 || !kv8_scales || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+  if (no_rows(plan, q, o, stream)) return PKV_OK;
+  if (!q || !kv8 || !kv8_scales || no_table(plan, kv_indices_d, stream) || !kv_indptr_d || !kv_last_page_len_d ||
+      !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   // The exponent bytes are copied in fours.
   if (!aligned(q, 16) || !aligned(kv8, 16) || !aligned(kv8_scales, 4) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
@@ -318,7 +333,9 @@ pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, cons
                                        const int32_t* kv_indptr_d, const int32_t* kv_last_page_len_d, void* o,
                                        float* lse, void* dev_ws, void* stream) {
   if (!plan || plan->kind != PKV_PLAN_PREFILL || !plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
-  if (!q || !qo_indptr_d || !kv8 || !kv8_scales || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+  if (no_rows(plan, q, o, stream)) return PKV_OK;
+  if (!q || !qo_indptr_d || !kv8 || !kv8_scales || no_table(plan, kv_indices_d, stream) || !kv_indptr_d ||
+      !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv8, 16) || !aligned(kv8_scales, 4) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
       !aligned(kv_indices_d, 4) || (lse && !aligned(lse, 4)))
@@ -335,7 +352,9 @@ pkv_status pkv_batch_mixed_paged(const pkv_plan* plan, const void* q, const int3
                                  const int32_t* kv_last_page_len_d, void* o, float* lse, void* dev_ws,
                                  void* stream) {
   if (!plan || plan->kind != PKV_PLAN_MIXED || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
-  if (!q || !qo_indptr_d || !kv_data || !kv_indices_d || !kv_indptr_d || !kv_last_page_len_d || !o || !dev_ws)
+  if (no_rows(plan, q, o, stream)) return PKV_OK;
+  if (!q || !qo_indptr_d || !kv_data || no_table(plan, kv_indices_d, stream) || !kv_indptr_d ||
+      !kv_last_page_len_d || !o || !dev_ws)
     return PKV_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_data, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
       !aligned(kv_indices_d, 4) || !aligned(kv_indptr_d, 4) || (lse && !aligned(lse, 4)))

@@ -73,6 +73,7 @@ struct pkv_plan {
   bool planned = false;
   int batch = 0;
   int64_t num_pages = 0;
+  int64_t kv_pages = 0;     // entries of kv_indices
   int64_t total_q = 0;
   int64_t mask_bits = 0;    // prefill: sum over requests of qo_len * kv_len (custom-mask size)
   int active_workers = 0;
@@ -88,6 +89,7 @@ struct pkv_plan {
   struct OnDevice {
     bool valid = false;
     int64_t num_pages = 0;
+    int64_t kv_pages = 0;
     int64_t total_q = 0;
     int64_t mask_bits = 0;
     int num_merge = 0;

@@ -1224,6 +1224,7 @@ pkv_status pkv_plan_compute(pkv_plan* plan, int batch, const int32_t* qo_indptr_
     reinterpret_cast<PlanHeader*>(host + plan->L.header)->num_pages = plan->packed ? plan->max_packed : num_pages;
   plan->batch = batch;
   plan->num_pages = num_pages;
+  plan->kv_pages = kv_indptr_h[batch];
   plan->total_q = plan->kind == PKV_PLAN_DECODE ? batch : (batch > 0 ? qo_indptr_h[batch] : 0);
   plan->planned = true;
   return PKV_OK;
@@ -1241,7 +1242,7 @@ pkv_status pkv_plan_run(pkv_plan* plan, int batch, const int32_t* qo_indptr_h, c
   if (st != PKV_OK) return st;
   auto s = static_cast<cudaStream_t>(stream);
   bool ok = true;
-  plan->on_device = {true, plan->num_pages, plan->total_q, plan->mask_bits, plan->num_merge};
+  plan->on_device = {true, plan->num_pages, plan->kv_pages, plan->total_q, plan->mask_bits, plan->num_merge};
   if (plan->pipelined) {
     const int r = plan->cur ^ 1;
     auto* dst = static_cast<uint8_t*>(dev_ws) + (r ? plan->L.alt : 0);
