@@ -521,7 +521,7 @@ typedef struct {
  *               position on axis x is entry x * nnz + t.  NULL: a token's place in its
  *               request (kv_len_b - n_b + i) on every axis.  They turn the rows and
  *               have no part in where a token is stored.
- * q_in, q_out : both NULL or neither.
+ * q_in, q_out : both NULL or neither; the same, or without overlap.
  * The frequencies are held in double precision and the angles computed modulo a turn
  * in 64-bit fixed point, without a rounding for any int32 position.  As there, no two
  * new tokens may have the same slot.  Errors: as pkv_append_paged_kv; PKV_ERR_INVALID_ARG also for a rotation

@@ -552,6 +552,10 @@ pkv_status append_axes(const pkv_params* p, const pkv_rope_axes* rope, int batch
       !aligned4(append_indptr_d) || !aligned4(kv_indptr_d) || !aligned4(kv_indices_d) ||
       !aligned4(kv_last_page_len_d) || !aligned4(positions_d) || !aligned4(error_d) || !aligned4(scales))
     return PKV_ERR_INVALID_ARG;
+  // Rows are read ahead of those that are written, so they turn in place or elsewhere.
+  const auto from = reinterpret_cast<uintptr_t>(q_in), to = reinterpret_cast<uintptr_t>(q_out);
+  const uint64_t q_bytes = static_cast<uint64_t>(nnz) * p->num_qo_heads * p->head_dim * 2;
+  if (from != to && (from < to ? to - from : from - to) < q_bytes) return PKV_ERR_INVALID_ARG;
   a.append_indptr = append_indptr_d;
   a.kv_indptr = kv_indptr_d;
   a.kv_indices = kv_indices_d;
