@@ -259,7 +259,8 @@ pkv_status pkv_plan_set_split_kv(pkv_plan* plan, int on);
  * q and o: [batch, Hq, d]; lse: [batch, Hq] fp32 (may be NULL).
  * For a batch without requests q, o and lse may be NULL (nothing is launched then), and
  * kv_indices_d for one in which no request holds a key, here and in the other run calls
- * (q and o there for a batch without query rows); not while the stream is captured.
+ * (q and o there for a batch without query rows), but for the _noalloc one; not while the
+ * stream is captured.
  * kv_indptr_d and kv_last_page_len_d must hold the values the plan saw; the
  * kernels read page ids from kv_indices_d and check kv_indptr_d against the
  * plan (a mismatch sets the device error word and skips the work).
