@@ -208,7 +208,7 @@ def run(state):
     if own:
         from paged_kv_cache_bsr_gb300 import api
         if op == "ragged":
-            s["plan"].run_ragged(s["q"], s["k"], s["v"], s["o"], s["lse"], qo_indptr=s["rows_d"], kv_indptr=s["kv_d"])
+            s["plan"].run_ragged(s["q"], s["k"], s["v"], s["o"], s["lse"])
         elif op == "weights":
             one = s["case"]["qo_hi"] == 1
             api.add_key_weights(s["params"], s["indptr_d"], s["indices"], s["last_d"], s["q"], s["lse"], s["cache"], s["weights"],
