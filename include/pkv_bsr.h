@@ -77,7 +77,8 @@ typedef enum {
     PKV_PLAN_PREFILL = 1,
     PKV_PLAN_MIXED = 2,
     PKV_PLAN_DECODE_KV8 = 3,  /* pkv_batch_decode_paged_kv8: the same over the 8-bit cache */
-    PKV_PLAN_PREFILL_KV8 = 4  /* pkv_batch_prefill_paged_kv8 */
+    PKV_PLAN_PREFILL_KV8 = 4, /* pkv_batch_prefill_paged_kv8 */
+    PKV_PLAN_PREFILL_RAGGED = 5  /* pkv_batch_prefill_ragged: keys and values packed, not in pages */
 } pkv_plan_kind;
 
 /* Problem description shared by plan and run calls. */
@@ -85,7 +86,7 @@ typedef struct {
     int num_qo_heads;   /* Hq, a multiple of num_kv_heads */
     int num_kv_heads;   /* Hkv */
     int head_dim;       /* d: 64 or 128 */
-    int page_size;      /* P: 1..16, or a multiple of 16 */
+    int page_size;      /* P: 1..16, or a multiple of 16 (PKV_PLAN_PREFILL_RAGGED: 1) */
     int dtype;          /* pkv_dtype of q, kv_data and o: PKV_F16 or PKV_BF16 */
     float sm_scale;     /* usually 1/sqrt(head_dim) */
     float logits_cap;   /* <= 0: off */
@@ -608,6 +609,42 @@ pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, cons
                                        const void* kv8, const uint8_t* kv8_scales, const int32_t* kv_indices_d,
                                        const int32_t* kv_indptr_d, const int32_t* kv_last_page_len_d, void* o,
                                        float* lse, void* dev_ws, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Whole prompts, and caches of bounded length.
+ *
+ * The FlashInfer pages have no counterpart of these calls.
+ */
+
+/*
+ * Batch prefill over keys and values that are not in pages: packed rows, request
+ * behind request, as the projections of a batch of prompts (or of an encoder's states)
+ * leave them.  What pkv_batch_prefill_paged computes, on a plan of kind
+ * PKV_PLAN_PREFILL_RAGGED.
+ *  - The plan: params->page_size must be 1; pkv_plan_run takes key counts' row pointer as
+ *    kv_indptr_h (request b's keys are rows kv_indptr[b] .. kv_indptr[b+1]-1 of k and v),
+ *    the rows of k and v as num_pages, and ignores kv_indices_h and kv_last_page_len_h
+ *    (NULL).  limits->max_kv_pages bounds the keys per call.  The row pointers travel in
+ *    the plan's tables: the run call takes none.
+ *  - q [total_q, Hq, d], k and v [num_pages, Hkv, d] of params->dtype; q_stride, k_stride
+ *    and v_stride are the elements from one row to the next: at least heads * d, a
+ *    multiple of 8, at most 2^38, so all three may be views of one projection's output.
+ *    o and lse are dense.  k and v may be NULL for a batch without keys (not while the
+ *    stream is captured).
+ *  - Built for head_dim 128 and groups 1/2/4/8.  Causal or not (params->causal), rows and
+ *    keys of a request counted apart: a row that sees no key gets o = 0, lse = -inf.
+ *  - Rows of k and v of other requests have no part in a request's result, NaN or not.  A
+ *    value that is NaN or infinite may make NaN also of rows of its request that share its
+ *    128-key block and do not see it (0 times it); a key's does not.
+ * The tensor maps are built at launch from q, k, v, their strides, the total query rows
+ * and the rows of k and v of the current plan: a captured graph can be replayed after
+ * re-planning a batch with the same ones.
+ * Errors: PKV_ERR_INVALID_ARG (a null or misaligned pointer, a stride out of range, a plan
+ * of another kind or not planned), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.
+ */
+pkv_status pkv_batch_prefill_ragged(const pkv_plan* plan, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, void* o, float* lse,
+                                    void* dev_ws, void* stream);
 
 /*
  * Read (and, with clear != 0, reset) the device error word a plan's kernels

@@ -24,6 +24,7 @@ PKV_OK = 0
 PKV_F16, PKV_BF16, PKV_F32 = 0, 1, 2
 PLAN_DECODE, PLAN_PREFILL, PLAN_MIXED = 0, 1, 2
 PLAN_DECODE_KV8, PLAN_PREFILL_KV8 = 3, 4  # over the 8-bit cache
+PLAN_PREFILL_RAGGED = 5  # over packed keys and values
 
 _DTYPES = {torch.float16: PKV_F16, torch.bfloat16: PKV_BF16, torch.float32: PKV_F32}
 _STORED = {PKV_F16: torch.float16, PKV_BF16: torch.bfloat16}
@@ -68,7 +69,7 @@ EXPORTS = [
     "pkv_plan_set_timing_events", "pkv_batch_decode_paged_noalloc", "pkv_append_paged_kv",
     "pkv_batch_prefill_paged_masked", "pkv_batch_mixed_paged", "pkv_plan_set_pipelined",
     "pkv_plan_set_split_kv", "pkv_append_paged_kv_axes", "pkv_append_paged_kv8", "pkv_batch_decode_paged_kv8",
-    "pkv_batch_prefill_paged_kv8",
+    "pkv_batch_prefill_paged_kv8", "pkv_batch_prefill_ragged",
 ]
 
 
@@ -117,6 +118,7 @@ def load(path: Optional[str] = None):
                                            vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "pkv_batch_decode_paged_kv8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "pkv_batch_prefill_paged_kv8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
+            "pkv_batch_prefill_ragged": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -438,6 +440,25 @@ def batch_prefill_paged_kv8(h, q, qo_indptr, kv8, kv8_scales, kv_indices, kv_ind
         _stream(stream)), "pkv_batch_prefill_paged_kv8")
 
 
+def _rows(x):
+    """(address, elements from row to row) of rows [n, heads, head_dim] whose heads lie dense: a view of a
+    projection's output may have wider rows."""
+    n, heads, d = x.shape
+    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+        raise ValueError("tensors must be on the current CUDA device")
+    if (d > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != d):
+        raise ValueError("the heads of a row must lie one behind another")
+    return x.data_ptr(), x.stride(0) if n > 1 else heads * d
+
+
+def batch_prefill_ragged(h, q, k, v, o, lse, dev_ws, stream=None) -> None:
+    """Prefill over packed keys and values, on a plan of kind PLAN_PREFILL_RAGGED.  q, k and v are
+    [rows, heads, head_dim] and may be views with wider rows (``_rows``); o and lse are dense."""
+    op, lp, wp = _ptrs((o, lse, dev_ws))
+    _check((_lib or load()).pkv_batch_prefill_ragged(h, *_rows(q), *_rows(k), *_rows(v), op, lp, wp, _stream(stream)),
+           "pkv_batch_prefill_ragged")
+
+
 def plan_set_timing_events(h, start=None, stop=None) -> None:
     """Record torch.cuda.Event ``start``/``stop`` around the main kernel of later run calls."""
     def handle(ev):
@@ -460,8 +481,9 @@ def get_device_error(h, dev_ws, clear: bool = False, stream=None) -> int:
 class Plan:
     """A plan handle plus the caller-side buffers it needs.
 
-    ``kind`` is PLAN_DECODE, PLAN_PREFILL, PLAN_MIXED, or PLAN_DECODE_KV8 / PLAN_PREFILL_KV8
-    for the 8-bit cache (``run`` then takes its scales too).  The device workspace and the
+    ``kind`` is PLAN_DECODE, PLAN_PREFILL, PLAN_MIXED, PLAN_DECODE_KV8 / PLAN_PREFILL_KV8
+    for the 8-bit cache (``run`` then takes its scales too), or PLAN_PREFILL_RAGGED for keys and
+    values outside pages (page_size 1, ``max_kv_pages`` and ``kv_indptr`` count keys, ``run_ragged``).  The device workspace and the
     pinned host staging buffer are allocated once here, with torch, for the
     given limits; ``plan()`` re-plans a new batch into them and ``run()``
     launches the kernels.  The workspace comes from the pool of the stream that is
@@ -500,11 +522,13 @@ class Plan:
 
     def plan(self, kv_indptr_h, kv_last_page_len_h, num_pages: int, *, qo_indptr_h=None, kv_indices_h=None,
              stream=None) -> None:
+        """Plan a batch.  PLAN_PREFILL_RAGGED: kv_indptr_h counts keys, kv_last_page_len_h is None, and
+        num_pages the rows of k and v."""
         batch = int(torch.as_tensor(kv_indptr_h).numel()) - 1
         plan_run(self.handle, batch, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h, num_pages,
                  self.dev_ws, self.host_ws, stream)
         self.num_pages = int(num_pages)
-        if self.kind in (PLAN_DECODE_KV8, PLAN_PREFILL_KV8):  # what run() checks its tensors against
+        if self.kind in (PLAN_DECODE_KV8, PLAN_PREFILL_KV8, PLAN_PREFILL_RAGGED):  # what run() checks its tensors against
             self.batch = batch
             self.total_q = batch if self.kind == PLAN_DECODE_KV8 else int(torch.as_tensor(qo_indptr_h)[-1])
             self.kv_pages = int(torch.as_tensor(kv_indptr_h)[-1])
@@ -528,6 +552,8 @@ class Plan:
 
     def run(self, q, kv_data, kv_indices, kv_indptr, kv_last_page_len, o, lse=None, *, qo_indptr=None,
             mask=None, kv_scales=None, stream=None) -> None:
+        if self.kind == PLAN_PREFILL_RAGGED:
+            raise ValueError("a plan over packed keys and values runs with run_ragged")
         if (kv_scales is not None) != (self.kind in (PLAN_DECODE_KV8, PLAN_PREFILL_KV8)):
             raise ValueError("kv_scales go with a plan for the 8-bit cache")
         if kv_scales is not None:
@@ -554,6 +580,22 @@ class Plan:
         else:
             batch_prefill_paged(self.handle, q, qo_indptr, kv_data, kv_indices, kv_indptr, kv_last_page_len, o,
                                 lse, self.dev_ws, stream)
+
+    def run_ragged(self, q, k, v, o, lse=None, *, stream=None) -> None:
+        """Attention over packed keys and values (kind PLAN_PREFILL_RAGGED): q [total_q, Hq, d], k and v
+        [rows, Hkv, d], whose rows may be views of wider ones."""
+        if self.kind != PLAN_PREFILL_RAGGED:
+            raise ValueError("run_ragged needs a plan over packed keys and values")
+        p = self.params
+        dtype, kv_rows = _STORED[p.dtype], (self.num_pages, p.num_kv_heads, p.head_dim)
+        shape = (self.total_q, p.num_qo_heads, p.head_dim)
+        if q.shape != shape or o.shape != shape or q.dtype is not dtype or o.dtype is not dtype:
+            raise ValueError("q and o must be [rows of the plan, num_qo_heads, head_dim] of the plan's dtype")
+        if k.shape != kv_rows or v.shape != kv_rows or k.dtype is not dtype or v.dtype is not dtype:
+            raise ValueError("k and v must be [rows of the plan, num_kv_heads, head_dim] of the plan's dtype")
+        if lse is not None and (lse.shape != shape[:2] or lse.dtype is not torch.float32):
+            raise ValueError("lse must be [rows of the plan, num_qo_heads] float32")
+        batch_prefill_ragged(self.handle, q, k, v, o, lse, self.dev_ws, stream)
 
     def info(self) -> PlanInfo:
         return plan_get_info(self.handle)

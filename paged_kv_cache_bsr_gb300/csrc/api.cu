@@ -256,7 +256,8 @@ static pkv_status prefill_run(const pkv_plan* plan, const void* q, const int32_t
                               const int32_t* kv_indices_d, const int32_t* kv_indptr_d,
                               const int32_t* kv_last_page_len_d, const uint8_t* mask, size_t mask_bytes, void* o,
                               float* lse, void* dev_ws, void* stream) {
-  if (!plan || plan->kind != PKV_PLAN_PREFILL || plan->kv8 || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
+  if (!plan || plan->kind != PKV_PLAN_PREFILL || plan->kv8 || plan->ragged || !plan->on_device.valid)
+    return PKV_ERR_INVALID_ARG;
   if (no_rows(plan, q, o, stream)) return PKV_OK;
   if (mask) {
     // whole 32-bit words covering every request's [qo_len, kv_len] block
@@ -294,6 +295,40 @@ pkv_status pkv_batch_prefill_paged_masked(const pkv_plan* plan, const void* q, c
   if (!packed_mask_d) return PKV_ERR_INVALID_ARG;
   return prefill_run(plan, q, qo_indptr_d, kv_data, kv_indices_d, kv_indptr_d, kv_last_page_len_d, packed_mask_d,
                      mask_bytes, o, lse, dev_ws, stream);
+}
+
+pkv_status pkv_batch_prefill_ragged(const pkv_plan* plan, const void* q, int64_t q_stride, const void* k,
+                                    int64_t k_stride, const void* v, int64_t v_stride, void* o, float* lse,
+                                    void* dev_ws, void* stream) {
+  if (!plan || !plan->ragged || !plan->on_device.valid) return PKV_ERR_INVALID_ARG;
+  if (no_rows(plan, q, o, stream)) return PKV_OK;
+  const pkv_params& p = plan->p;
+  auto s = static_cast<cudaStream_t>(stream);
+  const bool no_keys = plan->on_device.kv_pages == 0 && !k && !v && !maybe_capturing(s);
+  if (!q || ((!k || !v) && !no_keys) || !o || !dev_ws) return PKV_ERR_INVALID_ARG;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(o, 16) || !aligned(dev_ws, 256) ||
+      (lse && !aligned(lse, 4)))
+    return PKV_ERR_INVALID_ARG;
+  // A row holds its heads and starts on 16 bytes; a tensor map's strides stay below 2^40 bytes.
+  const int64_t d = p.head_dim, q_min = d * p.num_qo_heads, kv_min = d * p.num_kv_heads, most = int64_t{1} << 38;
+  for (int64_t x : {q_stride, k_stride, v_stride})
+    if (x % 8 || x > most) return PKV_ERR_INVALID_ARG;
+  if (q_stride < q_min || k_stride < kv_min || v_stride < kv_min) return PKV_ERR_INVALID_ARG;
+  pkv_status st = check_device(plan);
+  if (st != PKV_OK) return st;
+  const pkv::PrefillArgs a = prefill_args(plan, dev_ws, q, nullptr, nullptr, nullptr, 0, o, lse);
+  const pkv::RaggedRows r{k, v, q_stride, k_stride, v_stride, plan->on_device.total_q, plan->on_device.num_pages};
+  const bool split = plan->on_device.num_merge > 0 || maybe_capturing(s);
+  cudaError_t e = wait_tables(plan, s);
+  if (plan->time_start && e == cudaSuccess) cudaEventRecord(plan->time_start, s);
+  if (e == cudaSuccess)
+    e = pkv::launch_prefill_ragged(a, r, plan->group, p.dtype, p.logits_cap > 0.f, split, plan->grid_ctas, s);
+  if (plan->time_stop && e == cudaSuccess) cudaEventRecord(plan->time_stop, s);
+  // No merge launch without split tiles; a graph gets it for the plans it may be replayed with.
+  if (e == cudaSuccess && split)
+    e = pkv::launch_prefill_merge(a, p.head_dim, plan->group, p.dtype, plan->merge_grid, s);
+  if (e == cudaSuccess) e = release_tables(plan, s);
+  return launch_status(e);
 }
 
 pkv_status pkv_batch_decode_paged_kv8(const pkv_plan* plan, const void* q, const void* kv8, const uint8_t* kv8_scales,

@@ -170,6 +170,17 @@ cudaError_t launch_expand_pages(const PackArgs& a, const uint8_t* scales, int he
 // split tiles' partial states staged through shared memory.
 cudaError_t launch_prefill8(const PrefillArgs& a, int head_dim, int group, int dtype, bool cap, int grid,
                             int64_t total_q, int64_t num_pages, cudaStream_t stream);
+// Packed queries, keys and values [rows, heads, D], strides in elements from row to row.
+struct RaggedRows {
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;
+  int64_t total_q, total_kv;
+};
+// The prefill kernel over packed keys and values (a.kv, a.kv_indices and a.page_size
+// unused), as a dependent of the kernel before it; split: the plan has split tiles.
+cudaError_t launch_prefill_ragged(const PrefillArgs& a, const RaggedRows& r, int group, int dtype, bool cap, bool split,
+                                  int grid, cudaStream_t stream);
 cudaError_t launch_prefill_merge(const PrefillArgs& a, int head_dim, int group, int dtype, int grid,
                                  cudaStream_t stream);
 

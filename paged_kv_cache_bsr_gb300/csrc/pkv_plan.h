@@ -46,6 +46,9 @@ struct pkv_plan {
   // A plan of kind PKV_PLAN_DECODE_KV8 or PKV_PLAN_PREFILL_KV8: `kind` holds the decode or
   // prefill kind whose tables it makes, and only the 8-bit cache's run calls take it.
   bool kv8 = false;
+  // A plan of kind PKV_PLAN_PREFILL_RAGGED: a prefill plan whose pages are the single rows of
+  // packed keys and values; only pkv_batch_prefill_ragged takes it.
+  bool ragged = false;
   // Fixed grid and table capacities (depend on params and limits only).
   int grid_ctas = 0;
   int workers = 0;

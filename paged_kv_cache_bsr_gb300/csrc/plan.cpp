@@ -63,7 +63,7 @@ bool decode_on_tensor_cores(const pkv_params* p) {
          pkv::prefill_supported(p->head_dim, g, p->dtype, p->page_size);
 }
 
-pkv_status check_params(int kind, bool kv8, const pkv_params* p, const pkv_limits* lim) {
+pkv_status check_params(int kind, bool copied, const pkv_params* p, const pkv_limits* lim) {
   if (!p || !lim) return PKV_ERR_INVALID_ARG;
   if (kind != PKV_PLAN_DECODE && kind != PKV_PLAN_PREFILL && kind != PKV_PLAN_MIXED) return PKV_ERR_INVALID_ARG;
   if (p->num_qo_heads <= 0 || p->num_kv_heads <= 0 || p->num_qo_heads % p->num_kv_heads)
@@ -75,8 +75,9 @@ pkv_status check_params(int kind, bool kv8, const pkv_params* p, const pkv_limit
   const int g = p->num_qo_heads / p->num_kv_heads;
   if (p->dtype != PKV_F16 && p->dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
   if (kind != PKV_PLAN_PREFILL && !pkv::decode_supported(p->head_dim, g, p->dtype)) return PKV_ERR_UNSUPPORTED;
-  // A prefill over the 8-bit cache reads an expanded copy in 16-row pages.
-  if (kind != PKV_PLAN_DECODE && !pkv::prefill_supported(p->head_dim, g, p->dtype, kv8 ? 16 : p->page_size))
+  // A prefill over the 8-bit cache reads an expanded copy in 16-row pages, one over packed
+  // rows no pages.
+  if (kind != PKV_PLAN_DECODE && !pkv::prefill_supported(p->head_dim, g, p->dtype, copied ? 16 : p->page_size))
     return PKV_ERR_UNSUPPORTED;
   if (!is_pow2_group(g)) return PKV_ERR_UNSUPPORTED;
   return PKV_OK;
@@ -115,8 +116,11 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
   *out = nullptr;
   const bool kv8 = kind == PKV_PLAN_DECODE_KV8 || kind == PKV_PLAN_PREFILL_KV8;
   if (kv8) kind = kind == PKV_PLAN_DECODE_KV8 ? PKV_PLAN_DECODE : PKV_PLAN_PREFILL;
-  pkv_status st = check_params(kind, kv8, params, limits);
+  const bool ragged = kind == PKV_PLAN_PREFILL_RAGGED;
+  if (ragged) kind = PKV_PLAN_PREFILL;
+  pkv_status st = check_params(kind, kv8 || ragged, params, limits);
   if (st != PKV_OK) return st;
+  if (ragged && params->page_size != 1) return PKV_ERR_INVALID_ARG;  // kv_indptr counts keys
   // Worker ids (num_sms x kDecodeWarps) fit the 24-bit field of the whole-list decode plan's heap keys.
   if (num_sms <= 0 || num_sms >= (1 << 20)) return PKV_ERR_INVALID_ARG;
   if (kind == PKV_PLAN_MIXED && num_sms < 2) return PKV_ERR_INVALID_ARG;  // one SM for each half at least
@@ -124,6 +128,7 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
   if (!pl) return PKV_ERR_INVALID_ARG;
   pl->kind = kind;
   pl->kv8 = kv8;
+  pl->ragged = ragged;
   pl->p = *params;
   pl->lim = *limits;
   pl->device = device;
@@ -192,7 +197,7 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
     pl->merge_grid = num_sms * 4;
     // Pages of fewer than 8 rows, or of the 8-bit cache: the tensor-core prefill runs
     // over a packed copy in 16-row pages (a request of L keys fills ceil(L / 16) of them).
-    pl->packed = kind == PKV_PLAN_PREFILL && allow_pack && (kv8 || params->page_size < 8);
+    pl->packed = kind == PKV_PLAN_PREFILL && allow_pack && !ragged && (kv8 || params->page_size < 8);
     if (pl->packed) {
       pl->max_packed = ceil_div(static_cast<int64_t>(limits->max_kv_pages) * params->page_size, 16) + limits->max_batch;
       // Packed page ids and the packed copy's row coordinates are 32-bit.
@@ -211,7 +216,7 @@ pkv_status make_plan(pkv_plan** out, int kind, const pkv_params* params, const p
 // Common validation of the host index arrays.
 pkv_status validate(const pkv_plan* pl, int batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
                     const int32_t* kv_indices, const int32_t* kv_last, int64_t num_pages) {
-  if (batch < 0 || !kv_indptr || (batch > 0 && !kv_last)) return PKV_ERR_INVALID_ARG;
+  if (batch < 0 || !kv_indptr || (batch > 0 && !kv_last && !pl->ragged)) return PKV_ERR_INVALID_ARG;
   if (batch > pl->lim.max_batch) return PKV_ERR_WORKSPACE;
   if (pl->kind != PKV_PLAN_DECODE && !qo_indptr) return PKV_ERR_INVALID_ARG;
   if (num_pages < 0 || num_pages > INT32_MAX) return PKV_ERR_INVALID_ARG;
@@ -221,6 +226,7 @@ pkv_status validate(const pkv_plan* pl, int batch, const int32_t* qo_indptr, con
     // pair could wrap around to a positive page count.
     if (kv_indptr[b + 1] < kv_indptr[b]) return PKV_ERR_BAD_INDEX;
     const int64_t n = static_cast<int64_t>(kv_indptr[b + 1]) - kv_indptr[b];
+    if (pl->ragged) continue;
     if (n > 0 && (kv_last[b] < 1 || kv_last[b] > pl->p.page_size)) return PKV_ERR_BAD_INDEX;
     // Keys of one request are counted in int32 (a page id may be listed many times).
     if (n > 0 && (n - 1) * pl->p.page_size + kv_last[b] > INT32_MAX) return PKV_ERR_WORKSPACE;
@@ -228,6 +234,10 @@ pkv_status validate(const pkv_plan* pl, int batch, const int32_t* qo_indptr, con
   const int64_t nnz = kv_indptr[batch];
   if (nnz > pl->lim.max_kv_pages) return PKV_ERR_WORKSPACE;
   if (nnz > 0 && num_pages == 0) return PKV_ERR_BAD_INDEX;
+  if (pl->ragged) {  // num_pages rows of keys and values, and no page table
+    if (nnz > num_pages) return PKV_ERR_BAD_INDEX;
+    kv_indices = nullptr;
+  }
   if (kv_indices) {
     // One pass with no early exit, so that it vectorises: taken as unsigned, a
     // negative id wraps above every num_pages (at most INT32_MAX).
@@ -247,9 +257,10 @@ pkv_status validate(const pkv_plan* pl, int batch, const int32_t* qo_indptr, con
   return PKV_OK;
 }
 
+// kv_last: NULL where every page is full.
 int64_t kv_len_of(const int32_t* kv_indptr, const int32_t* kv_last, int b, int P) {
   const int64_t n = static_cast<int64_t>(kv_indptr[b + 1]) - kv_indptr[b];
-  return n > 0 ? (n - 1) * P + kv_last[b] : 0;
+  return n > 0 ? (n - 1) * P + (kv_last ? kv_last[b] : P) : 0;
 }
 
 // Decode work with the split turned off (pkv_plan_set_split_kv): every
@@ -928,7 +939,7 @@ pkv_status compute_prefill(pkv_plan* pl, int batch, const int32_t* qo_indptr, co
       t.kv_begin = it.kv_begin;
       t.kv_end = it.kv_end;
       t.idx_base = kv_indptr[it.b];
-      t.last_rows = kv_last[it.b];
+      t.last_rows = kv_last ? kv_last[it.b] : P;
       t.slot = it.slot;
       t.mask_off = mask_off[it.b];
       work[n] = t;
@@ -1185,6 +1196,7 @@ pkv_status pkv_plan_compute(pkv_plan* plan, int batch, const int32_t* qo_indptr_
   if (reinterpret_cast<uintptr_t>(host_ws) % 64) return PKV_ERR_INVALID_ARG;
   pkv_status st = validate(plan, batch, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h, num_pages);
   if (st != PKV_OK) return st;
+  if (plan->ragged) kv_last_page_len_h = nullptr;  // every key is a page of its own
   if (plan->copy_pending) {
     cudaEventSynchronize(plan->copy_done);
     plan->copy_pending = false;

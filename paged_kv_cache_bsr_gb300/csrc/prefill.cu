@@ -98,6 +98,22 @@ bool prefill_supported(int head_dim, int group, int dtype, int page_size) {
 
 namespace prefill_impl {
 
+cudaError_t make_rows_map(const void* base, int dtype, int heads, int64_t rows, int64_t row_stride, int box_heads,
+                          int box_rows, CUtensorMap& t) {
+  PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();
+  if (!encode) return cudaErrorNotSupported;
+  const CUtensorMapDataType dt = dtype == PKV_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows > 0 ? rows : 1)};
+  cuuint64_t strides[2] = {kD * 2, static_cast<cuuint64_t>(row_stride) * 2};
+  cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t es[3] = {1, 1, 1};
+  return encode(&t, dt, 3, const_cast<void*>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
 cudaError_t make_tensor_maps(const PrefillArgs& a, int group, int dtype, int64_t total_q, int64_t num_pages,
                              CUtensorMap& tq, CUtensorMap& tkv) {
   PFN_cuTensorMapEncodeTiled_v12000 encode = encode_fn();

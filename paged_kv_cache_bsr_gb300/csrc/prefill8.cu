@@ -23,7 +23,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // Launched as a programmatic dependent of the expansion: nothing global is touched
   // before that grid has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  prefill_cta<G, T, CAP, false, false, true>(a, tq, tkv, blockIdx.x, smem_raw);
+  prefill_cta<G, T, CAP, false, false, true>(a, tq, tkv, tkv, blockIdx.x, smem_raw);
 }
 
 template <typename T>

@@ -29,7 +29,10 @@
 //               256-byte row, into the same swizzled layout, zero-filled past
 //               the request; each lane waits for its own copies, fences them
 //               for the tensor cores and arrives on the block's barrier, while
-//               the next block's page ids load.
+//               the next block's page ids load.  Keys and values that are not in
+//               pages (RAGGED) come as one 128-row box per (block, half) of the
+//               packed rows; V rows of the requests behind this one are zeroed
+//               like the last page's.
 //   warp 1      one thread issues the tcgen05 MMAs, alternating the tiles:
 //               P_A V -> O_A, S_A(next) = Q_A K^T, P_B V -> O_B, S_B(next)
 //               (tile A only when the work tile's positions fit in it).
@@ -150,9 +153,11 @@ __device__ __forceinline__ void umma_ts_lo(uint32_t d_tmem, uint32_t a_tmem, uin
 // CTA's dynamic shared memory (kSmemBytes, or kSmemBytesSmall for SMALL).  Warps
 // 0-10 take the roles above; any further warp of the CTA only joins the two
 // CTA-wide barriers.
-template <int G, typename T, bool CAP, bool MASK, bool SMALL, bool STAGED>
+// RAGGED: keys and values packed like the queries, request b's from row idx_base on:
+// tkv is the keys' map, tv the values' (the paged instances have one for both).
+template <int G, typename T, bool CAP, bool MASK, bool SMALL, bool STAGED, bool RAGGED = false>
 __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensorMap& tq, const CUtensorMap& tkv,
-                                            int cta, uint8_t* sm) {
+                                            const CUtensorMap& tv, int cta, uint8_t* sm) {
   constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   constexpr int MP = kTM / G;  // query positions per UMMA tile
   const uint32_t base = smem_addr(sm);
@@ -194,10 +199,11 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
     t_end = a.worker_ptr[cta + 1];
   }
   const int num_pages = static_cast<int>(hdr->num_pages);
-  const int P = a.page_size;
+  const int P = RAGGED ? kBN : a.page_size;
   const int ppt = kBN / P;  // pages per key block
 
   auto page_of = [&](const PrefillTile& t, int j, int n_pages_req) {
+    if constexpr (RAGGED) return t.idx_base + t.kv_begin + j * kBN;  // the block's first row
     const int rel = (t.kv_begin + j * kBN) / P + lane;
     int id = num_pages;  // past the pool: TMA fills the box with zeros
     if (lane < ppt && rel < n_pages_req) {
@@ -332,9 +338,12 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
         if (lane == 0) mbar_arrive_expect_tx(bar(K_FULL + s), kTile);
         __syncwarp();
         const uint32_t sK = base + kOffK + s * kTile;
-        if (lane < ppt)
+        if constexpr (RAGGED) {
+          if (lane < 2) tma_load_3d(sK + lane * kHalf, &tkv, lane * 64, t.kvh, id, bar(K_FULL + s));
+        } else if (lane < ppt) {
           for (int h = 0; h < 2; ++h)
             tma_load_5d(sK + h * kHalf + lane * P * 128, &tkv, h * 64, 0, t.kvh, 0, id, bar(K_FULL + s));
+        }
         ++kvc;
       }
     }
@@ -371,23 +380,27 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
         }
         const int rel0 = (t.kv_begin + j * kBN) / P;
         const int last_rel = n_pages_req - 1 - rel0;
-        const bool partial = t.last_rows < P && last_rel >= 0 && last_rel < ppt;
+        const int last_rows = RAGGED ? t.kv_len - (n_pages_req - 1) * P : t.last_rows;
+        const bool partial = last_rows < P && last_rel >= 0 && last_rel < ppt;
         const uint32_t vbar = partial ? bar(V_LOAD + s) : bar(V_FULL + s);
         if (lane == 0) mbar_arrive_expect_tx(vbar, kTile);
         __syncwarp();
-        if (lane < ppt)
+        if constexpr (RAGGED) {
+          if (lane < 2) tma_load_3d(sV + lane * kHalf, &tv, lane * 64, t.kvh, id, vbar);
+        } else if (lane < ppt) {
           for (int h = 0; h < 2; ++h) tma_load_5d(sV + h * kHalf + lane * P * 128, &tkv, h * 64, 0, t.kvh, 1, id, vbar);
+        }
         if (partial) {
           // The last page's slots past kv_last_page_len may hold anything; the
           // P V product must see zeros there (0 * NaN would poison O).
           ok = __all_sync(kFull, wait(bar(V_LOAD + s), (vload_bits >> s) & 1));
           if (!ok) break;
           vload_bits ^= 1u << s;
-          const int chunks = (P - t.last_rows) * 8;  // 16-byte chunks per half
+          const int chunks = (P - last_rows) * 8;  // 16-byte chunks per half
           uint8_t* vgen = sm + kOffV + s * kTile;
           for (int i = lane; i < 2 * chunks; i += 32) {
             const int h = i / chunks, c = i % chunks;
-            *reinterpret_cast<uint4*>(vgen + h * kHalf + (last_rel * P + t.last_rows) * 128 + c * 16) =
+            *reinterpret_cast<uint4*>(vgen + h * kHalf + (last_rel * P + last_rows) * 128 + c * 16) =
                 make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
@@ -813,7 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ PrefillArgs a, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tkv) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  prefill_cta<G, T, CAP, MASK, SMALL, MASK>(a, tq, tkv, blockIdx.x, smem_raw);
+  prefill_cta<G, T, CAP, MASK, SMALL, MASK>(a, tq, tkv, tkv, blockIdx.x, smem_raw);
 }
 
 
@@ -842,6 +855,11 @@ cudaError_t launch_kernel(const PrefillArgs& a, int G, bool cap, int grid, const
 // kv_data (5D boxes of 64 columns x one page's rows) for the prefill tiles.
 cudaError_t make_tensor_maps(const PrefillArgs& a, int group, int dtype, int64_t total_q, int64_t num_pages,
                              CUtensorMap& tq, CUtensorMap& tkv);
+
+// The map of packed rows [rows, heads, D], `row_stride` elements from one row to the next,
+// with boxes of 64 columns x box_heads heads x box_rows rows.
+cudaError_t make_rows_map(const void* base, int dtype, int heads, int64_t rows, int64_t row_stride, int box_heads,
+                          int box_rows, CUtensorMap& t);
 
 // Each instance set is compiled in its own translation unit.
 extern template cudaError_t launch_kernel<__nv_bfloat16, false, false>(const PrefillArgs&, int, bool, int,

@@ -114,6 +114,34 @@ def prefill(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None,
     return _returned(stream, o, lse)
 
 
+def make_ragged_plan(q: torch.Tensor, k: torch.Tensor, qo_indptr, kv_indptr=None, sm_scale: Optional[float] = None,
+                     logits_cap: float = 0.0, causal: bool = True, stream=None) -> api.Plan:
+    """A plan for ``prefill_ragged`` over these tensors: qo_indptr and kv_indptr (None: the same) are the
+    requests' rows of q and of k, on the host."""
+    qo = torch.as_tensor(qo_indptr, dtype=torch.int32)
+    kv = qo if kv_indptr is None else torch.as_tensor(kv_indptr, dtype=torch.int32)
+    plan = api.Plan(api.PLAN_PREFILL_RAGGED, num_qo_heads=q.shape[1], num_kv_heads=k.shape[1], head_dim=q.shape[2],
+                    page_size=1, dtype=q.dtype, sm_scale=q.shape[2] ** -0.5 if sm_scale is None else sm_scale,
+                    logits_cap=logits_cap, causal=causal, max_batch=max(qo.numel() - 1, 1),
+                    max_total_q=max(q.shape[0], 1), max_kv_pages=max(k.shape[0], 1))
+    plan.plan(kv, None, k.shape[0], qo_indptr_h=qo, stream=stream)
+    return plan
+
+
+def prefill_ragged(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, qo_indptr=None, kv_indptr=None,
+                   plan: Optional[api.Plan] = None, stream=None, **variant) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Attention over whole prompts before anything is in pages: q [total_q, Hq, d], k and v
+    [total_kv, Hkv, d], the requests packed one behind another (views of a projection's output are
+    read in place).  Without a plan one is made (``make_ragged_plan``, its arguments)."""
+    with _on(stream):
+        if plan is None:
+            plan = make_ragged_plan(q, k, qo_indptr, kv_indptr, stream=stream, **variant)
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    plan.run_ragged(q, k, v, o, lse, stream=stream)
+    return _returned(stream, o, lse)
+
+
 def cascade(prefix: DeviceBatch, suffix: DeviceBatch, prefix_plan: Optional[api.Plan] = None,
             suffix_plan: Optional[api.Plan] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """Shared-prefix attention: one prefill over the prefix row block (all
