@@ -647,6 +647,52 @@ pkv_status pkv_batch_prefill_ragged(const pkv_plan* plan, const void* q, int64_t
                                     void* dev_ws, void* stream);
 
 /*
+ * Key weights: how much attention each cached key has had, for caches whose length is
+ * bounded by evicting the keys that have had the least.
+ *   weights [num_pages, num_kv_heads, page_size] fp32, beside the cache.
+ *
+ * pkv_add_key_weights adds the weights of one attention call: for key j of request b and
+ * kv head h
+ *   w[j, h] = decay * w[j, h] + sum over the request's query rows i that see j and the
+ *             query heads g that share h of exp(logit_ig(j) - lse_ig)
+ * with the logits of the attention calls (sm_scale, logits_cap) and lse what the call over
+ * the same keys returned, or the merged lse of several (cascade: one call for the prefix,
+ * a request of all rows, and one for the suffixes, each with the merged lse).  Without
+ * qo_indptr_d there is one row per request (a decode step), which sees all its keys; with
+ * it rows are ragged and params->causal means what it does for pkv_batch_prefill_paged, so
+ * the last n rows of a prompt can be passed alone.
+ *  - weighed_len_d [batch] int32 or NULL: the keys of each request that have weights
+ *    already.  Later keys' weights are set, not added to, whatever their slots hold.  NULL:
+ *    every key has one.  decay in [0, 1]; with 0 no weight is read.
+ *  - kv_pages: entries of kv_indices_d; the row pointers are checked against it on the
+ *    device, and total_q against qo_indptr_d.
+ *  - kv8_scales: NULL for the 16-bit cache, else kv holds the 8-bit cache's codes.
+ *  - A row whose lse is -inf adds nothing, whatever its query holds (rows that saw no key,
+ *    rows of a padded batch); a NaN lse makes the weights of the keys that the row sees NaN.
+ *  - A page may be listed by one request only (a shared prefix is a request of its own, see
+ *    above): two that list it would write its weights at the same time.
+ *  - Only slots of keys are written.  Sums are fp32 and in an order fixed by the arguments:
+ *    equal calls give equal bits.  Plan-free and graph-capturable: which kernel runs depends
+ *    on total_q / batch, the group and head_dim, everything else on the device arrays.
+ *  - Keys are 16-bit operands of the tensor cores with fp32 sums; from the 8-bit cache their
+ *    codes are exact, and for few rows per request queries keep 11 significant bits relative
+ *    to their row's largest element, as in pkv_batch_decode_paged_kv8.
+ *  - error_d: device int32 or NULL, OR-ed with 1 (a page id out of range: such keys are
+ *    skipped), 16 (a request whose row pointers, last-page length or rows do not fit: it is
+ *    skipped whole) or 4 (a bounded wait ran out).  The caller clears it.
+ * params: num_qo_heads, num_kv_heads (group 1/2/4/8), head_dim 64 or 128, page_size, dtype
+ * (of q, and of kv without scales), sm_scale, logits_cap, causal.
+ * Errors: PKV_ERR_INVALID_ARG (null or misaligned pointers, sizes or decay out of range, no
+ * qo_indptr_d and total_q != batch), PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA.  A batch without
+ * requests or pages is a no-op.
+ */
+pkv_status pkv_add_key_weights(const pkv_params* params, int batch, int64_t total_q, int64_t num_pages,
+                               int64_t kv_pages, const int32_t* qo_indptr_d, const int32_t* kv_indptr_d,
+                               const int32_t* kv_indices_d, const int32_t* kv_last_page_len_d,
+                               const int32_t* weighed_len_d, const void* q, const void* kv, const uint8_t* kv8_scales,
+                               const float* lse, float* weights, float decay, int32_t* error_d, void* stream);
+
+/*
  * Read (and, with clear != 0, reset) the device error word a plan's kernels
  * write when a check fails (page id out of range, indptr mismatch, a bounded
  * wait that ran out).  Synchronises `stream`.  *code = 0 means no error.

@@ -70,6 +70,7 @@ EXPORTS = [
     "pkv_batch_prefill_paged_masked", "pkv_batch_mixed_paged", "pkv_plan_set_pipelined",
     "pkv_plan_set_split_kv", "pkv_append_paged_kv_axes", "pkv_append_paged_kv8", "pkv_batch_decode_paged_kv8",
     "pkv_batch_prefill_paged_kv8", "pkv_batch_prefill_ragged",
+    "pkv_add_key_weights",
 ]
 
 
@@ -119,6 +120,8 @@ def load(path: Optional[str] = None):
             "pkv_batch_decode_paged_kv8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "pkv_batch_prefill_paged_kv8": (i32, [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]),
             "pkv_batch_prefill_ragged": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]),
+            "pkv_add_key_weights": (i32, [ctypes.POINTER(Params), i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                          ctypes.c_float, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -457,6 +460,40 @@ def batch_prefill_ragged(h, q, k, v, o, lse, dev_ws, stream=None) -> None:
     op, lp, wp = _ptrs((o, lse, dev_ws))
     _check((_lib or load()).pkv_batch_prefill_ragged(h, *_rows(q), *_rows(k), *_rows(v), op, lp, wp, _stream(stream)),
            "pkv_batch_prefill_ragged")
+
+
+def _table(kv_indptr, kv_indices, kv_last_page_len, *others) -> int:
+    """The batch of a page table on the device."""
+    _int32(kv_indptr, kv_indices, kv_last_page_len, *others)
+    batch = kv_indptr.numel() - 1
+    if batch < 0 or kv_last_page_len.numel() != batch:
+        raise ValueError("kv_indptr must have batch + 1 entries, kv_last_page_len batch")
+    return batch
+
+
+def add_key_weights(params: Params, kv_indptr, kv_indices, kv_last_page_len, q, lse, kv, weights, qo_indptr=None,
+                    kv_scales=None, decay: float = 1.0, weighed_len=None, error=None, stream=None) -> None:
+    """Add the probabilities that the rows ``q`` gave each cached key (their attention call's ``lse``) to its
+    ``weights`` [num_pages, Hkv, P] float32.  No qo_indptr: one row per request.  ``kv_scales``: kv is the
+    8-bit cache.  ``weighed_len`` [batch] int32: later keys' weights are set instead of added to."""
+    batch = _table(kv_indptr, kv_indices, kv_last_page_len, qo_indptr, weighed_len, error)
+    rows, dtype = (q.shape[0], params.num_qo_heads), _STORED.get(params.dtype)
+    if q.shape != (*rows, params.head_dim) or q.dtype is not dtype or lse.shape != rows or lse.dtype is not torch.float32:
+        raise ValueError("q must be [rows, num_qo_heads, head_dim] of the params' dtype, lse [rows, num_qo_heads] float32")
+    if (q.shape[0] != batch) if qo_indptr is None else (qo_indptr.numel() != batch + 1):
+        raise ValueError("q must hold a row per request, or qo_indptr batch + 1 entries")
+    if weighed_len is not None and weighed_len.numel() != batch:
+        raise ValueError("weighed_len must have an entry per request")
+    if kv_scales is not None:
+        _kv8_tensors(params, kv, kv_scales)
+    elif kv.shape[1:] != (2, params.num_kv_heads, params.page_size, params.head_dim) or kv.dtype is not dtype:
+        raise ValueError("kv must be [num_pages, 2, num_kv_heads, page_size, head_dim] of the params' dtype")
+    if weights.shape != (kv.shape[0], *kv.shape[2:4]) or weights.dtype is not torch.float32:
+        raise ValueError("weights must be [num_pages, num_kv_heads, page_size] float32")
+    _check((_lib or load()).pkv_add_key_weights(
+        ctypes.byref(params), batch, q.shape[0], kv.shape[0], kv_indices.numel(),
+        *_ptrs((qo_indptr, kv_indptr, kv_indices, kv_last_page_len, weighed_len, q, kv, kv_scales, lse, weights)),
+        decay, *_ptrs((error,)), _stream(stream)), "pkv_add_key_weights")
 
 
 def plan_set_timing_events(h, start=None, stop=None) -> None:
