@@ -693,6 +693,59 @@ pkv_status pkv_add_key_weights(const pkv_params* params, int batch, int64_t tota
                                const float* lse, float* weights, float decay, int32_t* error_d, void* stream);
 
 /*
+ * Which keys of a cache stay: for each request b and kv head h up to budget_d[b] keys, and
+ * never more than it has or than max_keep: its last `window` keys, then its first `sink`
+ * ones, then those of the largest weight (pkv_add_key_weights).  Of equal weights the key
+ * of the lower index stays; -0 equals +0, and NaN lies below every other weight.  Every kv
+ * head of a request keeps the same number of keys, each its own.
+ *  - keep [batch, num_kv_heads, max_keep] int32: the kept keys' indices (counted from the
+ *    request's first key) in ascending order, -1 behind the last; kept_len_d [batch] int32:
+ *    how many.
+ *  - weights, kv_pages, the page table and error_d as in pkv_add_key_weights (a key in a page
+ *    out of range counts as one of the lowest weight).  Pages may be shared here.
+ * A request whose row pointers or last-page length do not fit keeps nothing (flagged).
+ * Plan-free and graph-capturable.
+ * Errors: PKV_ERR_INVALID_ARG (null or misaligned pointers, sizes out of range),
+ * PKV_ERR_UNSUPPORTED (page size; batch * num_kv_heads past 2^25), PKV_ERR_CUDA.
+ */
+pkv_status pkv_select_keys(int batch, int num_kv_heads, int page_size, int64_t num_pages, int64_t kv_pages,
+                           const int32_t* kv_indptr_d, const int32_t* kv_indices_d,
+                           const int32_t* kv_last_page_len_d, const float* weights, const int32_t* budget_d, int sink,
+                           int window, int max_keep, int32_t* keep, int32_t* kept_len_d, int32_t* error_d,
+                           void* stream);
+
+/*
+ * Move the kept keys of each request and kv head, in their order, to slots 0 .. n - 1 of a
+ * page list (n = kept_len_d[b]), values, exponent bytes and weights with them.  Afterwards
+ * request b has n keys: its first ceil(n / page_size) pages, the last holding
+ * n - (pages - 1) * page_size of them; n follows from what the caller passed to
+ * pkv_select_keys, so the host's tables need no copy back.  Keys are stored turned
+ * (pkv_append_paged_kv and its likes), so attention does not change with their slots, but
+ * new tokens need their positions given (pkv_append_paged_kv_axes).
+ *  - keep, kept_len_d, max_keep: as pkv_select_keys writes them; any ascending indices will
+ *    do (others leave rows of mixed origin in the destination).
+ *  - dst_indptr_d, dst_indices_d NULL: in place, in the request's own first pages, which no
+ *    other request may list.  Else dst_indices_d[dst_indptr_d[b] ..] (dst_pages entries in
+ *    all) are the pages to fill, of the same pool and none of them a source page: for pages
+ *    that requests share.
+ *  - kv [num_pages, 2, num_kv_heads, page_size, head_dim]: params->dtype, or 8-bit codes with
+ *    kv8_scales.  weights: NULL, or moved too.
+ *  - Only the n slots are written; the slots and pages behind them keep what they held.
+ *  - error_d as in pkv_add_key_weights; an index that is no key of the request leaves its
+ *    place as it was (16), a request with n past its keys, max_keep or its pages is skipped
+ *    whole (16).
+ * params: num_kv_heads, head_dim (64 or 128), page_size, dtype.  Plan-free, graph-capturable.
+ * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (also a pool of 2^32 - 1 head rows or
+ * more), PKV_ERR_CUDA.
+ */
+pkv_status pkv_compact_paged_kv(const pkv_params* params, int batch, int64_t num_pages, int64_t kv_pages,
+                                const int32_t* kv_indptr_d, const int32_t* kv_indices_d,
+                                const int32_t* kv_last_page_len_d, int max_keep, const int32_t* keep,
+                                const int32_t* kept_len_d, int64_t dst_pages, const int32_t* dst_indptr_d,
+                                const int32_t* dst_indices_d, void* kv, uint8_t* kv8_scales, float* weights,
+                                int32_t* error_d, void* stream);
+
+/*
  * Read (and, with clear != 0, reset) the device error word a plan's kernels
  * write when a check fails (page id out of range, indptr mismatch, a bounded
  * wait that ran out).  Synchronises `stream`.  *code = 0 means no error.

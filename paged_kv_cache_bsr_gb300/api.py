@@ -70,7 +70,7 @@ EXPORTS = [
     "pkv_batch_prefill_paged_masked", "pkv_batch_mixed_paged", "pkv_plan_set_pipelined",
     "pkv_plan_set_split_kv", "pkv_append_paged_kv_axes", "pkv_append_paged_kv8", "pkv_batch_decode_paged_kv8",
     "pkv_batch_prefill_paged_kv8", "pkv_batch_prefill_ragged",
-    "pkv_add_key_weights",
+    "pkv_add_key_weights", "pkv_select_keys", "pkv_compact_paged_kv",
 ]
 
 
@@ -122,6 +122,9 @@ def load(path: Optional[str] = None):
             "pkv_batch_prefill_ragged": (i32, [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp]),
             "pkv_add_key_weights": (i32, [ctypes.POINTER(Params), i32, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp,
                                           ctypes.c_float, vp, vp]),
+            "pkv_select_keys": (i32, [i32, i32, i32, i64, i64, vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]),
+            "pkv_compact_paged_kv": (i32, [ctypes.POINTER(Params), i32, i64, i64, vp, vp, vp, i32, vp, vp, i64, vp, vp, vp,
+                                           vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -494,6 +497,47 @@ def add_key_weights(params: Params, kv_indptr, kv_indices, kv_last_page_len, q, 
         ctypes.byref(params), batch, q.shape[0], kv.shape[0], kv_indices.numel(),
         *_ptrs((qo_indptr, kv_indptr, kv_indices, kv_last_page_len, weighed_len, q, kv, kv_scales, lse, weights)),
         decay, *_ptrs((error,)), _stream(stream)), "pkv_add_key_weights")
+
+
+def select_keys(kv_indptr, kv_indices, kv_last_page_len, weights, budget, keep, kept_len, sink: int = 0, window: int = 0,
+                error=None, stream=None) -> None:
+    """The keys that stay, up to ``budget`` [batch] int32 a request and kv head: the last ``window``, the first
+    ``sink``, then the largest ``weights`` [num_pages, Hkv, P].  Writes ``keep`` [batch, Hkv, max_keep] int32
+    (ascending, -1 behind the last) and ``kept_len`` [batch] int32."""
+    batch = _table(kv_indptr, kv_indices, kv_last_page_len, budget, keep, kept_len, error)
+    if weights.dim() != 3 or weights.dtype is not torch.float32:
+        raise ValueError("weights must be [num_pages, num_kv_heads, page_size] float32")
+    pool, hkv, page = weights.shape
+    if keep.dim() != 3 or keep.shape[:2] != (batch, hkv) or budget.numel() != batch or kept_len.numel() != batch:
+        raise ValueError("keep must be [batch, num_kv_heads, max_keep], budget and kept_len [batch]")
+    _check((_lib or load()).pkv_select_keys(
+        batch, hkv, page, pool, kv_indices.numel(), *_ptrs((kv_indptr, kv_indices, kv_last_page_len, weights, budget)),
+        sink, window, keep.shape[2], *_ptrs((keep, kept_len, error)), _stream(stream)), "pkv_select_keys")
+
+
+def compact_paged_kv(kv_indptr, kv_indices, kv_last_page_len, keep, kept_len, kv, kv_scales=None, weights=None,
+                     dst_indptr=None, dst_indices=None, error=None, stream=None) -> None:
+    """Move the kept keys (``select_keys``) of the 16-bit cache ``kv``, or of the 8-bit one with its
+    ``kv_scales``, to the front of their pages, or into the pages of another table (dst_indptr, dst_indices)."""
+    batch = _table(kv_indptr, kv_indices, kv_last_page_len, keep, kept_len, dst_indptr, dst_indices, error)
+    if kv.dim() != 5 or kv.shape[1] != 2:
+        raise ValueError("kv must be [num_pages, 2, num_kv_heads, page_size, head_dim]")
+    pool, _, hkv, page, dim = kv.shape
+    if kv_scales is None and kv.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("kv must be float16 or bfloat16, or come with its kv_scales")
+    params = Params(hkv, hkv, dim, page, PKV_F16, 1.0, 0.0, 0)
+    if kv_scales is not None:
+        _kv8_tensors(params, kv, kv_scales)
+    if weights is not None and (weights.shape != (pool, hkv, page) or weights.dtype is not torch.float32):
+        raise ValueError("weights must be [num_pages, num_kv_heads, page_size] float32")
+    if keep.dim() != 3 or keep.shape[:2] != (batch, hkv) or kept_len.numel() != batch:
+        raise ValueError("keep must be [batch, num_kv_heads, max_keep], kept_len [batch]")
+    if (dst_indptr is None) != (dst_indices is None) or (dst_indptr is not None and dst_indptr.numel() != batch + 1):
+        raise ValueError("dst_indptr (batch + 1 entries) and dst_indices go together")
+    _check((_lib or load()).pkv_compact_paged_kv(
+        ctypes.byref(params), batch, pool, kv_indices.numel(), *_ptrs((kv_indptr, kv_indices, kv_last_page_len)),
+        keep.shape[2], *_ptrs((keep, kept_len)), 0 if dst_indices is None else dst_indices.numel(),
+        *_ptrs((dst_indptr, dst_indices, kv, kv_scales, weights, error)), _stream(stream)), "pkv_compact_paged_kv")
 
 
 def plan_set_timing_events(h, start=None, stop=None) -> None:

@@ -13,7 +13,7 @@ from __future__ import annotations
 
 import contextlib
 import dataclasses
-from typing import Optional, Sequence, Tuple
+from typing import Optional, Sequence, Tuple, Union
 
 import torch
 
@@ -257,6 +257,61 @@ def cascade_kv8(prefix: DeviceBatch, suffix: DeviceBatch, cache: Kv8Cache, prefi
     o_s, l_s = decode_kv8(suffix, cache, suffix_plan, stream)
     api.merge_state(o_p, l_p, o_s, l_s, o_p, l_p, stream=stream)
     return o_p, l_p
+
+
+def zero_key_weights(num_pages: int, num_kv_heads: int, page_size: int, device: str = "cuda") -> torch.Tensor:
+    """Key weights beside a cache of that many pages."""
+    return torch.zeros(num_pages, num_kv_heads, page_size, dtype=torch.float32, device=device)
+
+
+def add_key_weights(db: DeviceBatch, lse: torch.Tensor, weights: torch.Tensor, cache: Optional[Kv8Cache] = None,
+                    decay: float = 1.0, weighed_len: Optional[torch.Tensor] = None, error: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """Add to ``weights`` the probabilities that the batch's rows gave every key they see; ``lse`` from the
+    attention call (or merged from several) over the same keys.  ``cache``: the keys of the 8-bit cache."""
+    b = db.host
+    params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale, b.logits_cap, b.causal)
+    api.add_key_weights(params, db.kv_indptr, db.kv_indices, db.kv_last_page_len, db.q, lse,
+                        db.kv_data if cache is None else cache.codes, weights, qo_indptr=None if b.is_decode else db.qo_indptr,
+                        kv_scales=None if cache is None else cache.scales, decay=decay, weighed_len=weighed_len, error=error,
+                        stream=stream)
+
+
+def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[int]], sink: int = 0, window: int = 0,
+          cache: Optional[Kv8Cache] = None, error: Optional[torch.Tensor] = None, stream=None
+          ) -> Tuple[DeviceBatch, torch.Tensor]:
+    """Shorten each request's cache to ``budget`` keys (one number, or one a request) in place: for every kv
+    head the last ``window``, the first ``sink`` and the heaviest others.  No page may be listed by two requests.
+    Returns the batch with its shorter page tables, and the ids of the pages it no longer lists (on the host).
+    The key weights move with their keys; nothing is read back from the GPU."""
+    b = db.host
+    budgets = [int(budget)] * b.batch if isinstance(budget, int) else [int(x) for x in budget]
+    if len(budgets) != b.batch or min(budgets, default=0) < 0:
+        raise ValueError("budget must be a count of keys, or one for each request")
+    kept = [min(n, x) for n, x in zip(b.kv_lens, budgets)]
+    with _on(stream):
+        host_budget = torch.tensor(budgets, dtype=torch.int32)
+        keep = torch.empty(b.batch, b.num_kv_heads, max(kept, default=0), dtype=torch.int32, device=db.q.device)
+        kept_len = torch.empty(b.batch, dtype=torch.int32, device=db.q.device)
+        api.select_keys(db.kv_indptr, db.kv_indices, db.kv_last_page_len, weights, host_budget.to(db.q.device), keep, kept_len,
+                        sink=sink, window=window, error=error, stream=stream)
+        api.compact_paged_kv(db.kv_indptr, db.kv_indices, db.kv_last_page_len, keep, kept_len,
+                             db.kv_data if cache is None else cache.codes, kv_scales=None if cache is None else cache.scales,
+                             weights=weights, error=error, stream=stream)
+        pages = [-(-n // b.page_size) for n in kept]
+        first = [int(x) for x in b.kv_indptr]
+        listed = [b.kv_indices[s:s + n] for s, n in zip(first, pages)]
+        freed = [b.kv_indices[s + n:e] for s, n, e in zip(first, pages, first[1:])]
+        none = b.kv_indices[:0]
+        indptr = torch.zeros(b.batch + 1, dtype=torch.int32)
+        indptr[1:] = torch.tensor(pages, dtype=torch.int32).cumsum(0)
+        host = dataclasses.replace(b, kv_indptr=indptr, kv_indices=torch.cat([none, *listed]), kv_lens=kept,
+                                   kv_last_page_len=torch.tensor([n - (p - 1) * b.page_size if n else 0 for n, p in zip(kept, pages)],
+                                                                 dtype=torch.int32))
+        tables = [t.to(db.q.device) for t in (host.kv_indptr, host.kv_indices, host.kv_last_page_len)]
+    _returned(stream, *tables)
+    return dataclasses.replace(db, host=host, kv_indptr=tables[0], kv_indices=tables[1], kv_last_page_len=tables[2]), \
+        torch.cat([none, *freed])
 
 
 def mixed(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
