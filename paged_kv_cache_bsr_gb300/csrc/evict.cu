@@ -3,13 +3,17 @@
 //
 // Select.  For each (request, kv head) the last `window` keys stay, then the first `sink`
 // ones, then those of the largest weight (equal weights: the lower index), up to the
-// request's budget.  A radix select on the weights' bits in order of their values: four
-// passes of 8 bits find the weight T of the last key that stays and how many keys of
+// request's budget.  A radix select on the weights' bits in order of their values: passes of
+// 12, 10 and 10 bits find the weight T of the last key that stays and how many keys of
 // weight T stay; one more pass writes the indices in ascending order, places counted by
-// ballots.  The weights are read from global memory once and kept in shared memory as
-// ordered 32-bit integers (what does not fit is read again).  The CTAs of a cluster share
-// a long list, each a contiguous slice; they add their digit counts through distributed
-// shared memory.  Bound by latency for the lists of a serving batch.
+// ballots.  (The first digit holds the exponent and three bits of the mantissa.)  The weights
+// are read from global memory once and kept in shared memory as ordered 32-bit integers
+// (what does not fit is read again).  The CTAs of a cluster share a long list, each a
+// contiguous slice; they add their digit counts through distributed shared memory.  Bound
+// by latency: loops are unrolled over independent keys, and a digit is found by 64 threads
+// that each add up the counts above one (a chain of shuffles took 4800 of a list's 36000
+// cycles).  Measured, 8 kv heads: 64 requests of 512 to 4096 keys 15.2 us (20.7 us with
+// digits of 8 bits and a key at a time), 2 requests of 10^5 keys 25.4 us (50.3 us).
 //
 // Compact.  A kept key moves from its token index s to its place i <= s in the list of
 // kept keys.  In place, a CTA owns a column slice of one (request, kv head, K or V) and
@@ -81,9 +85,8 @@ __device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank)
 }
 
 // ---------------------------------------------------------------------------- select
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kMaxHeld = 48 * 1024;  // weights in shared memory
+
 
 struct SelectArgs {
   Table t;
@@ -93,26 +96,55 @@ struct SelectArgs {
   int32_t* keep;          // [batch, Hkv, max_keep]
   int32_t* kept_len;      // [batch]
   int share;              // CTAs of a cluster
-  int held;               // weights a CTA keeps in shared memory
+  int held;               // weights a CTA keeps in shared memory, a multiple of 4
+  uint32_t page_mul;      // ceil(2^32 / page_size) (page_size > 1)
+  int fours;              // four keys' weights are one aligned load
 };
 
+// Digits of the three passes, in one array of counters behind one another.
+__device__ constexpr int digit_bits(int pass) { return pass == 0 ? 12 : 10; }
+__device__ constexpr int digit_shift(int pass) { return 20 - 10 * pass; }
+__device__ constexpr int first_bin(int pass) { return pass == 0 ? 0 : 4096 + 1024 * (pass - 1); }
+constexpr int kBins = 6144, kGroup = 64;  // bins that are first counted together
+
+template <int THREADS>
 struct SelectShared {
-  uint32_t hist[4][256];
-  uint32_t warp_gt[kSelWarps], warp_eq[kSelWarps];
+  alignas(16) uint32_t hist[kBins];
+  alignas(16) uint32_t group[3][kGroup];
+  alignas(16) uint32_t all[2][kGroup];  // counts of 64 groups, then of the 64 bins of one, over the cluster
+  uint32_t warp_gt[THREADS / 32], warp_eq[THREADS / 32];
   uint32_t total[2];      // this CTA's keys above T, and of weight T
-  uint32_t digit, left;
+  uint32_t digit, left, group_at, group_left;
 };
 
-// The weight's bits in order of its value: NaN lowest, -0 equal to +0.
+// Of 64 counts in shared memory, the one that holds the left-th key from above: thread i of 64
+// adds up those above count i (no chain of shuffles).
+__device__ __forceinline__ void find_count(const uint32_t* counts, int i, uint32_t left, int base, uint32_t& digit,
+                                           uint32_t& rest) {
+  uint32_t above = 0;
+#pragma unroll
+  for (int k = 0; k < kGroup; k += 4) {
+    const uint4 c = *reinterpret_cast<const uint4*>(counts + k);
+    above += (k > i ? c.x : 0u) + (k + 1 > i ? c.y : 0u) + (k + 2 > i ? c.z : 0u) + (k + 3 > i ? c.w : 0u);
+  }
+  if (above < left && above + counts[i] >= left) {
+    digit = base + i;
+    rest = left - above;
+  }
+}
+
+// The weight's bits in order of its value: NaN lowest (1), -0 equal to +0.  0 stands for no key.
 __device__ __forceinline__ uint32_t ordered(float x) {
   const uint32_t v = __float_as_uint(x + 0.f);
-  if (x != x) return 0u;
+  if (x != x) return 1u;
   return v & 0x80000000u ? ~v : v | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) select_keys_kernel(const __grid_constant__ SelectArgs a) {
-  extern __shared__ uint32_t held[];
-  __shared__ SelectShared sh;
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_keys_kernel(const __grid_constant__ SelectArgs a) {
+  constexpr int kWarps = THREADS / 32;
+  extern __shared__ __align__(16) uint32_t held[];
+  __shared__ SelectShared<THREADS> sh;
   // Launched as a programmatic dependent of the kernel before it on the stream:
   // nothing global is touched before that grid has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -120,90 +152,172 @@ __global__ void __launch_bounds__(kSelThreads) select_keys_kernel(const __grid_c
   const int share = a.share, rank = share > 1 ? static_cast<int>(cluster_rank()) : 0;
   const int list = blockIdx.x / share, b = list / a.t.hkv, h = list - b * a.t.hkv;
   int page0, len;
+  const int asked = __ldg(a.budget + b);
   const bool ok = keys_of(a.t, b, page0, len);
   if (!ok && tid == 0) flag(a.t, kErrAppendLayout);
-  const int n = min(min(max(__ldg(a.budget + b), 0), len), a.max_keep);
+  const int n = min(min(max(asked, 0), len), a.max_keep);
   const int tail = min(a.window, n), front = min(a.sink, n - tail);
   const int pick = n - tail - front, mid = len - tail - front;  // pick of keys front .. front + mid - 1
+  const int P = a.t.page_size;
+  // The keys between in aligned groups of four, a run of groups for each CTA: entry e is key j0 + e.
+  const int first4 = front & ~3, end = front + mid, groups = (end - first4 + 3) / 4;
+  const int slice = (groups + share - 1) / share;
+  const int g0 = min(rank * slice, groups), count = (min(g0 + slice, groups) - g0) * 4, j0 = first4 + g0 * 4;
+  auto page_of = [&](int j) { return P == 1 ? j : [&] { const int q = __umulhi(j, a.page_mul); return q * P > j ? q - 1 : q; }(); };
+  auto row_of = [&](int j, int pg) -> int64_t {  // the weight of key j, or -1
+    const int page = __ldg(a.t.indices + page0 + pg);
+    if (page < 0 || page >= a.t.num_pages) {
+      flag(a.t, kErrPageIndex);
+      return -1;
+    }
+    return (static_cast<int64_t>(page) * a.t.hkv + h) * P + (j - pg * P);
+  };
+  auto fetch = [&](int e) -> uint32_t {
+    const int j = j0 + e;
+    if (j < front || j >= end) return 0u;
+    const int64_t at = row_of(j, page_of(j));
+    return at < 0 ? 1u : ordered(__ldg(a.weights + at));
+  };
+  const int in_smem = min(count, a.held);
+  if (pick > 0 && pick < mid) {
+    // Page ids of kAhead loads first, then the loads, then what they brought.
+    constexpr int kAhead = 4;
+    const int width = a.fours ? 4 : 1;
+    bool bad = false;
+    for (int e0 = tid * width; e0 < in_smem; e0 += kAhead * THREADS * width) {
+      int page[kAhead], at_slot[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int e = e0 + k * THREADS * width, j = j0 + e;  // fours: key j's page holds all four
+        const bool in = e < in_smem && (a.fours || (j >= front && j < end));
+        const int pg = in ? page_of(j) : 0;
+        at_slot[k] = j - pg * P;
+        page[k] = in ? __ldg(a.t.indices + page0 + pg) : -1;
+        if (!in) at_slot[k] = -1;
+      }
+      float4 w[kAhead];
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const bool use = page[k] >= 0 && page[k] < a.t.num_pages;
+        bad |= !use && at_slot[k] >= 0;
+        const float* at = a.weights + (use ? (static_cast<int64_t>(page[k]) * a.t.hkv + h) * P + at_slot[k] : 0);
+        const float nan = __int_as_float(0x7fffffff);  // a key in no page: one of the lowest
+        w[k] = make_float4(nan, nan, nan, nan);
+        if (a.fours) {
+          if (use) w[k] = __ldg(reinterpret_cast<const float4*>(at));
+        } else if (use) {
+          w[k].x = __ldg(at);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k) {
+        const int e = e0 + k * THREADS * width, j = j0 + e;
+        if (e >= in_smem) continue;
+        if (a.fours) {
+          *reinterpret_cast<uint4*>(held + e) =
+              make_uint4(j < front || j >= end ? 0u : ordered(w[k].x), j + 1 < front || j + 1 >= end ? 0u : ordered(w[k].y),
+                         j + 2 < front || j + 2 >= end ? 0u : ordered(w[k].z), j + 3 < front || j + 3 >= end ? 0u : ordered(w[k].w));
+        } else {
+          held[e] = j < front || j >= end ? 0u : ordered(w[k].x);
+        }
+      }
+    }
+    if (bad) flag(a.t, kErrPageIndex);
+  }
   int32_t* out = a.keep + static_cast<int64_t>(list) * a.max_keep;
   if (h == 0 && rank == 0 && tid == 0) a.kept_len[b] = n;
   // The keys that stay anyway, and what is past the list.
-  for (int i = rank * kSelThreads + tid; i < a.max_keep; i += share * kSelThreads) {
-    if (i < front) out[i] = i;
-    else if (i >= n) out[i] = -1;
-    else if (i >= n - tail) out[i] = len - (n - i);
-    else if (pick == mid) out[i] = i;
+  for (int i = rank * THREADS + tid; i < a.max_keep; i += share * THREADS) {
+    if (i >= front && i < n - tail && pick < mid) {
+      i += (n - tail - 1 - i) / (share * THREADS) * (share * THREADS);  // the chosen ones are written below
+      continue;
+    }
+    out[i] = i >= n ? -1 : i >= n - tail ? len - (n - i) : i;
   }
   if (pick == 0 || pick == mid) return;  // the same for all CTAs of a cluster
-
-  const int P = a.t.page_size;
-  const int slice = (mid + share - 1) / share;
-  const int lo = min(rank * slice, mid), count = min(slice, mid - lo);  // keys front + lo ...
-  auto fetch = [&](int i) -> uint32_t {
-    const int j = front + lo + i, pg = j / P, page = __ldg(a.t.indices + page0 + pg);
-    if (page < 0 || page >= a.t.num_pages) {
-      flag(a.t, kErrPageIndex);
-      return 0u;
-    }
-    return ordered(__ldg(a.weights + (static_cast<int64_t>(page) * a.t.hkv + h) * P + (j - pg * P)));
-  };
-  for (int i = tid; i < 4 * 256; i += kSelThreads) (&sh.hist[0][0])[i] = 0;
-  const int in_smem = min(count, a.held);
-#pragma unroll 4
-  for (int i = tid; i < in_smem; i += kSelThreads) held[i] = fetch(i);
-  auto value = [&](int i) { return i < in_smem ? held[i] : fetch(i); };
+  for (int i = tid * 4; i < kBins; i += THREADS * 4) *reinterpret_cast<uint4*>(sh.hist + i) = make_uint4(0u, 0u, 0u, 0u);
   __syncthreads();
 
   uint32_t prefix = 0;
   int left = pick;  // keys still to find among those whose upper digits are prefix
-  for (int pass = 0; pass < 4; ++pass) {
-    const int shift = 24 - 8 * pass;
-    for (int i = tid; i < count; i += kSelThreads) {
-      const uint32_t v = value(i);
-      if (pass == 0 || (v >> (shift + 8)) == prefix) atomicAdd(&sh.hist[pass][(v >> shift) & 255u], 1u);
-    }
-    if (share > 1) cluster_sync_all(); else __syncthreads();
-    if (warp == 0) {
-      // Lane l holds digits 255 - 8 l downwards.
-      uint32_t c[8], sum = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t* at = &sh.hist[pass][255 - 8 * lane - k];
-        c[k] = 0;
-        if (share > 1)
-          for (int r = 0; r < share; ++r) c[k] += ld_cluster_u32(at, r);
-        else
-          c[k] = *at;
-        sum += c[k];
-      }
-      uint32_t before = sum;  // keys of this lane's digits and of larger ones
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(kFullMask, before, o);
-        if (lane >= o) before += x;
-      }
-      before -= sum;
-      if (before < static_cast<uint32_t>(left) && before + sum >= static_cast<uint32_t>(left)) {
-        int k = 0;
-        uint32_t above = before;
-        while (k < 7 && above + c[k] < static_cast<uint32_t>(left)) above += c[k++];
-        sh.digit = 255 - 8 * lane - k;
-        sh.left = left - above;
-      }
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = digit_shift(pass), bits = digit_bits(pass);
+    uint32_t* hist = sh.hist + first_bin(pass);
+    auto count_key = [&](uint32_t v) {
+      if (v != 0u && (pass == 0 || v >> ((shift + bits) & 31) == prefix)) atomicAdd(hist + (v >> shift & ((1u << bits) - 1)), 1u);
+    };
+    for (int e0 = tid; e0 < in_smem; e0 += 4 * THREADS) {
+      uint32_t v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[k] = e0 + k * THREADS < in_smem ? held[e0 + k * THREADS] : 0u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) count_key(v[k]);
+    }
+    for (int e = in_smem + tid; e < count; e += THREADS) count_key(fetch(e));
+    __syncthreads();
+    // Groups of 64 bins are counted first: the group, then the bin, each over the cluster.
+    const int n_groups = (1 << bits) / kGroup;
+    for (int g = warp; g < kGroup; g += kWarps) {
+      const uint32_t c = g < n_groups ? __reduce_add_sync(kFullMask, hist[g * kGroup + lane] + hist[g * kGroup + 32 + lane]) : 0u;
+      if (lane == 0) sh.group[pass][g] = c;
+    }
+    auto over_cluster = [&](const uint32_t* x, uint32_t* sum) {  // 64 threads
+      uint32_t c[8];
+#pragma unroll
+      for (int r = 0; r < 8; ++r) c[r] = r < share ? ld_cluster_u32(x + tid, r) : 0u;
+      sum[tid] = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
+    };
+    const uint32_t* counts = sh.group[pass];
+    if (share > 1) {
+      cluster_sync_all();
+      if (tid < kGroup) over_cluster(counts, sh.all[0]);
+      counts = sh.all[0];
     }
     __syncthreads();
-    prefix = prefix << 8 | sh.digit;
-    left = static_cast<int>(sh.left);
+    if (tid < kGroup) find_count(counts, tid, left, 0, sh.group_at, sh.group_left);
     __syncthreads();
+    const int g = static_cast<int>(sh.group_at);
+    counts = hist + g * kGroup;
+    if (share > 1) {
+      if (tid < kGroup) over_cluster(counts, sh.all[1]);
+      counts = sh.all[1];
+      __syncthreads();
+    }
+    if (tid < kGroup) find_count(counts, tid, sh.group_left, g * kGroup, sh.digit, sh.left);
+    __syncthreads();
+    prefix = prefix << bits | sh.digit;
+    left = static_cast<int>(sh.left);
   }
   // prefix is T; left of the keys of weight T stay, those of the lowest index.  Each warp has a
   // contiguous run of the slice.
-  const int per_warp = ((count + kSelWarps - 1) / kSelWarps + 31) / 32 * 32;
+  const int per_warp = ((count + kWarps - 1) / kWarps + 31) / 32 * 32;
   const int w0 = min(warp * per_warp, count), w1 = min(w0 + per_warp, count);
   uint32_t gt = 0, eq = 0;
-  for (int i = w0 + lane; i < w1; i += 32) {
-    const uint32_t v = value(i);
-    gt += v > prefix;
-    eq += v == prefix;
+  // Four neighbouring chunks of 32 keys of a run.
+  auto load4 = [&](int e0, uint32_t (&v)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = e0 + k * 32 + lane < min(w1, in_smem) ? held[e0 + k * 32 + lane] : 0u;
+    if (e0 + 128 > in_smem && in_smem < w1) {
+#pragma unroll 1
+      for (int k = 0; k < 4; ++k) {
+        const int e = e0 + k * 32 + lane;
+        const uint32_t x = e >= in_smem && e < w1 ? fetch(e) : 0u;
+        if (k == 0) v[0] |= x;
+        if (k == 1) v[1] |= x;
+        if (k == 2) v[2] |= x;
+        if (k == 3) v[3] |= x;
+      }
+    }
+  };
+  for (int e0 = w0; e0 < w1; e0 += 128) {
+    uint32_t v[4];
+    load4(e0, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      gt += v[k] > prefix;
+      eq += v[k] == prefix;
+    }
   }
   gt = __reduce_add_sync(kFullMask, gt);
   eq = __reduce_add_sync(kFullMask, eq);
@@ -212,35 +326,45 @@ __global__ void __launch_bounds__(kSelThreads) select_keys_kernel(const __grid_c
     sh.warp_eq[warp] = eq;
   }
   __syncthreads();
-  uint32_t gt0 = 0, eq0 = 0;  // before this warp's run
-  for (int k = 0; k < kSelWarps; ++k) {
-    if (k < warp) {
-      gt0 += sh.warp_gt[k];
-      eq0 += sh.warp_eq[k];
-    }
-  }
+  // Before this warp's run.
+  uint32_t gt0 = __reduce_add_sync(kFullMask, lane < warp ? sh.warp_gt[lane] : 0u);
+  uint32_t eq0 = __reduce_add_sync(kFullMask, lane < warp ? sh.warp_eq[lane] : 0u);
   if (share > 1) {
-    if (tid == kSelThreads - 1) {  // the last warp's end is the slice's
-      sh.total[0] = gt0 + sh.warp_gt[kSelWarps - 1];
-      sh.total[1] = eq0 + sh.warp_eq[kSelWarps - 1];
+    if (tid == THREADS - 1) {  // the last warp's end is the slice's
+      sh.total[0] = gt0 + sh.warp_gt[kWarps - 1];
+      sh.total[1] = eq0 + sh.warp_eq[kWarps - 1];
     }
     cluster_sync_all();
-    for (int r = 0; r < rank; ++r) {
-      gt0 += ld_cluster_u32(&sh.total[0], r);
-      eq0 += ld_cluster_u32(&sh.total[1], r);
+    uint32_t g[8], q[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      g[r] = r < rank ? ld_cluster_u32(&sh.total[0], r) : 0u;
+      q[r] = r < rank ? ld_cluster_u32(&sh.total[1], r) : 0u;
+    }
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+      gt0 += g[r];
+      eq0 += q[r];
     }
   }
   const uint32_t below = (1u << lane) - 1;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t v = i < w1 ? value(i) : 0u;
-    const bool g = i < w1 && v > prefix, e = i < w1 && v == prefix;
-    const unsigned mg = __ballot_sync(kFullMask, g), me = __ballot_sync(kFullMask, e);
-    const uint32_t e_at = eq0 + __popc(me & below), g_at = gt0 + __popc(mg & below);
-    if (g || (e && e_at < static_cast<uint32_t>(left)))
-      out[front + g_at + min(e_at, static_cast<uint32_t>(left))] = front + lo + i;
-    gt0 += __popc(mg);
-    eq0 += __popc(me);
+  for (int e0 = w0; e0 < w1; e0 += 128) {
+    uint32_t v[4];
+    load4(e0, v);
+    unsigned mg[4], mq[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      mg[k] = __ballot_sync(kFullMask, v[k] > prefix);
+      mq[k] = __ballot_sync(kFullMask, v[k] == prefix);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t q_at = eq0 + __popc(mq[k] & below), g_at = gt0 + __popc(mg[k] & below);
+      if (v[k] > prefix || (v[k] == prefix && q_at < static_cast<uint32_t>(left)))
+        out[front + g_at + min(q_at, static_cast<uint32_t>(left))] = j0 + e0 + k * 32 + lane;
+      gt0 += __popc(mg[k]);
+      eq0 += __popc(mq[k]);
+    }
   }
   if (share > 1) cluster_sync_all();  // a CTA's counts stay until they have been read
 }
@@ -484,16 +608,22 @@ extern "C" pkv_status pkv_select_keys(int batch, int num_kv_heads, int page_size
   a.keep = keep;
   a.kept_len = kept_len_d;
   // Lists too few for the chip are shared by clusters, as long as a CTA has 1024 keys of a
-  // list of average length.  Shared memory for twice that length: longer lists read the
-  // rest again.
+  // list of average length.  Shared memory for twice that length, as far as it goes: longer
+  // lists read the rest again.  256 threads where that is 6144 keys or fewer, so that the
+  // lists of a serving batch run at once.
   const int64_t lists = static_cast<int64_t>(batch) * num_kv_heads, avg = kv_pages * page_size / batch;
   a.share = 1;
   while (a.share < 8 && lists * a.share * 2 <= 2 * sms && avg / (a.share * 2) >= 1024) a.share *= 2;
-  a.held = static_cast<int>(std::min<int64_t>(kMaxHeld, std::max<int64_t>(2 * avg / a.share, 1024) + 31) & ~int64_t{31});
-  cudaError_t e = ensure_smem_limit(select_keys_kernel, kMaxHeld * 4);
-  if (e == cudaSuccess)
-    e = launch_clusters(select_keys_kernel, lists, a.share, kSelThreads, a.held * 4, static_cast<cudaStream_t>(stream), a);
-  return status_of(e);
+  const int64_t room = std::max<int64_t>(5 * avg / 4 / a.share, 20 * 1024);  // two CTAs an SM, or a quarter more than the average
+  a.held = static_cast<int>(std::min<int64_t>(kMaxHeld, (std::max<int64_t>(std::min(2 * avg / a.share, room), 1024) + 35) & ~int64_t{31}));
+  a.page_mul = page_size > 1 ? static_cast<uint32_t>(((int64_t{1} << 32) + page_size - 1) / page_size) : 0u;
+  a.fours = page_size % 4 == 0 && aligned(weights, 16);
+  auto s = static_cast<cudaStream_t>(stream);
+  auto launch = [&](auto kern, int threads) {
+    cudaError_t e = ensure_smem_limit(kern, kMaxHeld * 4);
+    return e == cudaSuccess ? launch_clusters(kern, lists, a.share, threads, a.held * 4, s, a) : e;
+  };
+  return status_of(a.held <= 6144 ? launch(select_keys_kernel<256>, 256) : launch(select_keys_kernel<512>, 512));
 }
 
 extern "C" pkv_status pkv_compact_paged_kv(const pkv_params* p, int batch, int64_t num_pages, int64_t kv_pages,
