@@ -11,18 +11,22 @@
 // no atomics, and equal calls give equal bits.
 //
 // Two kernels, both reading K once:
-//  - stream: few query rows per request (a decode step).  HBM-bound on K.  A warp takes
-//    16 keys at a time straight from global memory into the A fragments of mma.sync
-//    m16n8k16 (which dims a k step holds does not matter as long as the query fragments
-//    hold the same ones, so a lane's 16-byte chunk of a row serves whole k steps without
-//    shared memory), against columns of 8 (row, head) pairs held in registers.  Two tiles
-//    are in flight per warp and 16 warps per SM.
+//  - stream: few query rows per request (a decode step).  HBM-bound on K.  Every warp streams
+//    keys through its own ring of shared memory by cp.async and multiplies 16 keys at a
+//    time with mma.sync m16n8k16, against columns of 8 (row, head) pairs (which dims a k
+//    step holds does not matter as long as the query fragments hold the same ones, so a
+//    lane's 16-byte chunk of a row serves whole k steps).  Measured: 64 requests of 512 to
+//    4096 keys, group 4, 49.3 us, 95 % of measured HBM bandwidth; two of 10^5 in the 8-bit
+//    cache, group 8, 48.1 us, 80 % (issue slots: a key row is 128 bytes there).
 //  - tile: many rows per request (prompts, or the last rows of one).  S^T = K Q^T on
-//    tcgen05: a CTA owns 128 keys of one kv head in tensor memory and streams 64-column
+//    tcgen05: a CTA holds 128 keys of one kv head in tensor memory and streams 64-column
 //    tiles of (row, head) pairs past them by TMA; a thread is a key, and sums its
-//    exponentials over the columns in registers.  Few key tiles before many rows are
-//    shared by the CTAs of a cluster, which add their sums in rank order through
-//    distributed shared memory.
+//    exponentials over the columns in registers.  Four CTAs share an SM, so that one's
+//    start and waits are another's products.  Many columns before few keys are shared by
+//    the CTAs of a cluster, which add their sums in rank order through distributed shared
+//    memory.  Bound by the instructions around the exponentials (2.5 issue slots for each,
+//    5.5 with a cap).  Measured: 10 prompts of 128 to 1500 rows, 8 kv heads, group 4, 74 us;
+//    the last 32 to 64 rows of 7 prompts of 2000 to 9000 keys, group 2, capped, 38.4 us.
 // Both find their work from the device's row pointers alone: request b's tiles start at
 //     first(b) = floor(kv_indptr[b] P / K) + b        (K keys a tile),
 // which leaves each request room for its ceil(len / K) tiles and at most one unused
@@ -111,17 +115,6 @@ __device__ __forceinline__ Request load_request(const WeightArgs& a, int b) {
 }
 
 // ---------------------------------------------------------------------------- stream
-__device__ __forceinline__ uint4 ld_stream_v4(const void* p, bool use) {
-  uint4 r;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.s32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(r.x), "=&r"(r.y), "=&r"(r.z), "=&r"(r.w)
-      : "l"(p), "r"(static_cast<int>(use)));
-  return r;
-}
-
 template <typename T>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                             uint32_t b0, uint32_t b1) {
@@ -143,59 +136,193 @@ __device__ __forceinline__ void e4m3x4_to_half(uint32_t w, uint32_t& lo, uint32_
       : "r"(w));
 }
 
-constexpr int kStreamKeys = 16;
-constexpr int kStreamThreads = 256;
-
-// A tile on its way: lane (g, t) holds 16-byte chunks t, t + 4, ... of keys g and g + 8.
-template <int CH>
-struct KeyTile {
-  uint4 k[2][CH];
-  float scale[2];  // 8-bit cache: 2^(s - 127) of the two keys
-  float old;       // lanes t = 0, 1: the weight of key g + 8 t before the call, decayed
-  float* at;       // and where it goes (nullptr: nowhere)
+// A warp's ring of tiles of 16 keys (rows of 256 bytes) or 32 (shorter ones: what goes with a
+// tile, its page ids and addresses, is as many instructions for 16 keys of the 8-bit cache as
+// their products).  Behind a tile's rows: the keys' weights before the call, the rows of the
+// weights they go to (kNoRow: none) and, for the 8-bit cache, the aligned word around each
+// exponent byte and the byte's place in it.  Two 10^5-token contexts of the 8-bit cache: 16
+// keys a tile 54 us; 32 keys with 16 warps of 3 tiles 69 us (128 registers do not hold two
+// products' fragments), with 8 of 6 58 us, with 12 of 4 48 us.
+template <int D, bool KV8>
+struct StreamShape {
+  static constexpr int kRow = D * (KV8 ? 1 : 2);
+  static constexpr int kKeys = kRow == 256 ? 16 : 32;
+  static constexpr int kTile = kKeys * kRow;
+  static constexpr int kStage = kTile + kKeys * (KV8 ? 16 : 8);
+  static constexpr int kWarps = kKeys == 16 ? 16 : 12;
+  static constexpr int kStages = kKeys == 16 ? 3 : kTile == 4096 ? 4 : 6;
+  static constexpr int kSmem = kWarps * kStages * kStage;
+  static_assert(kSmem <= 232448 - 1024, "stream rings exceed shared memory");
 };
+constexpr uint32_t kNoRow = 0xffffffffu;
 
-template <int D, typename T, bool KV8, bool CAP>
-__global__ void __launch_bounds__(kStreamThreads, 2) key_weights_stream_kernel(const __grid_constant__ WeightArgs a) {
-  constexpr int CH = KV8 ? D / 64 : D / 32;  // chunks of a row per lane
-  constexpr int ES = KV8 ? 1 : 2;            // bytes per element
+// Byte offset of 16-byte chunk c of row r inside a tile: a fragment load reads 2 rows x 4
+// chunks at a time, in different banks.
+template <int ROW>
+__device__ __forceinline__ uint32_t key_off(int r, int c) {
+  return r * ROW + ((ROW >= 128 ? c ^ ((r & 1) << 2) : c) << 4);
+}
+
+__device__ __forceinline__ void cp_async_16_hint(uint32_t dst, const void* src, uint32_t src_bytes, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst), "l"(src), "r"(src_bytes),
+               "l"(policy)
+               : "memory");
+}
+// Four bytes, both addresses 4-byte aligned; bytes past src_bytes are filled with zeros.
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t at) {
+  uint4 r;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(at));
+  return r;
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t at) {
+  uint32_t r;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(at));
+  return r;
+}
+__device__ __forceinline__ void sts32(uint32_t at, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(at), "r"(v) : "memory");
+}
+
+// MULTI: more than 8 columns a request on average.  Two tiles' fragments stay in registers
+// while the columns pass by (from L1), 8 at a time; without it the first 8 columns stay.
+template <int D, typename T, bool KV8, bool MULTI>
+__global__ void __launch_bounds__(StreamShape<D, KV8>::kWarps * 32, 1) key_weights_stream_kernel(const __grid_constant__ WeightArgs a) {
+  using S = StreamShape<D, KV8>;
+  using O = std::conditional_t<KV8, __half, T>;  // operands: e4m3 codes are exact in fp16
+  constexpr int KS = D / 16;                     // k steps
+  constexpr int CH = S::kRow / 64;               // 16-byte chunks of a row per lane
+  constexpr int K = S::kKeys;
+  constexpr int SPS = MULTI && K == 16 ? 2 : 1;  // tiles of the ring a step
+  constexpr int NS = K / 16, NT = SPS * NS;      // products of 16 keys: of a tile, of a step
+  constexpr int CPR = S::kRow / 16, RPI = 32 / CPR;  // chunks per row, rows per copy instruction
+  extern __shared__ __align__(128) uint8_t smem[];
   // Launched as a programmatic dependent of the kernel before it on the stream:
   // nothing global is touched before that grid has finished.
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t ring = smem_addr(smem) + warp * (S::kStages * S::kStage);
   const int P = a.page_size;
-  const int64_t worker = static_cast<int64_t>(blockIdx.x) * (kStreamThreads / 32) + (threadIdx.x >> 5);
-  const int64_t workers = static_cast<int64_t>(gridDim.x) * (kStreamThreads / 32);
+  const bool whole = P % 16 == 0;  // 16 keys lie in one page
+  const bool cap = a.cap > 0.f;
+  const float cap_in = cap ? a.scale * 2.f * kLog2e / a.cap : 0.f, cap_out = a.cap * kLog2e;
+  const uint32_t vdist = static_cast<uint32_t>(a.hkv) * P;  // rows from a K row to its V row
+  const uint8_t* kv = static_cast<const uint8_t*>(a.kv);
+  const uint64_t policy = l2_policy_evict_first();
+  const int64_t worker = static_cast<int64_t>(warp) * gridDim.x + blockIdx.x;
+  const int64_t workers = static_cast<int64_t>(gridDim.x) * S::kWarps;
   const int64_t listed = min(max(static_cast<int64_t>(__ldg(a.kv_indptr + a.batch)), int64_t{0}), a.kv_pages);
-  const int64_t U = listed * P / kStreamKeys + a.batch;  // places of tiles per kv head
+  const int64_t U = listed * P / K + a.batch;  // places of tiles per kv head
   const int64_t run = (U * a.hkv + workers - 1) / workers;
   int64_t f = worker * run;
   const int64_t f_end = min(f + run, U * a.hkv);
   while (f < f_end) {
     const int h = static_cast<int>(f / U);
     const int64_t base = h * U, u = f - base;
-    const int b = find_request<kStreamKeys>(a, u, lane);
+    const int b = find_request<K>(a, u, lane);
     const Request rq = load_request(a, b);
-    const int64_t c0 = first_tile<kStreamKeys>(a, b), c1 = b + 1 < a.batch ? first_tile<kStreamKeys>(a, b + 1) : U;
+    const int64_t c0 = first_tile<K>(a, b), c1 = b + 1 < a.batch ? first_tile<K>(a, b + 1) : U;
     const int64_t stop = min(f_end, base + max(c1, u + 1));
     f = stop;
     if (!rq.ok) {
       if (lane == 0) flag(a, kErrAppendLayout);
       continue;
     }
-    const int n_tiles = (rq.kv_len + kStreamKeys - 1) / kStreamKeys;
+    const int n_tiles = (rq.kv_len - 1 + K) / K;
     const int t_end = static_cast<int>(min(static_cast<int64_t>(n_tiles), stop - base - c0));
-    int tile = static_cast<int>(max(u - c0, int64_t{0}));
-    if (tile >= t_end) continue;
+    const int t_begin = static_cast<int>(max(u - c0, int64_t{0}));
+    if (t_begin >= t_end) continue;
+
+    // The copy side.  Lane i (of 16, or of 32) looks after key i of a tile: its page id is fetched a
+    // tile ahead, its row counted over the pool's rows.
+    int feed = t_begin, stage_in = 0;
+    int pg = static_cast<int>(static_cast<int64_t>(t_begin) * K / P);
+    int slot = t_begin * K - pg * P;
+    int id, my_slot;
+    auto fetch_id = [&] {
+      const bool in = lane < K && feed < t_end && feed * K + lane < rq.kv_len;
+      int skip = 0, x = slot + lane;
+      if (!whole)
+        skip = static_cast<int>((static_cast<uint32_t>(x) * a.small_div) >> 12);
+      else if (x >= P)  // the second 16 keys' page
+        skip = 1;
+      id = in ? __ldg(a.kv_indices + rq.page0 + pg + skip) : -1;
+      my_slot = in ? x - skip * P : -1;
+      slot += K;
+      if (whole) {
+        while (slot >= P) {
+          slot -= P;
+          ++pg;
+        }
+      } else {
+        const int full = static_cast<int>((static_cast<uint32_t>(slot) * a.small_div) >> 12);
+        pg += full;
+        slot -= full * P;
+      }
+    };
+    // Start the next tile's copies as one cp.async group (an empty one past the last tile).
+    auto issue = [&] {
+      if (feed < t_end) {
+        const uint32_t dst = ring + stage_in * S::kStage;
+        stage_in = stage_in + 1 == S::kStages ? 0 : stage_in + 1;
+        const bool use = id >= 0 && id < a.num_pages;
+        if (!use && my_slot >= 0) flag(a, kErrPageIndex);
+        const uint32_t row = use ? (static_cast<uint32_t>(id) * 2u * a.hkv + h) * P + my_slot : kNoRow;
+        if (whole) {
+          // 16 rows are contiguous: chunk it * 32 + lane.
+          const int left = rq.kv_len - feed * K;
+#pragma unroll
+          for (int n = 0; n < NS; ++n) {
+            const uint32_t first = __shfl_sync(kFullMask, row, 16 * n);
+            const int valid = first == kNoRow ? 0 : left - 16 * n;
+            const uint8_t* src = kv + static_cast<uint64_t>(first == kNoRow ? 0u : first) * S::kRow + lane * 16;
+#pragma unroll
+            for (int it = 0; it < 16 / RPI; ++it) {
+              const int r = it * RPI + lane / CPR;
+              cp_async_16_hint(dst + key_off<S::kRow>(16 * n + r, lane % CPR), r < valid ? src + it * 512 : kv,
+                               r < valid ? 16u : 0u, policy);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int it = 0; it < K / RPI; ++it) {
+            const int r = it * RPI + lane / CPR;
+            const uint32_t at = __shfl_sync(kFullMask, row, r);
+            const uint8_t* src = kv + static_cast<uint64_t>(at == kNoRow ? 0u : at) * S::kRow + (lane % CPR) * 16;
+            cp_async_16_hint(dst + key_off<S::kRow>(r, lane % CPR), src, at == kNoRow ? 0u : 16u, policy);
+          }
+        }
+        if (lane < K) {
+          const uint32_t at = dst + S::kTile + lane * 4;
+          const uint32_t w_row = use ? row - static_cast<uint32_t>(id) * vdist : kNoRow;
+          const bool before = use && a.decay != 0.f && feed * K + lane < rq.weighed;
+          cp_async_4(at, before ? a.weights + w_row : a.weights, before ? 4u : 0u);
+          sts32(at + 4 * K, w_row);
+          if constexpr (KV8) {
+            const uint32_t byte = use ? row : 0u, word = byte & ~3u;
+            const uint64_t rest = static_cast<uint64_t>(a.num_pages) * 2 * vdist - word;  // bytes of the pool from this word on
+            cp_async_4(at + 8 * K, a.scales + word, use ? static_cast<uint32_t>(rest < 4 ? rest : 4) : 0u);
+            sts32(at + 12 * K, (byte - word) * 8);
+          }
+        }
+        ++feed;
+        fetch_id();
+      }
+      cp_async_commit();
+    };
+    fetch_id();
+#pragma unroll 1
+    for (int i = 0; i < S::kStages - 1; ++i) issue();
 
     const int cols = rq.rows << a.lg;
     const int off = rq.kv_len - rq.rows;  // causal: row i sees keys up to i + off
-    // Columns c0 .. c0 + 7: lane (g, t) loads chunk(s) t, t + 4, ... of column c0 + g, and
-    // the negated lse of columns c0 + 2 t and c0 + 2 t + 1 (out: such a column adds nothing).
-    uint32_t qf[D / 16][2];
+    // Columns first .. first + 7: lane (g, t) loads chunk(s) t, t + 4, ... of column first + g, and
+    // the negated lse of columns first + 2 t and first + 2 t + 1.
+    uint32_t qf[KS][2];
     float qs[2] = {1.f, 1.f}, nl[2];
-    bool out[2];
-    int see[2];  // the last key that the column's row sees
+    int see[2];  // the last key that the column's row sees; -1: the column adds nothing
     auto load_columns = [&](int first) {
       const int c = first + g;
       const bool use = c < cols;
@@ -204,11 +331,11 @@ __global__ void __launch_bounds__(kStreamThreads, 2) key_weights_stream_kernel(c
       if constexpr (!KV8) {
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const uint4 x = use ? ld_nc_v4(row + (t + 4 * i) * 8) : make_uint4(0u, 0u, 0u, 0u);
-          qf[2 * i][0] = x.x;
-          qf[2 * i][1] = x.y;
-          qf[2 * i + 1][0] = x.z;
-          qf[2 * i + 1][1] = x.w;
+          const uint4 v = use ? ld_nc_v4(row + (t + 4 * i) * 8) : make_uint4(0u, 0u, 0u, 0u);
+          qf[2 * i][0] = v.x;
+          qf[2 * i][1] = v.y;
+          qf[2 * i + 1][0] = v.z;
+          qf[2 * i + 1][1] = v.w;
         }
       } else {
         // fp16 of q over the power of two below its row's largest element.
@@ -246,164 +373,136 @@ __global__ void __launch_bounds__(kStreamThreads, 2) key_weights_stream_kernel(c
       }
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        const int cc = first + 2 * t + k;
-        const int i = cc >> a.lg;
+        const int cc = first + 2 * t + k, i = cc >> a.lg;
         float l = -INFINITY;
         if (cc < cols) l = __ldg(a.lse + static_cast<int64_t>(rq.row0 + i) * a.hq + (h << a.lg) + (cc & ((1 << a.lg) - 1)));
-        out[k] = l == -INFINITY;
         nl[k] = -l * kLog2e;
-        see[k] = a.causal ? i + off : INT_MAX;
+        see[k] = l == -INFINITY ? -1 : a.causal ? i + off : INT_MAX;
       }
     };
+    load_columns(0);
 
-    // The tile whose page ids are being fetched: its first key's page (of the request) and slot.
-    int ids_tile = tile, pg = static_cast<int>(static_cast<int64_t>(tile) * kStreamKeys / P);
-    int slot = tile * kStreamKeys - pg * P;
-    int id[2], at_slot[2];
-    auto fetch_ids = [&] {
+    int stage_out = 0;
+    for (int tile = t_begin; tile < t_end; tile += SPS) {
+      // Of the kStages - 1 groups ahead the first SPS must have landed.
+      cp_async_wait<S::kStages - 1 - SPS>();
+      __syncwarp();
+      uint32_t fr[NT][KS][4];  // A fragments: keys g and g + 8
+      float ksc[NT][2], sum[NT][2];
+      uint32_t meta[NT];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int x = slot + g + 8 * k;
-        const int skip = P < kStreamKeys ? static_cast<int>((static_cast<uint32_t>(x) * a.small_div) >> 12) : 0;
-        const bool in = ids_tile * kStreamKeys + g + 8 * k < rq.kv_len;
-        id[k] = in ? __ldg(a.kv_indices + rq.page0 + pg + skip) : -1;
-        at_slot[k] = in ? x - skip * P : -1;
-      }
-      ++ids_tile;
-      slot += kStreamKeys;
-      if (P >= kStreamKeys) {
-        if (slot == P) {
-          slot = 0;
-          ++pg;
-        }
-      } else {
-        const int full = static_cast<int>((static_cast<uint32_t>(slot) * a.small_div) >> 12);
-        pg += full;
-        slot -= full * P;
-      }
-    };
-    auto fill = [&](KeyTile<CH>& kt, int tile_no) {
-      const uint8_t* kv = static_cast<const uint8_t*>(a.kv);
-      bool use[2];
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        use[k] = id[k] >= 0 && id[k] < a.num_pages;
-        if (!use[k] && at_slot[k] >= 0 && t == 0) flag(a, kErrPageIndex);
-        const int64_t row = use[k] ? (static_cast<int64_t>(id[k]) * 2 * a.hkv + h) * P + at_slot[k] : 0;
-        const uint8_t* src = kv + row * (D * ES) + t * 16;
-#pragma unroll
-        for (int i = 0; i < CH; ++i) kt.k[k][i] = ld_stream_v4(src + i * 64, use[k]);
-        if constexpr (KV8) kt.scale[k] = __uint_as_float(static_cast<uint32_t>(use[k] ? __ldg(a.scales + row) : 0) << 23);
-      }
-      const int me = t & 1;
-      const bool mine = t < 2 && (me ? use[1] : use[0]);
-      kt.at = mine ? a.weights + (static_cast<int64_t>(me ? id[1] : id[0]) * a.hkv + h) * P + (me ? at_slot[1] : at_slot[0])
-                   : nullptr;
-      const bool before = mine && a.decay != 0.f && tile_no * kStreamKeys + g + 8 * me < rq.weighed;
-      kt.old = before ? *kt.at * a.decay : 0.f;
-    };
-    auto use_tile = [&](const KeyTile<CH>& kt, int tile_no) {
-      const int j = tile_no * kStreamKeys + g;
-      float sum[2] = {0.f, 0.f};
-      for (int first = 0; first < cols; first += 8) {
-        if (cols > 8) load_columns(first);
-        float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < NT; ++n) {
+        const uint32_t at = ring + stage_out * S::kStage;
+        if (n % NS == NS - 1) stage_out = stage_out + 1 == S::kStages ? 0 : stage_out + 1;
+        const int r0 = 16 * (n % NS);  // first row of the 16
+        meta[n] = at + S::kTile + r0 * 4;
+        sum[n][0] = sum[n][1] = 0.f;
 #pragma unroll
         for (int i = 0; i < CH; ++i) {
-          const uint4 x = kt.k[0][i], z = kt.k[1][i];
-          if constexpr (!KV8) {
-            mma_16x8x16<T>(sa, x.x, z.x, x.y, z.y, qf[2 * i][0], qf[2 * i][1]);
-            mma_16x8x16<T>(sb, x.z, z.z, x.w, z.w, qf[2 * i + 1][0], qf[2 * i + 1][1]);
-          } else {
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, zw[4] = {z.x, z.y, z.z, z.w};
+          const uint4 v = lds128(at + key_off<S::kRow>(r0 + g, t + 4 * i)), z = lds128(at + key_off<S::kRow>(r0 + g + 8, t + 4 * i));
+          if constexpr (KV8) {
+            const uint32_t vw[4] = {v.x, v.y, v.z, v.w}, zw[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
-              uint32_t a0, a1, a2, a3;
-              e4m3x4_to_half(xw[w], a0, a2);
-              e4m3x4_to_half(zw[w], a1, a3);
-              mma_16x8x16<__half>((w & 1) ? sb : sa, a0, a1, a2, a3, qf[i * 4 + w][0], qf[i * 4 + w][1]);
+              e4m3x4_to_half(vw[w], fr[n][4 * i + w][0], fr[n][4 * i + w][2]);
+              e4m3x4_to_half(zw[w], fr[n][4 * i + w][1], fr[n][4 * i + w][3]);
             }
+          } else {
+            fr[n][2 * i][0] = v.x; fr[n][2 * i][2] = v.y;
+            fr[n][2 * i + 1][0] = v.z; fr[n][2 * i + 1][2] = v.w;
+            fr[n][2 * i][1] = z.x; fr[n][2 * i][3] = z.y;
+            fr[n][2 * i + 1][1] = z.z; fr[n][2 * i + 1][3] = z.w;
           }
         }
+        if constexpr (KV8) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {  // key j + 8 (k / 2), column 2 t + k % 2
-          const int c = k & 1, r = k >> 1;
-          float s = sa[k] + sb[k];
-          if constexpr (KV8) s *= qs[c] * kt.scale[r];
-          float y;
-          if constexpr (CAP)
-            y = fmaf(a.cap * kLog2e, tanh_from_log2(s * (a.scale * 2.f * kLog2e / a.cap)), nl[c]);
-          else
-            y = fmaf(s, a.scale, nl[c]);
-          const float p = fast_exp2(y);
-          sum[r] += out[c] || j + 8 * r > see[c] ? 0.f : p;
+          for (int r = 0; r < 2; ++r) {
+            const uint32_t k = (g + 8 * r) * 4;
+            ksc[n][r] = __uint_as_float(((lds32(meta[n] + 8 * K + k) >> lds32(meta[n] + 12 * K + k)) & 255u) << 23);
+          }
         }
       }
+      for (int first = 0;;) {
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        sum[r] += __shfl_xor_sync(kFullMask, sum[r], 1);
-        sum[r] += __shfl_xor_sync(kFullMask, sum[r], 2);
+        for (int n = 0; n < NT; ++n) {
+          float sa[4] = {0.f, 0.f, 0.f, 0.f}, sb[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < KS; i += 2) {
+            mma_16x8x16<O>(sa, fr[n][i][0], fr[n][i][1], fr[n][i][2], fr[n][i][3], qf[i][0], qf[i][1]);
+            mma_16x8x16<O>(sb, fr[n][i + 1][0], fr[n][i + 1][1], fr[n][i + 1][2], fr[n][i + 1][3], qf[i + 1][0], qf[i + 1][1]);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {  // key g + 8 (k / 2) of the tile, column 2 t + k % 2
+            const int c = k & 1, r = k >> 1, j = tile * K + 16 * n + g + 8 * r;
+            float s = sa[k] + sb[k];
+            if constexpr (KV8) s *= qs[c] * ksc[n][r];
+            const float y = cap ? fmaf(cap_out, tanh_from_log2(s * cap_in), nl[c]) : fmaf(s, a.scale, nl[c]);
+            const float p = fast_exp2(y);
+            sum[n][r] += j > see[c] ? 0.f : p;
+          }
+        }
+        first += 8;
+        if (first >= cols) break;
+        load_columns(first);
       }
-      if (kt.at) *kt.at = kt.old + ((t & 1) ? sum[1] : sum[0]);
-    };
-
-    if (cols <= 8) load_columns(0);
-    KeyTile<CH> even, odd;
-    fetch_ids();
-    fill(even, tile);
-    fetch_ids();
-    for (;;) {
-      if (tile + 1 < t_end) {
-        fill(odd, tile + 1);
-        fetch_ids();
+      if (cols > 8) load_columns(0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          sum[n][r] += __shfl_xor_sync(kFullMask, sum[n][r], 1);
+          sum[n][r] += __shfl_xor_sync(kFullMask, sum[n][r], 2);
+        }
+        // Lane t = 0 has key g, t = 1 key g + 8.
+        if (t < 2 && tile + n / NS < t_end) {
+          const uint32_t k = (g + 8 * t) * 4, w_row = lds32(meta[n] + 4 * K + k);
+          if (w_row != kNoRow) a.weights[w_row] = fmaf(__uint_as_float(lds32(meta[n] + k)), a.decay, t ? sum[n][1] : sum[n][0]);
+        }
       }
-      use_tile(even, tile);
-      if (++tile >= t_end) break;
-      if (tile + 1 < t_end) {
-        fill(even, tile + 1);
-        fetch_ids();
-      }
-      use_tile(odd, tile);
-      if (++tile >= t_end) break;
+      __syncwarp();  // every lane has read the stages before they are filled again
+#pragma unroll 1
+      for (int n = 0; n < SPS; ++n) issue();
     }
+    cp_async_wait<0>();
+    __syncwarp();
   }
 }
 
 // ------------------------------------------------------------------------------ tile
 constexpr int kD = prefill_impl::kD;
 constexpr int kTileKeys = 128;
-constexpr int kTileCols = 64;             // (row, head) pairs of one product
-constexpr int kQStages = 5;
-constexpr int kSBufs = 3;
+constexpr int kTileCols = 64;                 // (row, head) pairs of one product
+constexpr int kQStages = 3;                   // the last two bring the keys first
 constexpr uint32_t kQHalf = kTileCols * 128;  // 64 of the 128 dims of 64 columns
 constexpr uint32_t kQTile = 2 * kQHalf;
-constexpr int kTileThreads = 320;         // two groups of 4 warps, the Q producer, the MMA issuer
+constexpr int kTileThreads = 192;             // four warps of keys, the Q producer, the MMA issuer
+constexpr int kTileCtas = 4;                  // per SM
 constexpr int kTileSmem = kQStages * kQTile + 1024;
-constexpr uint32_t kWTmemCols = 256;      // K 64, then three S^T buffers: two CTAs share an SM's 512
+constexpr uint32_t kWTmemCols = 128;          // K 64, S^T 64
 constexpr uint32_t kColSt = 64;
 
 struct TileShared {
-  uint64_t q_full[kQStages], q_empty[kQStages], s_full[kSBufs], s_empty[kSBufs], k_full, drain;
+  uint64_t q_full[kQStages], q_empty[kQStages], s_full, s_empty, k_full, drain;
+  alignas(16) float nl[2][kTileCols];  // read as float4; negated lse in log2 units, -inf for a column that adds nothing
+  float sum[kTileKeys];
   uint32_t tmem;
   int abort;
-  alignas(16) float nl[2][2][kTileCols];  // read as float4; [group][buffer]: negated lse in log2 units, -inf for a column that adds nothing
-  float part[2][kTileKeys];
-  float sum[kTileKeys];
 };
 
-// All 128 threads of a group arrive; true where any of them brought true.
-__device__ __forceinline__ bool group_any(int group, bool x) {
+// All 128 threads with keys arrive; true where any of them brought true.
+__device__ __forceinline__ bool keys_any(bool x) {
   int r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %1, 0;\n\t"
-      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+      "barrier.cta.red.or.pred q, 1, 128, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"(static_cast<int>(x)), "r"(group + 1)
+      : "r"(static_cast<int>(x))
       : "memory");
   return r != 0;
 }
 
 __device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -421,17 +520,11 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   return v;
 }
 
-__device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]) {
-  asm volatile(
-      "{\n\t.reg .b32 a1;\n\tadd.u32 a1, %64, 32;\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
-      "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [a1];\n\t"
-      "tcgen05.wait::ld.sync.aligned;\n\t}"
-      : PKV_R32(r), PKV_R32((r + 32))
-      : "r"(taddr)
-      : "memory");
+// The smaller of the two; NaN where one is.
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
 }
 
 // Four e4m3 codes to two pairs of T (exact).
@@ -447,7 +540,7 @@ __device__ __forceinline__ void e4m3x4_to(uint32_t w, uint32_t& lo, uint32_t& hi
 }
 
 template <typename T, bool KV8, bool CAP>
-__global__ void __launch_bounds__(kTileThreads, 2)
+__global__ void __launch_bounds__(kTileThreads, kTileCtas)
     key_weights_tile_kernel(const __grid_constant__ WeightArgs a, const __grid_constant__ CUtensorMap tq, int share) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ TileShared sh;
@@ -457,7 +550,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   constexpr uint32_t kFmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int P = a.page_size;
-  const uint32_t rank = share > 1 ? cluster_rank() : 0u;
+  const int rank = share > 1 ? static_cast<int>(cluster_rank()) : 0;
   // This cluster's key tile: kv heads of a tile side by side.
   const int64_t item = blockIdx.x / share;
   const int64_t u = item / a.hkv;
@@ -474,7 +567,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
   const int row_first = a.causal ? min(max(k0 - off, 0), rq.rows) : 0;  // the first row that sees key k0
   const int per = kTileCols >> a.lg;                                    // rows of a column tile
   const int n_all = (rq.rows - row_first + per - 1) / per;
-  const int n = n_all > static_cast<int>(rank) ? (n_all - 1 - static_cast<int>(rank)) / share + 1 : 0;  // rank, rank + share, ...
+  const int n = n_all > rank ? (n_all - 1 - rank) / share + 1 : 0;      // column tiles rank, rank + share, ...
 
   uint32_t base = smem_addr(smem_raw);
   base = (base + 1023u) & ~1023u;
@@ -484,16 +577,14 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       mbar_init(bar(sh.q_full[i]), 1);
       mbar_init(bar(sh.q_empty[i]), 1);
     }
-    for (int i = 0; i < kSBufs; ++i) {
-      mbar_init(bar(sh.s_full[i]), 1);
-      mbar_init(bar(sh.s_empty[i]), 128);
-    }
-    mbar_init(bar(sh.k_full), 256);
+    mbar_init(bar(sh.s_full), 1);
+    mbar_init(bar(sh.s_empty), 128);
+    mbar_init(bar(sh.k_full), 128);
     mbar_init(bar(sh.drain), 1);
     sh.abort = 0;
     fence_mbar_init();
   }
-  if (warp == 9) {
+  if (warp == 5) {
     tmem_alloc(smem_addr(&sh.tmem), kWTmemCols);
     tmem_relinquish();
   }
@@ -518,17 +609,18 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     return true;
   };
 
-  float old = 0.f;
+  float old = 0.f, total = 0.f;
   float* at = nullptr;
-  if (warp == 8) {
+  if (warp == 4) {
     // ------------------------------------------------------------ Q producer
     if (lane == 0) {
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % kQStages;
+        if (i == 1 && !wait(sh.k_full, 0)) break;  // the keys have left the room of stages 1 and 2
         if (i >= kQStages && !wait(sh.q_empty[s], (i / kQStages - 1) & 1)) break;
         mbar_arrive_expect_tx(bar(sh.q_full[s]), kQTile);
-        const int row = rq.row0 + row_first + (static_cast<int>(rank) + i * share) * per;
+        const int row = rq.row0 + row_first + (rank + i * share) * per;
         for (int x = 0; x < 2; ++x)
           tma_load_3d(base + s * kQTile + x * kQHalf, &tq, x * 64, h << a.lg, row, bar(sh.q_full[s]));
       }
@@ -543,7 +635,7 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       }
     }
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
     if (lane == 0) {
       const uint32_t idesc = umma_idesc_f16(kFmt, kTileKeys, kTileCols, 0);
@@ -552,17 +644,17 @@ __global__ void __launch_bounds__(kTileThreads, 2)
       bool ok = n == 0 || wait(sh.k_full, 0);
       tc_fence_after();
       for (int i = 0; i < n && ok; ++i) {
-        const int s = i % kQStages, d = i % kSBufs;
-        if (i >= kSBufs && !(ok = wait(sh.s_empty[d], (i / kSBufs - 1) & 1))) break;
+        const int s = i % kQStages;
         if (!(ok = wait(sh.q_full[s], (i / kQStages) & 1))) break;
+        if (i > 0 && !(ok = wait(sh.s_empty, (i - 1) & 1))) break;
         tc_fence_after();
-        const uint32_t dst = tmem + kColSt + d * kTileCols, b0 = q_lo + s * (kQTile >> 4);
+        const uint32_t dst = tmem + kColSt, b0 = q_lo + s * (kQTile >> 4);
         prefill_impl::umma_ts_lo<false>(dst, tmem, b0, hi, idesc);
 #pragma unroll
         for (int kk = 1; kk < kD / 16; ++kk)
           prefill_impl::umma_ts_lo<true>(dst, tmem + kk * 8, b0 + (kk / 4) * (kQHalf >> 4) + (kk % 4) * 2, hi, idesc);
+        umma_commit(bar(sh.s_full));
         umma_commit(bar(sh.q_empty[s]));
-        umma_commit(bar(sh.s_full[d]));
       }
       // Every MMA issued so far must finish before tensor memory is released.
       umma_commit(bar(sh.drain));
@@ -576,87 +668,91 @@ __global__ void __launch_bounds__(kTileThreads, 2)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ keys, then their sums
-    const int x = warp >> 2, quarter = warp & 3;
-    const int r = quarter * 32 + lane, j = k0 + r;   // this thread's key
-    const uint32_t lane_off = static_cast<uint32_t>(quarter * 32) << 16;
-    const int gt = tid & 127;                        // thread of the group
-    bool use = j < rq.kv_len;
-    int64_t row = 0;
-    if (use) {
+    const int j = k0 + tid;  // this thread's key: its lane of tensor memory
+    const uint32_t lane_off = static_cast<uint32_t>(warp * 32) << 16;
+    uint32_t row = kNoRow;
+    float mul = a.scale;
+    if (j < rq.kv_len) {
       const int pg = j / P, page = __ldg(a.kv_indices + rq.page0 + pg);
-      use = page >= 0 && page < a.num_pages;
-      if (use) {
-        row = (static_cast<int64_t>(page) * 2 * a.hkv + h) * P + (j - pg * P);
-        if (x == 0 && rank == 0) {
+      if (page >= 0 && page < a.num_pages) {
+        row = (static_cast<uint32_t>(page) * 2u * a.hkv + h) * P + (j - pg * P);
+        if (rank == 0) {
           at = a.weights + (static_cast<int64_t>(page) * a.hkv + h) * P + (j - pg * P);
           if (a.decay != 0.f && j < rq.weighed) old = *at * a.decay;
         }
-      } else if (x == 0) {
+      } else {
         flag(a, kErrPageIndex);
       }
     }
-    float mul = a.scale;
+    __syncwarp();
+    // The key's values, two to a column: the A operand.  A warp brings its 32 rows, whole
+    // segments a copy, through the later Q stages' room; then a lane reads its own row.
     {
-      // Group x brings the key's dims 64 x .. 64 x + 63 into its lane of tensor memory, two
-      // 16-bit values a column: the A operand.
-      uint32_t w[32];
-      if constexpr (KV8) {
-        const uint8_t* src = static_cast<const uint8_t*>(a.kv) + row * kD + x * 64;
+      constexpr int kRow = KV8 ? kD : 2 * kD, kCpr = kRow / 16, kRpi = 32 / kCpr;
+      const uint32_t room = base + kQTile + warp * 32 * kRow;
+      const uint8_t* kv = static_cast<const uint8_t*>(a.kv) + (lane % kCpr) * 16;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint4 v = ld_stream_v4(src + i * 16, use);
-          e4m3x4_to<T>(v.x, w[8 * i], w[8 * i + 1]);
-          e4m3x4_to<T>(v.y, w[8 * i + 2], w[8 * i + 3]);
-          e4m3x4_to<T>(v.z, w[8 * i + 4], w[8 * i + 5]);
-          e4m3x4_to<T>(v.w, w[8 * i + 6], w[8 * i + 7]);
-        }
-        mul *= __uint_as_float(static_cast<uint32_t>(use ? __ldg(a.scales + row) : 0) << 23);
-      } else {
-        const T* src = static_cast<const T*>(a.kv) + row * kD + x * 64;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint4 v = ld_stream_v4(src + i * 8, use);
-          w[4 * i] = v.x;
-          w[4 * i + 1] = v.y;
-          w[4 * i + 2] = v.z;
-          w[4 * i + 3] = v.w;
-        }
+      for (int it = 0; it < 32 / kRpi; ++it) {
+        const int r = it * kRpi + lane / kCpr;
+        const uint32_t from = __shfl_sync(kFullMask, row, r);
+        cp_async_16(room + r * kRow + (((lane % kCpr) ^ (r & 7)) << 4), kv + static_cast<uint64_t>(from == kNoRow ? 0u : from) * kRow,
+                    from == kNoRow ? 0u : 16u);
       }
-      tmem_st32(tmem + lane_off + x * 32, w);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(bar(sh.k_full));
+      cp_async_commit();
+      if constexpr (KV8) mul *= __uint_as_float(static_cast<uint32_t>(row != kNoRow ? __ldg(a.scales + row) : 0) << 23);
+      cp_async_wait<0>();
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < kCpr / 2; ++i) {
+          const uint4 v = lds128(room + lane * kRow + (((x * (kCpr / 2) + i) ^ (lane & 7)) << 4));
+          if constexpr (KV8) {
+            e4m3x4_to<T>(v.x, w[8 * i], w[8 * i + 1]);
+            e4m3x4_to<T>(v.y, w[8 * i + 2], w[8 * i + 3]);
+            e4m3x4_to<T>(v.z, w[8 * i + 4], w[8 * i + 5]);
+            e4m3x4_to<T>(v.w, w[8 * i + 6], w[8 * i + 7]);
+          } else {
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+          }
+        }
+        tmem_st32(tmem + lane_off + x * 32, w);
+      }
+      fence_proxy_async_smem();  // the room is the Q copies' from here on
     }
-    // Column gt (< 64) of a column tile: its negated lse, -inf where it adds nothing.
+    tmem_wait_st();
+    tc_fence_before();
+    mbar_arrive(bar(sh.k_full));
+    // Column tid (< 64) of column tile i: its negated lse, -inf where it adds nothing.
     auto load_nl = [&](int i) {
       float v = -INFINITY;
-      if (i < n && gt < kTileCols) {
-        const int q_row = row_first + (static_cast<int>(rank) + i * share) * per + (gt >> a.lg);
+      if (i < n && tid < kTileCols) {
+        const int q_row = row_first + (rank + i * share) * per + (tid >> a.lg);
         if (q_row < rq.rows) {
           const float l =
-              __ldg(a.lse + static_cast<int64_t>(rq.row0 + q_row) * a.hq + (h << a.lg) + (gt & ((1 << a.lg) - 1)));
+              __ldg(a.lse + static_cast<int64_t>(rq.row0 + q_row) * a.hq + (h << a.lg) + (tid & ((1 << a.lg) - 1)));
           v = l == -INFINITY ? -INFINITY : -l * kLog2e;
         }
       }
       return v;
     };
     float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-    float next_nl = load_nl(x);
+    float next_nl = load_nl(0);
     bool ok = true;
-    for (int i = x, k = 0; i < n; i += 2, ++k) {  // every warp meets the group's barrier n times, come what may
-      float* nl = sh.nl[x][k & 1];
-      if (gt < kTileCols) nl[gt] = next_nl;
-      const bool some_out = group_any(x, gt < kTileCols && next_nl == -INFINITY);
-      next_nl = load_nl(i + 2);
-      const int d = i % kSBufs;
-      if (ok) ok = __all_sync(kFullMask, wait(sh.s_full[d], (i / kSBufs) & 1));
+    for (int i = 0; i < n; ++i) {  // every warp meets the barrier n times, come what may
+      float* nl = sh.nl[i & 1];
+      if (tid < kTileCols) nl[tid] = next_nl;
+      const bool some_out = keys_any(tid < kTileCols && next_nl == -INFINITY);
+      next_nl = load_nl(i + 1);
+      if (ok) ok = __all_sync(kFullMask, wait(sh.s_full, i & 1));
       if (!ok) continue;
       tc_fence_after();
-      uint32_t sr[64];
-      tmem_ld64_sync(tmem + lane_off + kColSt + d * kTileCols, sr);
-      tc_fence_before();
-      mbar_arrive(bar(sh.s_empty[d]));
-      const int q_row = row_first + (static_cast<int>(rank) + i * share) * per;
+      const int q_row = row_first + (rank + i * share) * per;
+      const int cols = min((rq.rows - q_row) << a.lg, kTileCols);  // (no overflow: at most 64 are asked for)
       // The first column whose row sees this key.
       const int c_min = a.causal ? max(j - off - q_row, 0) << a.lg : 0;
       const bool masked = some_out || (a.causal && k0 + kTileKeys - 1 - off > q_row);
@@ -666,67 +762,86 @@ __global__ void __launch_bounds__(kTileThreads, 2)
         k_in = mul * 2.f * kLog2e / a.cap;
         k_out = a.cap * kLog2e;
       }
-#pragma unroll
-      for (int c = 0; c < kTileCols; c += 4) {
-        const float4 l4 = *reinterpret_cast<const float4*>(nl + c);
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float2 s = make_float2(__uint_as_float(sr[c + 2 * e]), __uint_as_float(sr[c + 2 * e + 1]));
-          const float2 l = e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
-          float2 y;
-          if constexpr (CAP) {
-            // cap tanh(y) = k_out - 2 k_out / (e^(2y) + 1), e^(2y) = 2^(s k_in)
-            float2 z = fmul2(s, make_float2(k_in, k_in));
-            z.x = fast_exp2(z.x);
-            z.y = fast_exp2(z.y);
-            z = fadd2(z, make_float2(1.f, 1.f));
-            z.x = fast_rcp(z.x);
-            z.y = fast_rcp(z.y);
-            y = fadd2(ffma2(z, make_float2(-2.f * k_out, -2.f * k_out), make_float2(k_out, k_out)), l);
-          } else {
-            y = ffma2(s, mul2, l);
-          }
-          float2 p = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-          if (masked) {
-            if (c + 2 * e < c_min || l.x == -INFINITY) p.x = 0.f;
-            if (c + 2 * e + 1 < c_min || l.y == -INFINITY) p.y = 0.f;
-          }
-          acc[e] = fadd2(acc[e], p);
+#pragma unroll(CAP ? 1 : 2)
+      for (int half = 0; half < 2; ++half) {
+        uint32_t sr[32];
+        const bool any = half * 32 < cols;
+        if (any) tmem_ld32_sync(tmem + lane_off + kColSt + half * 32, sr);
+        if (half == 1) {  // S^T is free for the next column tile
+          tc_fence_before();
+          mbar_arrive(bar(sh.s_empty));
         }
+        if (!any) break;
+        auto add = [&](auto masked_c) {
+          constexpr bool kMasked = decltype(masked_c)::value;
+          const int c_from = c_min - half * 32;
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 l4 = *reinterpret_cast<const float4*>(nl + half * 32 + c);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 s = make_float2(__uint_as_float(sr[c + 2 * e]), __uint_as_float(sr[c + 2 * e + 1]));
+              const float2 l = e ? make_float2(l4.z, l4.w) : make_float2(l4.x, l4.y);
+              // Which of the two do not count (always known to be false without kMasked).
+              const bool out0 = kMasked && (c + 2 * e < c_from || l.x == -INFINITY);
+              const bool out1 = kMasked && (c + 2 * e + 1 < c_from || l.y == -INFINITY);
+              float2 y;
+              if constexpr (CAP) {
+                // cap tanh(y) = k_out - 2 k_out / (e^(2y) + 1), e^(2y) = 2^(s k_in), with one
+                // reciprocal for both: 1 / a = b (1 / ab).  2^60 is infinity here, so that ab
+                // stays finite; NaN stays NaN, and one that does not count is kept from the other.
+                float2 z = fmul2(s, make_float2(k_in, k_in));
+                z.x = out0 ? 0.f : min_nan(z.x, 60.f);
+                z.y = out1 ? 0.f : min_nan(z.y, 60.f);
+                z = fadd2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(1.f, 1.f));
+                const float r = fast_rcp(z.x * z.y);
+                z = fmul2(make_float2(z.y, z.x), make_float2(r, r));
+                y = fadd2(ffma2(z, make_float2(-2.f * k_out, -2.f * k_out), make_float2(k_out, k_out)), l);
+              } else {
+                y = ffma2(s, mul2, l);
+              }
+              const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
+              acc[e] = fadd2(acc[e], make_float2(out0 ? 0.f : p0, out1 ? 0.f : p1));
+            }
+          }
+        };
+        if (masked)
+          add(std::true_type{});
+        else
+          add(std::false_type{});
       }
     }
     const float2 s2 = fadd2(acc[0], acc[1]);
-    sh.part[x][r] = s2.x + s2.y;
+    total = s2.x + s2.y;
+    sh.sum[tid] = total;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, kWTmemCols);
+  if (warp == 5) tmem_dealloc(tmem, kWTmemCols);
   if (sh.abort) at = nullptr;  // sums that a wait left incomplete
   if (share > 1) {
-    if (tid < kTileKeys) sh.sum[tid] = sh.part[0][tid] + sh.part[1][tid];
-    __syncwarp();
     cluster_sync_all();
-    if (rank == 0 && at) {
-      float v = 0.f;
-      for (int k = 0; k < share; ++k) v += ld_cluster_f32(smem_addr(&sh.sum[tid]), k);
-      *at = old + v;
+    if (at) {  // rank 0's keys
+      total = 0.f;
+      for (int k = 0; k < share; ++k) total += ld_cluster_f32(smem_addr(&sh.sum[tid]), k);
     }
-    __syncwarp();
     cluster_sync_all();  // a CTA's sums stay until they have been read
-  } else if (at) {
-    *at = old + (sh.part[0][tid] + sh.part[1][tid]);
   }
+  if (at) *at = old + total;
 }
 
 template <int D, typename T>
-cudaError_t launch_stream(const WeightArgs& a, bool cap, int grid, cudaStream_t s) {
+cudaError_t launch_stream(const WeightArgs& a, bool multi, int grid, cudaStream_t s) {
   void (*kern)(WeightArgs) = nullptr;
   if (a.scales)
-    kern = cap ? key_weights_stream_kernel<D, T, true, true> : key_weights_stream_kernel<D, T, true, false>;
+    kern = multi ? key_weights_stream_kernel<D, T, true, true> : key_weights_stream_kernel<D, T, true, false>;
   else
-    kern = cap ? key_weights_stream_kernel<D, T, false, true> : key_weights_stream_kernel<D, T, false, false>;
-  return launch_dependent(kern, grid, kStreamThreads, 0, s, a);
+    kern = multi ? key_weights_stream_kernel<D, T, false, true> : key_weights_stream_kernel<D, T, false, false>;
+  const int smem = a.scales ? StreamShape<D, true>::kSmem : StreamShape<D, false>::kSmem;
+  const int warps = a.scales ? StreamShape<D, true>::kWarps : StreamShape<D, false>::kWarps;
+  cudaError_t e = ensure_smem_limit(kern, smem);
+  return e == cudaSuccess ? launch_dependent(kern, grid, warps * 32, smem, s, a) : e;
 }
 
 template <typename T>
@@ -786,6 +901,9 @@ extern "C" pkv_status pkv_add_key_weights(const pkv_params* p, int batch, int64_
   if (batch == 0 || kv_pages == 0) return PKV_OK;  // no keys
   if (!kv_indptr_d || !kv_indices_d || !kv_last_page_len_d || !kv || !weights) return PKV_ERR_INVALID_ARG;
   if (total_q > 0 && (!q || !lse)) return PKV_ERR_INVALID_ARG;
+  // Rows of the pool are counted in 32 bits, with the last value for none.
+  if (static_cast<double>(num_pages) * 2 * p->num_kv_heads * p->page_size >= 4294967295.0) return PKV_ERR_UNSUPPORTED;
+  if (!aligned(kv8_scales, 4)) return PKV_ERR_INVALID_ARG;  // exponent bytes are copied in fours
   if (!aligned(q, 16) || !aligned(kv, 16) || !aligned(lse, 4) || !aligned(weights, 4) || !aligned(qo_indptr_d, 4) ||
       !aligned(kv_indptr_d, 4) || !aligned(kv_indices_d, 4) || !aligned(kv_last_page_len_d, 4) ||
       !aligned(weighed_len_d, 4) || !aligned(error_d, 4))
@@ -824,12 +942,14 @@ extern "C" pkv_status pkv_add_key_weights(const pkv_params* p, int batch, int64_
   auto s = static_cast<cudaStream_t>(stream);
   const int64_t tokens = kv_pages * p->page_size;
   // Many columns per request: the tensor-core tiles.
-  const int64_t items = (tokens / kTileKeys + batch) * p->num_kv_heads;
+  const int64_t places = tokens / kTileKeys + batch, items = places * p->num_kv_heads;
   if (p->head_dim == kD && total_q * g > int64_t{32} * batch && items <= INT32_MAX / 8) {
-    // Key tiles too few for the chip are shared by a cluster, as long as each of its CTAs
-    // has a column tile.
+    // Causal prompts' key tiles differ in their columns, up to all of a request's for the first
+    // one: clusters share the columns of a tile until there are six CTAs an SM, as long as each
+    // has eight column tiles of a request of average length.  (Prompts of 128 to 1500 rows, 8 kv
+    // heads: alone 94 us, two CTAs a tile 74 us, four 73 us.)
     int share = 1;
-    while (share < 8 && items * share * 2 <= 2 * sms && total_q * g >= int64_t{kTileCols} * batch * share * 2) share *= 2;
+    while (share < 8 && items * share < 6 * sms && total_q * g >= int64_t{16 * kTileCols} * batch * share) share *= 2;
     CUtensorMap tq;
     cudaError_t e = prefill_impl::make_rows_map(q, p->dtype, a.hq, total_q, static_cast<int64_t>(a.hq) * kD, g, kTileCols / g, tq);
     if (e == cudaSuccess)
@@ -837,12 +957,13 @@ extern "C" pkv_status pkv_add_key_weights(const pkv_params* p, int batch, int64_
                                : launch_tile<__half>(a, cap, items, share, tq, s);
     return status_of(e);
   }
-  const int64_t tiles = (tokens / kStreamKeys + batch) * p->num_kv_heads, ctas = (tiles + 7) / 8;
-  const int grid = static_cast<int>(std::min<int64_t>(ctas, 2 * sms));
+  const int64_t tiles = (tokens / 16 + batch) * p->num_kv_heads;  // (of 32 keys: half as many)
+  const int grid = static_cast<int>(std::min<int64_t>(tiles, sms));
+  const bool multi = total_q * g > int64_t{8} * batch;
   cudaError_t e;
   if (p->head_dim == 128)
-    e = p->dtype == PKV_BF16 ? launch_stream<128, __nv_bfloat16>(a, cap, grid, s) : launch_stream<128, __half>(a, cap, grid, s);
+    e = p->dtype == PKV_BF16 ? launch_stream<128, __nv_bfloat16>(a, multi, grid, s) : launch_stream<128, __half>(a, multi, grid, s);
   else
-    e = p->dtype == PKV_BF16 ? launch_stream<64, __nv_bfloat16>(a, cap, grid, s) : launch_stream<64, __half>(a, cap, grid, s);
+    e = p->dtype == PKV_BF16 ? launch_stream<64, __nv_bfloat16>(a, multi, grid, s) : launch_stream<64, __half>(a, multi, grid, s);
   return status_of(e);
 }
