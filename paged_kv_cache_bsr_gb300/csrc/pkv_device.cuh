@@ -102,6 +102,13 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return y;
 }
 
+// The smaller of the two; NaN where one is.
+__device__ __forceinline__ float min_nan(float x, float y) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(y));
+  return r;
+}
+
 // tanh(y) from the identity tanh(y) = 1 - 2 / (e^(2y) + 1), with e^(2y) written as
 // 2^(y * 2 log2(e)): the caller passes t = y * 2 log2(e).  Two SFU operations and no
 // branch; it saturates to +1 (e^(2y) = inf) and -1 (e^(2y) = 0).  Near 0 the

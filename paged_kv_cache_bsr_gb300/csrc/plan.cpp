@@ -748,9 +748,9 @@ int64_t key_chunk(int64_t total, int C) { return std::max<int64_t>(ceil_div(tota
 // their times.
 constexpr int64_t kItemOverhead = 2;
 int64_t prefill_makespan(const std::vector<int64_t>& nb_tiles, int64_t total, int C, std::vector<int64_t>& by_cost,
-                         std::vector<int64_t>& by_load) {
+                         std::vector<int64_t>& by_load, int64_t chunk = 0) {
   if (C <= 0) return 0;
-  const int64_t chunk = key_chunk(total, C);
+  if (chunk <= 0) chunk = key_chunk(total, C);
   by_cost.assign(chunk + 1 + kItemOverhead, 0);
   int64_t items = 0;
   auto add = [&](int64_t c, int64_t m) {
@@ -788,6 +788,30 @@ int64_t prefill_makespan(const std::vector<int64_t>& nb_tiles, int64_t total, in
   return worst;
 }
 
+// Key blocks per work item of a plan over packed rows: key_chunk's, or larger ones up to
+// whole tiles where the cut does not pay.  Estimated in key blocks: the makespan, and for
+// cut tiles the merge's launch (3 us) and their fp32 states' way through memory (256 KB
+// written and read a slot), against 1.83 us a block.  12 heads x 5 requests of 170 to 650
+// rows against 330 to 1480 keys, 132 tiles of up to 12 blocks on 152 CTAs: a call
+// with 108 of them cut 59.7 us, with all whole 48.4 us.
+int64_t ragged_chunk(const std::vector<int64_t>& nb_tiles, int64_t total, int C, std::vector<int64_t>& by_cost,
+                     std::vector<int64_t>& by_load) {
+  const int64_t least = key_chunk(total, C), whole = std::max<int64_t>(static_cast<int64_t>(nb_tiles.size()) - 1, 1);
+  int64_t best = least;
+  double best_cost = 0.0;
+  for (int64_t chunk = std::min(least, whole);; chunk = std::min(chunk * 2, whole)) {
+    int64_t slots = 0;
+    for (int64_t nb = chunk + 1; nb < static_cast<int64_t>(nb_tiles.size()); ++nb) slots += nb_tiles[nb] * ceil_div(nb, chunk);
+    const double cost = static_cast<double>(prefill_makespan(nb_tiles, total, C, by_cost, by_load, chunk)) +
+                        (slots ? 1.6 + 0.05 * static_cast<double>(slots) : 0.0);
+    if (chunk == std::min(least, whole) || cost <= best_cost) {
+      best_cost = cost;
+      best = chunk;
+    }
+    if (chunk == whole) return best;
+  }
+}
+
 // Prefill work over `C` CTAs; with skip_single the requests holding one query
 // row are left out (they are the decode half of a mixed batch).
 pkv_status compute_prefill(pkv_plan* pl, int batch, const int32_t* qo_indptr, const int32_t* kv_indptr,
@@ -814,8 +838,9 @@ pkv_status compute_prefill(pkv_plan* pl, int batch, const int32_t* qo_indptr, co
     mask_off[b + 1] = mask_off[b] + static_cast<int64_t>(qo_indptr[b + 1] - qo_indptr[b]) *
                                         kv_len_of(kv_indptr, kv_last, b, P);
   pl->mask_bits = mask_off[batch];
-  const int64_t total = query_tile_blocks(pl, batch, qo_indptr, kv_indptr, kv_last, skip_single, nullptr, P);
-  const int64_t chunk = key_chunk(total, C);
+  const int64_t total =
+      query_tile_blocks(pl, batch, qo_indptr, kv_indptr, kv_last, skip_single, pl->ragged ? &sc.nb_tiles : nullptr, P);
+  const int64_t chunk = pl->ragged ? ragged_chunk(sc.nb_tiles, total, C, sc.by_cost, sc.by_load) : key_chunk(total, C);
   // Each tile gives at most as many items as it counts blocks.
   items.reserve(static_cast<size_t>(std::min<int64_t>(total, pl->max_work) + 1));
   item_cost.reserve(items.capacity());

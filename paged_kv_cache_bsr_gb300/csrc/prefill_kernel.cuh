@@ -582,14 +582,33 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
           const float k_in = scale * 2.f * kLog2e / a.cap, k_out = a.cap * kLog2e;
           const float2 kin2 = make_float2(k_in, k_in), one2 = make_float2(1.f, 1.f);
           const float2 m2k = make_float2(-2.f * k_out, -2.f * k_out), kout2 = make_float2(k_out, k_out);
+          if constexpr (RAGGED) {
+            // Keys that the row does not see are kept from the pairs below.
+            if (!full) {
+#pragma unroll
+              for (int i = 0; i < kBN; ++i)
+                if (key0 + i >= limit) sr[i] = 0u;
+            }
+          }
 #pragma unroll
           for (int i = 0; i < kBN; i += 2) {
             float2 e = fmul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), kin2);
+            if constexpr (RAGGED) {  // 2^60 is infinity here, so that the product of two stays finite
+              e.x = min_nan(e.x, 60.f);
+              e.y = min_nan(e.y, 60.f);
+            }
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
             float2 d = fadd2(e, one2);
-            d.x = fast_rcp(d.x);
-            d.y = fast_rcp(d.y);
+            if constexpr (RAGGED) {
+              // One reciprocal for two (half the exponential's rate): 1 / a = b (1 / ab).  (The
+              // other instances keep their bits.)
+              const float r = fast_rcp(d.x * d.y);
+              d = fmul2(make_float2(d.y, d.x), make_float2(r, r));
+            } else {
+              d.x = fast_rcp(d.x);
+              d.y = fast_rcp(d.y);
+            }
             const float2 x = ffma2(d, m2k, kout2);
             sr[i] = __float_as_uint(x.x);
             sr[i + 1] = __float_as_uint(x.y);

@@ -175,20 +175,31 @@ def test_another_stream_and_equal_bits():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
-def test_equals_the_paged_prefill():
-    """The same rows in pages give the same bits: only the loads differ."""
-    q, k, v = tensors([257, 64], [257, 64], 8, 2, BF, seed=9)
-    o, lse = runner.prefill_ragged(q, k, v, [0, 257, 321])
-    P, pages = 16, [17, 4]
-    kv = torch.zeros(21, 2, 2, P, 128, dtype=BF, device="cuda")
-    for b, (r0, n) in enumerate(((0, 257), (257, 64))):
+@pytest.mark.parametrize("lens", [(257, 64), (120, 128)])
+def test_equals_the_paged_prefill(lens):
+    """The same rows in pages: within the error of both, and the same bits where neither plan cuts a tile's keys
+    (only the loads differ then; over packed rows tiles are cut more rarely)."""
+    n0, total = lens[0], sum(lens)
+    q, k, v = tensors(lens, lens, 8, 2, BF, seed=9)
+    rag = runner.make_ragged_plan(q, k, [0, n0, total])
+    o, lse = runner.prefill_ragged(q, k, v, plan=rag)
+    P, pages = 16, [-(-n // 16) for n in lens]
+    kv = torch.zeros(sum(pages), 2, 2, P, 128, dtype=BF, device="cuda")
+    for p0, r0, n in ((0, 0, n0), (pages[0], n0, lens[1])):
         i = torch.arange(n, device="cuda")
-        kv[17 * b + i // P, 0, :, i % P], kv[17 * b + i // P, 1, :, i % P] = k[r0:r0 + n], v[r0:r0 + n]
+        kv[p0 + i // P, 0, :, i % P], kv[p0 + i // P, 1, :, i % P] = k[r0:r0 + n], v[r0:r0 + n]
     plan = api.Plan(api.PLAN_PREFILL, num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=P, dtype=BF,
-                    sm_scale=128 ** -0.5, causal=True, max_batch=2, max_total_q=321, max_kv_pages=21)
+                    sm_scale=128 ** -0.5, causal=True, max_batch=2, max_total_q=total, max_kv_pages=sum(pages))
     ints = lambda *x: torch.tensor(x, dtype=torch.int32)
-    plan.plan(ints(0, 17, 21), ints(1, 16), 21, qo_indptr_h=ints(0, 257, 321))
+    indptr_h, last_h = ints(0, pages[0], sum(pages)), ints(*(n - (p - 1) * P for n, p in zip(lens, pages)))
+    plan.plan(indptr_h, last_h, sum(pages), qo_indptr_h=ints(0, n0, total))
     o2, lse2 = torch.empty_like(o), torch.empty_like(lse)
-    plan.run(q, kv, torch.arange(21, dtype=torch.int32, device="cuda"), ints(0, 17, 21).cuda(), ints(1, 16).cuda(), o2, lse2,
-             qo_indptr=ints(0, 257, 321).cuda())
-    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    plan.run(q, kv, torch.arange(sum(pages), dtype=torch.int32, device="cuda"), indptr_h.cuda(), last_h.cuda(), o2, lse2,
+             qo_indptr=ints(0, n0, total).cuda())
+    ref = plain(q, k, v, lens, lens, True)
+    check(o, lse, ref, BF)
+    check(o2, lse2, ref, BF)
+    if plan.info().num_merge == rag.info().num_merge == 0:
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    else:
+        assert lens != (120, 128)
