@@ -277,7 +277,10 @@ def test_prompt_to_bounded_decode(kv8):
     else:
         runner.append_kv(db, k_new, v_new, rotate_q=False)
         o2, lse2 = runner.prefill(db)
-        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+        # The two plans cut tiles differently.  Each output is off by at most half a step of itself and, of the
+        # largest value, half a step of its probabilities and 4e-4 (their logits); so they differ by twice that.
+        off = 2 * (2.0 ** -8 * (o2.double().abs() * 1.01) + (2.0 ** -8 + 4e-4) * v_new.double().abs().max())
+        assert bool(((o.double() - o2.double()).abs() <= off).all()) and bool(((lse - lse2).abs() <= 8e-4).all())
     err = ints([0])
     weights = torch.full((b.num_pages, 2, 16), float("nan"), device="cuda")
     # the last 20 rows of each prompt weigh its keys
