@@ -566,7 +566,7 @@ bool sm_count(int& sms) {
   return false;
 }
 
-// Sizes that both calls share; PKV_OK with `none` set where there is nothing to do.
+// Sizes that both calls share.
 pkv_status check_table(int batch, int hkv, int page_size, int64_t num_pages, int64_t kv_pages, int max_keep) {
   if (batch < 0 || hkv <= 0 || num_pages < 0 || kv_pages < 0 || max_keep < 0) return PKV_ERR_INVALID_ARG;
   if (page_size <= 0 || (page_size > 16 && page_size % 16)) return PKV_ERR_UNSUPPORTED;

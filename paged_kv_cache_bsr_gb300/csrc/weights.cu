@@ -24,13 +24,14 @@
 //    exponentials over the columns in registers.  Four CTAs share an SM, so that one's
 //    start and waits are another's products.  Many columns before few keys are shared by
 //    the CTAs of a cluster, which add their sums in rank order through distributed shared
-//    memory.  Bound by the instructions around the exponentials (2.5 issue slots for each,
-//    5.5 with a cap).  Measured: 10 prompts of 128 to 1500 rows, 8 kv heads, group 4, 74 us;
-//    the last 32 to 64 rows of 7 prompts of 2000 to 9000 keys, group 2, capped, 38.4 us.
+//    memory.  Bound by the exponentials and the instructions around them (3 issue slots
+//    for each, 6.5 with a cap).  Measured: 10 prompts of 128 to 1500 rows, 8 kv heads, group 4, 65 us;
+//    the last 32 to 64 rows of 7 prompts of 2000 to 9000 keys, group 2, capped, 40.5 us.
 // Both find their work from the device's row pointers alone: request b's tiles start at
 //     first(b) = floor(kv_indptr[b] P / K) + b        (K keys a tile),
 // which leaves each request room for its ceil(len / K) tiles and at most one unused
 // place, so no scan over the batch is needed and a captured graph follows the arrays.
+// (Prompts take the same places in another order: all first tiles, then all second ones.)
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -61,10 +62,28 @@ struct WeightArgs {
   int batch, hq, hkv, page_size;
   int lg;                    // log2 of the group
   int causal;
-  float scale;               // sm_scale (log2(e) sm_scale without a cap)
+  float scale;               // log2(e) sm_scale
+  float scale_lo;            // tile kernel: what `scale` lacks, relative to it
   float cap, decay;
   uint32_t small_div;        // page_size < 16: ceil(4096 / page_size)
+  int by_level;              // tile kernel: all requests' first key tiles first
 };
+
+// tanh(u) = u + u t h(t), t = u^2, for |u| <= 1: h of degree 6, a least-maximum fit (5.3e-9 of tanh).  A logit
+// y within the cap is then y + (y t) h(t): its first term is exact up to one rounding of the sum with
+// the lse, the correction is small.  By e^(2u) an error of 2^-23 in the exponential is one of cap 2^-24
+// in every logit (at a cap of 30, 2e-6 of a weight; so 6e-7).
+constexpr float kTanhIn = 1.f;
+__device__ __forceinline__ constexpr float tanh_term(int i) {
+  return i == 0 ? -0.33333296f : i == 1 ? 0.13332345f : i == 2 ? -0.0538798f : i == 3 ? 0.021486657f
+       : i == 4 ? -0.0079461057f : i == 5 ? 0.002301364f : -0.00035845183f;
+}
+__device__ __forceinline__ float tanh_correction(float t) {  // t h(t)
+  float h = tanh_term(6);
+#pragma unroll
+  for (int i = 5; i >= 0; --i) h = fmaf(h, t, tanh_term(i));
+  return t * h;
+}
 
 __device__ __forceinline__ void flag(const WeightArgs& a, int bits) {
   if (a.err) atomicOr(a.err, bits);
@@ -207,7 +226,7 @@ __global__ void __launch_bounds__(StreamShape<D, KV8>::kWarps * 32, 1) key_weigh
   const int P = a.page_size;
   const bool whole = P % 16 == 0;  // 16 keys lie in one page
   const bool cap = a.cap > 0.f;
-  const float cap_in = cap ? a.scale * 2.f * kLog2e / a.cap : 0.f, cap_out = a.cap * kLog2e;
+  const float cap_out = a.cap * kLog2e, cap_in = cap ? a.scale / cap_out : 0.f;
   const uint32_t vdist = static_cast<uint32_t>(a.hkv) * P;  // rows from a K row to its V row
   const uint8_t* kv = static_cast<const uint8_t*>(a.kv);
   const uint64_t policy = l2_policy_evict_first();
@@ -436,7 +455,12 @@ __global__ void __launch_bounds__(StreamShape<D, KV8>::kWarps * 32, 1) key_weigh
             const int c = k & 1, r = k >> 1, j = tile * K + 16 * n + g + 8 * r;
             float s = sa[k] + sb[k];
             if constexpr (KV8) s *= qs[c] * ksc[n][r];
-            const float y = cap ? fmaf(cap_out, tanh_from_log2(s * cap_in), nl[c]) : fmaf(s, a.scale, nl[c]);
+            float y = fmaf(s, a.scale, nl[c]);
+            if (cap) {
+              const float u = s * cap_in;
+              y = fabsf(u) <= kTanhIn ? fmaf(s * a.scale, tanh_correction(u * u), y)
+                                      : fmaf(cap_out, tanh_from_log2(u * (2.f * kLog2e)), nl[c]);
+            }
             const float p = fast_exp2(y);
             sum[n][r] += j > see[c] ? 0.f : p;
           }
@@ -471,6 +495,7 @@ __global__ void __launch_bounds__(StreamShape<D, KV8>::kWarps * 32, 1) key_weigh
 // ------------------------------------------------------------------------------ tile
 constexpr int kD = prefill_impl::kD;
 constexpr int kTileKeys = 128;
+constexpr int kLevelBatch = 128;              // requests whose key tiles may be taken longest first
 constexpr int kTileCols = 64;                 // (row, head) pairs of one product
 constexpr int kQStages = 3;                   // the last two bring the keys first
 constexpr uint32_t kQHalf = kTileCols * 128;  // 64 of the 128 dims of 64 columns
@@ -520,6 +545,51 @@ __device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// The u-th key tile in the order of their places in their requests (all first tiles, then all
+// second ones, ...): under a causal mask the first tiles have the most columns, so the longest
+// work starts first.  By the whole warp; false past the last tile.
+__device__ __forceinline__ bool tile_by_level(const WeightArgs& a, int64_t u, int lane, int& b, int64_t& tile) {
+  auto tiles_of = [&](int r) -> int {
+    if (r >= a.batch) return 0;
+    const Request q = load_request(a, r);
+    return q.ok ? (q.kv_len + kTileKeys - 1) / kTileKeys : 0;
+  };
+  // Tiles of the first kOwn * 32 requests stay in registers: lane l has requests l, l + 32, ...
+  constexpr int kOwn = kLevelBatch / 32;
+  int mine[kOwn], most = 0;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    mine[k] = k * 32 < a.batch ? tiles_of(k * 32 + lane) : 0;
+    most = max(most, mine[k]);
+  }
+  most = __reduce_max_sync(kFullMask, most);
+  auto below = [&](int level) {  // tiles of levels before `level`
+    int64_t sum = 0;
+#pragma unroll
+    for (int k = 0; k < kOwn; ++k)
+      if (k * 32 < a.batch) sum += static_cast<uint32_t>(__reduce_add_sync(kFullMask, static_cast<uint32_t>(min(mine[k], level))));
+    return sum;
+  };
+  if (u >= below(most)) return false;
+  int lo = 0, hi = most;  // below(lo) <= u < below(hi)
+  while (hi - lo > 1) {
+    const int mid = lo + (hi - lo) / 2;
+    if (below(mid) <= u) lo = mid; else hi = mid;
+  }
+  int left = static_cast<int>(u - below(lo));  // the left-th request that has a tile `lo`
+  tile = lo;
+  b = 0;
+#pragma unroll
+  for (int k = 0; k < kOwn; ++k) {
+    const unsigned at = __ballot_sync(kFullMask, mine[k] > lo);
+    const int c = __popc(at);
+    if (left >= 0 && left < c) b = k * 32 + __fns(at, 0, left + 1);
+    left -= c;
+    if (left < 0) left = INT_MIN / 2;
+  }
+  return true;
+}
+
 // Four e4m3 codes to two pairs of T (exact).
 template <typename T>
 __device__ __forceinline__ void e4m3x4_to(uint32_t w, uint32_t& lo, uint32_t& hi) {
@@ -548,9 +618,16 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
   const int64_t item = blockIdx.x / share;
   const int64_t u = item / a.hkv;
   const int h = static_cast<int>(item - u * a.hkv);
-  const int b = find_request<kTileKeys>(a, u, lane);
+  int b = 0;
+  int64_t tile = 0;
+  if (a.by_level) {
+    if (blockIdx.x == 0 && tid < a.batch && !load_request(a, tid).ok) flag(a, kErrAppendLayout);
+    if (!tile_by_level(a, u, lane, b, tile)) return;  // the same for all CTAs of a cluster
+  } else {
+    b = find_request<kTileKeys>(a, u, lane);
+    tile = u - first_tile<kTileKeys>(a, b);
+  }
   const Request rq = load_request(a, b);
-  const int64_t tile = u - first_tile<kTileKeys>(a, b);
   if (!rq.ok || tile < 0 || tile * kTileKeys >= rq.kv_len) {  // the same for all CTAs of a cluster
     if (!rq.ok && tid == 0) flag(a, kErrAppendLayout);
     return;
@@ -733,8 +810,13 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
       }
       return v;
     };
-    float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+    float2 all = make_float2(0.f, 0.f);  // of the halves' sums, so that an error grows with the root of their number
     float next_nl = load_nl(0);
+    float u_in = 0.f, k_out = 0.f;  // the cap's argument is u_in times the product
+    if constexpr (CAP) {
+      k_out = a.cap * kLog2e;
+      u_in = mul / k_out;
+    }
     bool ok = true;
     for (int i = 0; i < n; ++i) {  // every warp meets the barrier n times, come what may
       float* nl = sh.nl[i & 1];
@@ -749,12 +831,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
       // The first column whose row sees this key.
       const int c_min = a.causal ? max(j - off - q_row, 0) << a.lg : 0;
       const bool masked = some_out || (a.causal && k0 + kTileKeys - 1 - off > q_row);
-      const float2 mul2 = make_float2(mul, mul);
-      float k_in = 0.f, k_out = 0.f;
-      if constexpr (CAP) {
-        k_in = mul * 2.f * kLog2e / a.cap;
-        k_out = a.cap * kLog2e;
-      }
+      const float2 mul2 = make_float2(mul, mul), mul_lo2 = make_float2(mul * a.scale_lo, mul * a.scale_lo);
 #pragma unroll(CAP ? 1 : 2)
       for (int half = 0; half < 2; ++half) {
         uint32_t sr[32];
@@ -765,8 +842,10 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
           mbar_arrive(bar(sh.s_empty));
         }
         if (!any) break;
-        auto add = [&](auto masked_c) {
-          constexpr bool kMasked = decltype(masked_c)::value;
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        // CAP: kSmall, every argument of the warp's 32 columns is within [-1, 1].
+        auto add = [&](auto masked_c, auto small_c) {
+          constexpr bool kMasked = decltype(masked_c)::value, kSmall = decltype(small_c)::value;
           const int c_from = c_min - half * 32;
 #pragma unroll
           for (int c = 0; c < 32; c += 4) {
@@ -779,11 +858,19 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
               const bool out0 = kMasked && (c + 2 * e < c_from || l.x == -INFINITY);
               const bool out1 = kMasked && (c + 2 * e + 1 < c_from || l.y == -INFINITY);
               float2 y;
-              if constexpr (CAP) {
-                // cap tanh(y) = k_out - 2 k_out / (e^(2y) + 1), e^(2y) = 2^(s k_in), with one
-                // reciprocal for both: 1 / a = b (1 / ab).  2^60 is infinity here, so that ab
-                // stays finite; NaN stays NaN, and one that does not count is kept from the other.
-                float2 z = fmul2(s, make_float2(k_in, k_in));
+              if constexpr (CAP && kSmall) {
+                auto two = [](float x) { return make_float2(x, x); };
+                float2 t = fmul2(s, two(u_in));
+                t = fmul2(t, t);
+                float2 f = two(tanh_term(6));
+#pragma unroll
+                for (int i = 5; i >= 0; --i) f = ffma2(f, t, two(tanh_term(i)));
+                y = ffma2(fmul2(s, mul2), ffma2(f, t, two(a.scale_lo)), ffma2(s, mul2, l));
+              } else if constexpr (CAP) {
+                // cap tanh(u) = k_out - 2 k_out / (e^(2u) + 1), with one reciprocal for both:
+                // 1 / a = b (1 / ab).  2^60 is infinity here, so that ab stays finite; NaN stays
+                // NaN, and one that does not count is kept from the other.
+                float2 z = fmul2(s, make_float2(u_in * (2.f * kLog2e), u_in * (2.f * kLog2e)));
                 z.x = out0 ? 0.f : min_nan(z.x, 60.f);
                 z.y = out1 ? 0.f : min_nan(z.y, 60.f);
                 z = fadd2(make_float2(fast_exp2(z.x), fast_exp2(z.y)), make_float2(1.f, 1.f));
@@ -791,21 +878,30 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
                 z = fmul2(make_float2(z.y, z.x), make_float2(r, r));
                 y = fadd2(ffma2(z, make_float2(-2.f * k_out, -2.f * k_out), make_float2(k_out, k_out)), l);
               } else {
-                y = ffma2(s, mul2, l);
+                y = ffma2(s, mul_lo2, ffma2(s, mul2, l));
               }
               const float p0 = fast_exp2(y.x), p1 = fast_exp2(y.y);
               acc[e] = fadd2(acc[e], make_float2(out0 ? 0.f : p0, out1 ? 0.f : p1));
             }
           }
         };
-        if (masked)
-          add(std::true_type{});
+        bool small = true;
+        if constexpr (CAP) {
+          float most = 0.f;  // (NaN gives NaN by either formula)
+#pragma unroll
+          for (int c = 0; c < 32; ++c) most = fmaxf(most, fabsf(__uint_as_float(sr[c])));
+          small = __all_sync(kFullMask, most * u_in <= kTanhIn);
+        }
+        if (!small)
+          add(std::true_type{}, std::false_type{});
+        else if (masked)
+          add(std::true_type{}, std::true_type{});
         else
-          add(std::false_type{});
+          add(std::false_type{}, std::true_type{});
+        all = fadd2(all, fadd2(acc[0], acc[1]));
       }
     }
-    const float2 s2 = fadd2(acc[0], acc[1]);
-    total = s2.x + s2.y;
+    total = all.x + all.y;
     sh.sum[tid] = total;
   }
   tc_fence_before();
@@ -928,7 +1024,13 @@ extern "C" pkv_status pkv_add_key_weights(const pkv_params* p, int batch, int64_
   a.page_size = p->page_size;
   a.lg = g == 1 ? 0 : g == 2 ? 1 : g == 4 ? 2 : 3;
   a.causal = p->causal != 0 && qo_indptr_d;
-  a.scale = cap ? p->sm_scale : p->sm_scale * kLog2e;
+  // The tensor core cuts its partial sums off: of 400000 products over 128 dims, those within one standard
+  // deviation of 0 were 0.7e-7 of themselves nearer to 0 than the exact ones, those past three 1.4e-7, in a
+  // large logit (20) 2e-6 of its weight.  The tile kernel adds 1e-7, and what the rounding of the scale
+  // took, by a second product (3 us of those prompts' 65, an error of 6e-7 of the weights to 1.3e-7).
+  const double scale = static_cast<double>(p->sm_scale) * 1.4426950408889634;
+  a.scale = static_cast<float>(scale);
+  a.scale_lo = static_cast<float>(scale / a.scale * (1 + 1e-7) - 1);
   a.cap = cap ? p->logits_cap : 0.f;
   a.decay = decay;
   a.small_div = p->page_size < 16 ? (4096 + p->page_size - 1) / p->page_size : 0;
@@ -940,9 +1042,14 @@ extern "C" pkv_status pkv_add_key_weights(const pkv_params* p, int batch, int64_
     // Causal prompts' key tiles differ in their columns, up to all of a request's for the first
     // one: clusters share the columns of a tile until there are six CTAs an SM, as long as each
     // has eight column tiles of a request of average length.  (Prompts of 128 to 1500 rows, 8 kv
-    // heads: alone 94 us, two CTAs a tile 74 us, four 73 us.)
+    // heads, before the second product below: alone 92 us, two CTAs a tile 62 us, four 75 us.)
     int share = 1;
     while (share < 8 && items * share < 6 * sms && total_q * g >= int64_t{16 * kTileCols} * batch * share) share *= 2;
+    // A causal call whose rows are most of its keys: a request's first key tile has columns of
+    // all its rows, its last one of 128 rows.  The longest start first then, or the last CTAs
+    // run alone (12 us of those prompts' 74).  Where keys are many
+    // times the rows all tiles are alike, and the longer search only costs.
+    a.by_level = a.causal && batch <= kLevelBatch && tokens <= 4 * total_q;
     CUtensorMap tq;
     cudaError_t e = prefill_impl::make_rows_map(q, p->dtype, a.hq, total_q, static_cast<int64_t>(a.hq) * kD, g, kTileCols / g, tq);
     if (e == cudaSuccess)

@@ -211,3 +211,37 @@ def test_pool_past_4_gib():
     w = torch.zeros(pool, hkv, P, device="cuda")
     api.add_key_weights(params(x), x.indptr, to.to(torch.int32), x.last, x.q, lse, big, w)
     assert torch.equal(w[to], a[x.indices.long()]) and not w[:pool - x.indices.numel()].any()
+
+
+@pytest.mark.parametrize("batch", [1, 31, 40, 128, 129, 200])
+@pytest.mark.parametrize("bad", [False, True])
+def test_many_prompts_of_very_different_lengths(batch, bad):
+    """Key tiles in the order of their places up to 128 requests, in request order beyond; a request with bad
+    arrays is left out and flagged, the others are as they were."""
+    lens = [(37 * i * i + 5) % 700 if i % 7 else 0 for i in range(1, batch + 1)]
+    x = Paged(lens, 16, 2, qo_lens=lens, group=4, seed=batch)
+    got, _ = check(x, causal=True)
+    if bad:
+        b = max(range(batch), key=lambda i: lens[i])
+        lse = x.lse(x.d ** -0.5, 0.0, True)
+        before = torch.zeros_like(got)
+        good, err = run(x, lse, before, causal=True)
+        assert err == 0
+        x.last[b] = 17
+        w, err = run(x, lse, before, causal=True)
+        page, _ = x.places(b, torch.arange(lens[b], device="cuda"))
+        good[page] = 0
+        assert err == 16 and torch.equal(w, good)
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+def test_no_rows_only_decay(kv8):
+    """A call without a row, as a captured step with nothing new has: the weights decay, new keys start at 0."""
+    x = Paged([40, 17], 16, 2, kv8=kv8, qo_lens=[0, 0], group=4, seed=3)
+    before = torch.rand(x.pool, 2, 16, device="cuda")
+    lse = torch.empty(0, 8, device="cuda")
+    got, err = run(x, lse, before, causal=True, decay=0.5, weighed=[30, 17])
+    want = torch.where(x.held[:, None, :], before * 0.5, before)
+    page, slot = x.places(0, torch.arange(30, 40, device="cuda"))
+    want[page, :, slot] = 0
+    assert err == 0 and torch.equal(got, want)
