@@ -348,6 +348,18 @@ __device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]
       : "memory");
 }
 // 128 consecutive fp32 columns of this thread's TMEM lane: four loads, one wait.
+__device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]) {
+  asm volatile(
+      "{\n\t.reg .b32 a1;\n\tadd.u32 a1, %64, 32;\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+      "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%64];\n\t"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, "
+      "%45, %46, %47, %48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, [a1];\n\t"
+      "tcgen05.wait::ld.sync.aligned;\n\t}"
+      : PKV_R32(r), PKV_R32((r + 32))
+      : "r"(taddr)
+      : "memory");
+}
 __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, uint32_t (&r)[128]) {
   asm volatile(
       "{\n\t.reg .b32 a1, a2, a3;\n\t"
@@ -367,6 +379,15 @@ __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, uint32_t (&r)[12
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// True in one lane of a converged warp.  A branch on it tells the compiler that a single thread is
+// inside: in a branch on the lane number every tcgen05.mma is issued with a check that its operands
+// are alike across the lanes, 125 cycles a product where 64 would do.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+  return one != 0;
+}
 
 // Shared-memory matrix descriptor of a 128B-swizzled operand tile whose
 // 1024-byte swizzle atoms (8 rows of 128 bytes) start at `addr`.

@@ -38,7 +38,13 @@
 //               (tile A only when the work tile's positions fit in it).
 //               S, P and O stay in tensor memory: S_A, S_B, O_A, O_B take the
 //               512 columns, and each P (bf16/fp16) overwrites the first 64
-//               columns of its S, the A operand of its P V MMA.
+//               columns of its S, the A operand of its P V MMA.  RAGGED instances
+//               take keys 64 at a time, each tile's S in two buffers of 64
+//               columns: S of half block i + 2 is issued right after the P V of
+//               half block i, so a softmax warp finds its next S ready.  (A product
+//               of 64 columns costs 54 cycles against 64 for 128, so the tensor
+//               cores do 1.4 times the work, and the chain of S, softmax and P V is
+//               gone: prompts of 128 to 1500 rows 70.9 -> 68.6 us, capped 115 -> 99 us.)
 //   warps 2-5   softmax of tile A, warps 6-9 of tile B (two warps per
 //               scheduler, so one group's softmax overlaps the other group's
 //               MMAs): thread = query row = TMEM lane.  Each reads its S row,
@@ -94,7 +100,10 @@ static_assert(kSmemBytesSmall <= 232448, "shared memory budget");
 enum { Q_FULL = 0, Q_EMPTY = 1, K_FULL = 2, K_EMPTY = K_FULL + kKStages, V_FULL = K_EMPTY + kKStages,
        V_EMPTY = V_FULL + kVStages, S_FULL = V_EMPTY + kVStages, P_FULL = S_FULL + 2, O_DONE = P_FULL + 2,
        O_FREE = O_DONE + 2, V_LOAD = O_FREE + 2, DRAIN = V_LOAD + kVStages, NUM_BARS = DRAIN + 1 };
-static_assert(NUM_BARS * 8 + 8 <= 256, "barrier area");
+// RAGGED instances only: the second barrier of S and of P (odd half blocks), and each P V's end.
+enum { S_ODD = NUM_BARS, P_ODD = S_ODD + 2, PV_DONE = P_ODD + 2, NUM_BARS_RAGGED = PV_DONE + 4 };
+static_assert(NUM_BARS_RAGGED * 8 + 16 <= 256, "barrier area");
+constexpr int kHB = kBN / 2;             // keys of a half block
 constexpr uint32_t kGroupThreads = 128;  // softmax threads of one tile
 constexpr uint32_t kTmemCols = 512;      // S_A, S_B, O_A, O_B
 constexpr uint32_t kColS = 0, kColO = 256;
@@ -166,15 +175,21 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
     return;
   }
   uint64_t* bars = reinterpret_cast<uint64_t*>(sm + kOffBar);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + NUM_BARS);
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + NUM_BARS + 1);
+  constexpr int kBars = RAGGED ? NUM_BARS_RAGGED : NUM_BARS;
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(bars + kBars);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + kBars + 1);
   auto bar = [&](int i) { return base + kOffBar + 8u * i; };
+  // RAGGED: the barriers of tile x's half block g (counted over the CTA's tiles).
+  auto s_bar = [&](int x, int g) { return bar((g & 1 ? S_ODD : S_FULL) + x); };
+  auto p_bar = [&](int x, int g) { return bar((g & 1 ? P_ODD : P_FULL) + x); };
+  auto pv_bar = [&](int x, int g) { return bar(PV_DONE + 2 * x + (g & 1)); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   constexpr bool small = SMALL;  // cp.async gather: every producer lane arrives on the FULL barriers
   if (threadIdx.x == 0) {
-    for (int i = 0; i < NUM_BARS; ++i) {
+    for (int i = 0; i < kBars; ++i) {
       uint32_t count = 1;
+      if (RAGGED && (i == P_ODD || i == P_ODD + 1)) count = kGroupThreads;
       if (i == P_FULL || i == P_FULL + 1 || i == O_FREE || i == O_FREE + 1) count = kGroupThreads;
       if (small && ((i >= K_FULL && i < K_FULL + kKStages) || (i >= V_FULL && i < V_FULL + kVStages))) count = 32;
       mbar_init(bar(i), count);
@@ -412,7 +427,7 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t id_s = umma_idesc_f16(kFmt, kTM, kBN, 0);
       const uint32_t id_o = umma_idesc_f16(kFmt, kTM, kD, 1);
       int kvc = 0;
@@ -456,6 +471,34 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
         for (int kk = 1; kk < kBN / 16; ++kk) umma_ts_lo<true>(d, p + kk * 8, b0 + kk * (2048 >> 4), hi, id_o);
         if (last) umma_commit(bar(O_DONE + x));
       };
+      // The same for half blocks: half block g of tile x has the 64 columns g % 2 of its S.
+      constexpr uint32_t kHalfRows16 = (kHB * 128) >> 4;
+      const uint32_t id_sh = umma_idesc_f16(kFmt, kTM, kHB, 0);
+      auto mma_s_half = [&](int x, int g, int c, int half) {
+        const uint32_t a0 = q_lo + x * kTile16;
+        const uint32_t b0 = k_lo + (c % kKStages) * kTile16 + half * kHalfRows16;
+        const uint32_t d = tmem + kColS + x * kTM + (g & 1) * kHB;
+        umma_ss_lo<false>(d, a0, b0, hi, id_sh);
+#pragma unroll
+        for (int kk = 1; kk < kD / 16; ++kk) {
+          const uint32_t koff = (kk / 4) * kHalf16 + (kk % 4) * 2;
+          umma_ss_lo<true>(d, a0 + koff, b0 + koff, hi, id_sh);
+        }
+        umma_commit(s_bar(x, g));
+      };
+      auto mma_pv_half = [&](int x, int g, int c, int half, bool acc, bool last) {
+        const uint32_t b0 = v_lo + (c % kVStages) * kTile16 + half * kHalfRows16;
+        const uint32_t d = tmem + kColO + x * kTM, p = tmem + kColS + x * kTM + (g & 1) * kHB;
+        if (acc)
+          umma_ts_lo<true>(d, p, b0, hi, id_o);
+        else
+          umma_ts_lo<false>(d, p, b0, hi, id_o);
+#pragma unroll
+        for (int kk = 1; kk < kHB / 16; ++kk) umma_ts_lo<true>(d, p + kk * 8, b0 + kk * (2048 >> 4), hi, id_o);
+        umma_commit(pv_bar(x, g));
+        if (last) umma_commit(bar(O_DONE + x));
+      };
+      int hc[2] = {0, 0};  // half blocks of each UMMA tile so far
       for (int ti = t_begin, tn = 0; ti < t_end && ok; ++ti, ++tn) {
         const PrefillTile t = a.tiles[ti];
         const int n = ceil_div_i(t.kv_end - t.kv_begin, kBN);
@@ -470,6 +513,45 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
         }
         if (!(ok = wait(bar(K_FULL + kvc % kKStages), (kvc / kKStages) & 1))) break;
         tc_fence_after();
+        if constexpr (RAGGED) {
+          // Two S of each tile are on their way before the first P: the next S never
+          // waits for a P V, and a softmax warp finds its S ready.
+          const int nh = ceil_div_i(t.kv_end - t.kv_begin, kHB);
+          for (int i = 0; i < 2 && i < nh; ++i)
+            for (int x = 0; x < nx; ++x) mma_s_half(x, hc[x] + i, kvc, i);
+          umma_commit(bar(K_EMPTY + kvc % kKStages));
+          if (nh <= 2) umma_commit(bar(Q_EMPTY));
+          for (int i = 0; i < nh && ok; ++i) {
+            const int c = kvc + i / 2, half = i & 1;
+            for (int x = 0; x < nx && ok; ++x) {
+              const int g = hc[x] + i;
+              if (!(ok = wait(p_bar(x, g), (g >> 1) & 1))) break;
+              if (i == 0 && o_used[x]) {  // the previous tile's epilogue has read O_x
+                if (!(ok = wait(bar(O_FREE + x), ofree[x] & 1))) break;
+                ++ofree[x];
+              }
+              if (x == 0 && half == 0 && !(ok = wait(bar(V_FULL + c % kVStages), (c / kVStages) & 1))) break;
+              tc_fence_after();
+              mma_pv_half(x, g, c, half, i > 0, i == nh - 1);
+              o_used[x] = true;
+              if (x == nx - 1 && (half == 1 || i == nh - 1)) umma_commit(bar(V_EMPTY + c % kVStages));
+              if (i + 2 < nh) {
+                if (x == 0 && half == 0) {
+                  if (!(ok = wait(bar(K_FULL + (c + 1) % kKStages), ((c + 1) / kKStages) & 1))) break;
+                  tc_fence_after();
+                }
+                mma_s_half(x, g + 2, c + 1, half);
+                if (x == nx - 1) {
+                  if (half == 1 || i + 2 == nh - 1) umma_commit(bar(K_EMPTY + (c + 1) % kKStages));
+                  if (i + 2 == nh - 1) umma_commit(bar(Q_EMPTY));
+                }
+              }
+            }
+          }
+          for (int x = 0; x < nx; ++x) hc[x] += nh;
+          kvc += n;
+          continue;
+        }
         mma_s(0, kvc);
         if (nx == 2) mma_s(1, kvc);
         umma_commit(bar(K_EMPTY + kvc % kKStages));
@@ -531,7 +613,7 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
     const uint32_t col_s = tmem + lane_off + kColS + x * kTM;
     const uint32_t col_o = tmem + lane_off + kColO + x * kTM;
     const float scale = CAP ? a.sm_scale : a.sm_scale * kLog2e;
-    int sc = 0, odc = 0;
+    int sc = 0, odc = 0, hc = 0;
     bool ok = true;
     for (int ti = t_begin; ti < t_end && ok; ++ti) {
       const PrefillTile t = a.tiles[ti];
@@ -551,7 +633,94 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
       limit = min(limit, t.kv_end);
       lim0 = min(lim0, t.kv_end);
       float m_ref = -INFINITY, l = 0.f;
-      for (int j = 0; j < n; ++j) {
+      if constexpr (RAGGED) {
+        const int nh = ceil_div_i(t.kv_end - t.kv_begin, kHB);
+        for (int i = 0; i < nh; ++i) {
+          const int key0 = t.kv_begin + i * kHB, g = hc + i;
+          const uint32_t col = col_s + (g & 1) * kHB;
+          if (!(ok = __all_sync(kFull, wait(s_bar(x, g), (g >> 1) & 1)))) break;
+          tc_fence_after();
+          const bool full = key0 + kHB <= lim0;
+          uint32_t sr[kHB];
+          tmem_ld64_sync(col, sr);
+          float mul = scale;
+          if constexpr (CAP) {
+            // cap * tanh(y) = k_out - 2 k_out / (e^(2y) + 1), in log2 units, with one reciprocal for
+            // two (half the exponential's rate): 1 / a = b (1 / ab).  2^60 is infinity here, so that
+            // ab stays finite, and keys that the row does not see are kept from the pairs.
+            const float k_in = scale * 2.f * kLog2e / a.cap, k_out = a.cap * kLog2e;
+            const float2 kin2 = make_float2(k_in, k_in), one2 = make_float2(1.f, 1.f);
+            const float2 m2k = make_float2(-2.f * k_out, -2.f * k_out), kout2 = make_float2(k_out, k_out);
+            if (!full) {
+#pragma unroll
+              for (int k = 0; k < kHB; ++k)
+                if (key0 + k >= limit) sr[k] = 0u;
+            }
+#pragma unroll
+            for (int k = 0; k < kHB; k += 2) {
+              float2 e = fmul2(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), kin2);
+              e = make_float2(fast_exp2(min_nan(e.x, 60.f)), fast_exp2(min_nan(e.y, 60.f)));
+              float2 d = fadd2(e, one2);
+              const float r = fast_rcp(d.x * d.y);
+              d = ffma2(fmul2(make_float2(d.y, d.x), make_float2(r, r)), m2k, kout2);
+              sr[k] = __float_as_uint(d.x);
+              sr[k + 1] = __float_as_uint(d.y);
+            }
+            mul = 1.f;
+          }
+          if (!full) {
+#pragma unroll
+            for (int k = 0; k < kHB; ++k)
+              if (key0 + k >= limit) sr[k] = 0xff800000u;  // -inf
+          }
+          float mx4[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mx4[k] = __uint_as_float(sr[k]);
+#pragma unroll
+          for (int k = 4; k < kHB; ++k) mx4[k & 3] = fmaxf(mx4[k & 3], __uint_as_float(sr[k]));
+          const float m_new = fmaxf(m_ref, fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3])) * mul);
+          const bool resc = (m_ref == -INFINITY) ? (m_new != -INFINITY) : (m_new > m_ref + 8.f);
+          float alpha = 1.f;
+          if (resc) {
+            alpha = fast_exp2(m_ref - m_new);
+            m_ref = m_new;
+            l *= alpha;
+          }
+          const float sub = (m_ref == -INFINITY) ? 0.f : m_ref;
+          const float2 mul2 = make_float2(mul, mul), nsub2 = make_float2(-sub, -sub);
+          float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          uint32_t pr[kHB / 2];
+#pragma unroll
+          for (int k = 0; k < kHB; k += 2) {
+            float2 v = ffma2(make_float2(__uint_as_float(sr[k]), __uint_as_float(sr[k + 1])), mul2, nsub2);
+            v.x = fast_exp2(v.x);
+            v.y = fast_exp2(v.y);
+            sum[(k >> 1) & 1] = fadd2(sum[(k >> 1) & 1], v);
+            pr[k >> 1] = pack2<T>(v.x, v.y);
+          }
+          const float2 s2 = fadd2(sum[0], sum[1]);
+          l += s2.x + s2.y;
+          tmem_st32(col, pr);  // P over the first half of this S's columns (already read)
+          if (i >= 1 && __any_sync(kFull, resc)) {
+            // O may still be added to by the P V before this one.
+            if (!(ok = __all_sync(kFull, wait(pv_bar(x, g - 1), ((g - 1) >> 1) & 1)))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < kD / 32; ++c) {
+              uint32_t rr[32];
+              tmem_ld32_sync(col_o + c * 32, rr);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) rr[k] = __float_as_uint(__uint_as_float(rr[k]) * alpha);
+              tmem_st32(col_o + c * 32, rr);
+            }
+          }
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(p_bar(x, g));
+        }
+        hc += nh;
+      }
+      for (int j = 0; j < (RAGGED ? 0 : n); ++j) {  // RAGGED: done, in half blocks
         const int key0 = t.kv_begin + j * kBN;
         // Custom mask: this row's bits for keys key0 .. key0 + 127, read (from L2)
         // before the wait for S so the loads overlap it.
@@ -582,33 +751,14 @@ __device__ __forceinline__ void prefill_cta(const PrefillArgs& a, const CUtensor
           const float k_in = scale * 2.f * kLog2e / a.cap, k_out = a.cap * kLog2e;
           const float2 kin2 = make_float2(k_in, k_in), one2 = make_float2(1.f, 1.f);
           const float2 m2k = make_float2(-2.f * k_out, -2.f * k_out), kout2 = make_float2(k_out, k_out);
-          if constexpr (RAGGED) {
-            // Keys that the row does not see are kept from the pairs below.
-            if (!full) {
-#pragma unroll
-              for (int i = 0; i < kBN; ++i)
-                if (key0 + i >= limit) sr[i] = 0u;
-            }
-          }
 #pragma unroll
           for (int i = 0; i < kBN; i += 2) {
             float2 e = fmul2(make_float2(__uint_as_float(sr[i]), __uint_as_float(sr[i + 1])), kin2);
-            if constexpr (RAGGED) {  // 2^60 is infinity here, so that the product of two stays finite
-              e.x = min_nan(e.x, 60.f);
-              e.y = min_nan(e.y, 60.f);
-            }
             e.x = fast_exp2(e.x);
             e.y = fast_exp2(e.y);
             float2 d = fadd2(e, one2);
-            if constexpr (RAGGED) {
-              // One reciprocal for two (half the exponential's rate): 1 / a = b (1 / ab).  (The
-              // other instances keep their bits.)
-              const float r = fast_rcp(d.x * d.y);
-              d = fmul2(make_float2(d.y, d.x), make_float2(r, r));
-            } else {
-              d.x = fast_rcp(d.x);
-              d.y = fast_rcp(d.y);
-            }
+            d.x = fast_rcp(d.x);
+            d.y = fast_rcp(d.y);
             const float2 x = ffma2(d, m2k, kout2);
             sr[i] = __float_as_uint(x.x);
             sr[i + 1] = __float_as_uint(x.y);

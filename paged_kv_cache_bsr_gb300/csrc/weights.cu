@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
   float* at = nullptr;
   if (warp == 4) {
     // ------------------------------------------------------------ Q producer
-    if (lane == 0) {
+    if (elect_one()) {
       int i = 0;
       for (; i < n; ++i) {
         const int s = i % kQStages;
@@ -707,7 +707,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
     __syncwarp();
   } else if (warp == 5) {
     // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
+    if (elect_one()) {
       const uint32_t idesc = umma_idesc_f16(kFmt, kTileKeys, kTileCols, 0);
       const uint64_t dq = sw128_desc(base, 16, 1024);
       const uint32_t hi = static_cast<uint32_t>(dq >> 32), q_lo = static_cast<uint32_t>(dq);

@@ -177,8 +177,8 @@ def test_another_stream_and_equal_bits():
 
 @pytest.mark.parametrize("lens", [(257, 64), (120, 128)])
 def test_equals_the_paged_prefill(lens):
-    """The same rows in pages: within the error of both, and the same bits where neither plan cuts a tile's keys
-    (only the loads differ then; over packed rows tiles are cut more rarely)."""
+    """The same rows in pages: both within their error of the definition (the packed rows' keys are taken 64 at a
+    time, the pages' 128, so the bits differ)."""
     n0, total = lens[0], sum(lens)
     q, k, v = tensors(lens, lens, 8, 2, BF, seed=9)
     rag = runner.make_ragged_plan(q, k, [0, n0, total])
@@ -199,7 +199,18 @@ def test_equals_the_paged_prefill(lens):
     ref = plain(q, k, v, lens, lens, True)
     check(o, lse, ref, BF)
     check(o2, lse2, ref, BF)
-    if plan.info().num_merge == rag.info().num_merge == 0:
-        assert torch.equal(o, o2) and torch.equal(lse, lse2)
-    else:
-        assert lens != (120, 128)
+
+
+@pytest.mark.parametrize("group,hkv,dtype,cap", [(4, 8, BF, 0.0), (1, 4, FP, 0.0), (8, 2, FP, 50.0)])
+def test_a_maximum_that_grows_with_every_block(group, hkv, dtype, cap):
+    """Logits that grow by 8 every 64 keys, so that every block's rows are summed against a new maximum, over many
+    tiles of odd and even numbers of blocks a CTA.  (Their products' terms sum to less than 30: 128 x 30 x 2^-24 is
+    2.3e-4, which with the cap's 43 x 2^-22 is within the 4e-4 that a logit may be off.)"""
+    lens = [200, 33, 129, 70, 1, 190, 64, 65] * 4
+    q, k, v = tensors(lens, lens, group * hkv, hkv, dtype, seed=group)
+    u = torch.randn(128, generator=torch.Generator("cuda").manual_seed(1), device="cuda").sign()
+    place = torch.cat([torch.arange(n, device="cuda") for n in lens]).view(-1, 1, 1)
+    q = (u + 0.05 * q.float()).to(dtype)
+    k = (u * place / 64 * (8 / 128 ** 0.5) + 0.05 * k.float()).to(dtype)
+    o, lse = runner.prefill_ragged(q, k, v, indptr(lens), logits_cap=cap)
+    check(o, lse, plain(q, k, v, lens, lens, True, cap), dtype)
