@@ -1,8 +1,8 @@
 // prefill_ragged.cu -- the prefill kernel (prefill_kernel.cuh) over keys and values that
 // are not in pages: rows packed request behind request, as a projection leaves them.
 //
-// The attention is the paged kernel's, tile for tile; what differs is where a 128-key
-// block comes from: one TMA box per 64 columns of a tensor map over the packed rows,
+// The attention is the paged kernel's, with keys taken 64 at a time (see there); what
+// differs else is where a 128-key block comes from: one TMA box per 64 columns of a tensor map over the packed rows,
 // whose row stride may be any multiple of 16 bytes, so queries, keys and values may be
 // views of one projection's output and are read in place.  A box is one copy whatever
 // the request's length: 128 rows from its first key on.  Rows past the request's last
