@@ -793,13 +793,14 @@ int64_t prefill_makespan(const std::vector<int64_t>& nb_tiles, int64_t total, in
 // cut tiles the merge's launch (3 us) and their fp32 states' way through memory (256 KB
 // written and read a slot), against 1.83 us a block.  12 heads x 5 requests of 170 to 650
 // rows against 330 to 1480 keys, 132 tiles of up to 12 blocks on 152 CTAs: a call
-// with 108 of them cut 59.7 us, with all whole 48.4 us.
+// with 108 of them cut 59.7 us, with all whole 48.4 us.  Chunks are tried in steps of a
+// third (two of those requests, 60 tiles: chunks of 4 blocks 29.2 us, of 3 or 6 35 us).
 int64_t ragged_chunk(const std::vector<int64_t>& nb_tiles, int64_t total, int C, std::vector<int64_t>& by_cost,
                      std::vector<int64_t>& by_load) {
   const int64_t least = key_chunk(total, C), whole = std::max<int64_t>(static_cast<int64_t>(nb_tiles.size()) - 1, 1);
   int64_t best = least;
   double best_cost = 0.0;
-  for (int64_t chunk = std::min(least, whole);; chunk = std::min(chunk * 2, whole)) {
+  for (int64_t chunk = std::min(least, whole);; chunk = std::min(chunk + (chunk + 2) / 3, whole)) {
     int64_t slots = 0;
     for (int64_t nb = chunk + 1; nb < static_cast<int64_t>(nb_tiles.size()); ++nb) slots += nb_tiles[nb] * ceil_div(nb, chunk);
     const double cost = static_cast<double>(prefill_makespan(nb_tiles, total, C, by_cost, by_load, chunk)) +
