@@ -363,3 +363,71 @@ def test_a_shared_prefix_is_weighed_with_the_merged_lse():
     assert int(err) == 0
     assert (w - total).abs().max() <= 1e-5 * float(total.max())
     assert abs(float(w.double().sum()) - 6 * 8) < 1e-2
+
+
+def small_batch(seed):
+    qo = [120, 77]
+    b = W.make_paged_batch(qo_lens=qo, kv_lens=qo, num_qo_heads=8, num_kv_heads=2, head_dim=128, page_size=16, dtype=BF, seed=seed,
+                           causal=True, pool_pages=20)
+    db = runner.DeviceBatch.from_host(b)
+    db.kv_data = torch.randn(db.kv_data.shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda").to(BF)
+    return db
+
+
+def shorten(db, stream=None):
+    o, lse = runner.prefill(db, stream=stream)
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.stream(torch.cuda.current_stream()):
+        w = runner.zero_key_weights(db.host.num_pages, 2, 16)
+    runner.add_key_weights(db, lse, w, stream=stream)
+    short, freed = runner.evict(db, w, [50, 33], sink=1, window=4, stream=stream)
+    return short, freed, w
+
+
+def test_two_caches_on_two_streams_at_once():
+    """Every step of two batches on streams of their own, beside each other, gives what one after the other gives."""
+    want = []
+    for seed in (1, 2):
+        db = small_batch(seed)
+        short, freed, w = shorten(db)
+        want.append((db.kv_data, w, freed, short.kv_indices))
+    batches, streams = [small_batch(s) for s in (1, 2)], [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for db, s in zip(batches, streams):
+        got.append(shorten(db, s))
+    torch.cuda.synchronize()
+    for db, (short, freed, w), (kv, w0, freed0, ids) in zip(batches, got, want):
+        assert torch.equal(db.kv_data.view(torch.int16), kv.view(torch.int16)) and torch.equal(w, w0)
+        assert torch.equal(freed, freed0) and torch.equal(short.kv_indices, ids) and short.host.kv_lens == [50, 33]
+
+
+def test_a_choice_and_a_move_in_one_graph_follow_the_budgets():
+    """select_keys and compact_paged_kv captured together, replayed with other budgets and weights."""
+    x = Paged([300, 200], 16, 2, seed=11)
+    w = torch.rand(x.pool, 2, 16, device="cuda")
+    budget, kept = ints([100, 50]), ints([0, 0])
+    keep = torch.empty(2, 2, 150, dtype=torch.int32, device="cuda")
+    kv0 = x.kv.clone()
+
+    def call():
+        api.select_keys(x.indptr, x.indices, x.last, w, budget, keep, kept, sink=1, window=3)
+        api.compact_paged_kv(x.indptr, x.indices, x.last, keep, kept, x.kv, weights=w)
+
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for n, seed in (([100, 50], 1), ([150, 1], 2), ([0, 149], 3)):
+        budget.copy_(ints(n))
+        w.copy_(torch.rand(w.shape, generator=torch.Generator("cuda").manual_seed(seed), device="cuda"))
+        x.kv.copy_(kv0)
+        before = w.clone()
+        graph.replay()
+        for b in range(2):
+            page, slot = x.places(b, torch.arange(x.kv_lens[b], device="cuda"))
+            for h in range(2):
+                want = chosen(before[page, h, slot].cpu().numpy(), n[b], 1, 3)
+                assert keep[b, h, :n[b]].tolist() == want and int(kept[b]) == n[b]
+        assert torch.equal(x.kv.view(torch.int16), moved(x, keep, n, kv0.view(torch.int16)))
+        assert torch.equal(w, moved(x, keep, n, before))
