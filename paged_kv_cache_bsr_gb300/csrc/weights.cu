@@ -24,9 +24,10 @@
 //    exponentials over the columns in registers.  Four CTAs share an SM, so that one's
 //    start and waits are another's products.  Many columns before few keys are shared by
 //    the CTAs of a cluster, which add their sums in rank order through distributed shared
-//    memory.  Bound by the exponentials and the instructions around them (3 issue slots
-//    for each, 6.5 with a cap).  Measured: 10 prompts of 128 to 1500 rows, 8 kv heads, group 4, 65 us;
-//    the last 32 to 64 rows of 7 prompts of 2000 to 9000 keys, group 2, capped, 40.5 us.
+//    memory.  Prompts are bound by L2 (each key tile streams its request's queries): 10 of
+//    128 to 1500 rows, 8 kv heads, group 4, 64 us, 456 MB at 7.1 TB/s, where boxes of
+//    128-byte rows come at about 9 on all SMs.  Few columns are bound by a tile's start:
+//    the last 32 to 64 rows of 7 prompts of 2000 to 9000 keys, group 2, capped, 40 us.
 // Both find their work from the device's row pointers alone: request b's tiles start at
 //     first(b) = floor(kv_indptr[b] P / K) + b        (K keys a tile),
 // which leaves each request room for its ceil(len / K) tiles and at most one unused
