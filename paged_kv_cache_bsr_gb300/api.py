@@ -12,6 +12,7 @@ staging buffer it needs (allocated with torch, i.e. by the caller).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional, Tuple
@@ -157,12 +158,14 @@ def _ptr(t: Optional[torch.Tensor]):
 
 # The current stream's handle without a Stream object around it (3 us a call on the host).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# The current device without a check that CUDA was started: where a tensor is on one it was.
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
     if stream is None:
         if _raw_stream is not None and torch.cuda.is_initialized():
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         stream = torch.cuda.current_stream()
     if isinstance(stream, int):
         return ctypes.c_void_p(stream)
@@ -348,7 +351,7 @@ def _ptrs(tensors):
             continue
         at = x.get_device()
         if at != dev:
-            if dev != -2 or at < 0 or at != torch.cuda.current_device():
+            if dev != -2 or at < 0 or at != _device():
                 raise ValueError("tensors must be on the current CUDA device")
             dev = at
         if not x.is_contiguous():
@@ -450,11 +453,12 @@ def _rows(x):
     """(address, elements from row to row) of rows [n, heads, head_dim] whose heads lie dense: a view of a
     projection's output may have wider rows."""
     n, heads, d = x.shape
-    if not x.is_cuda or x.get_device() != torch.cuda.current_device():
+    if not x.is_cuda or x.get_device() != _device():
         raise ValueError("tensors must be on the current CUDA device")
-    if (d > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != d):
+    row, head, one = x.stride()
+    if (d > 1 and one != 1) or (heads > 1 and head != d):
         raise ValueError("the heads of a row must lie one behind another")
-    return x.data_ptr(), x.stride(0) if n > 1 else heads * d
+    return x.data_ptr(), row if n > 1 else heads * d
 
 
 def batch_prefill_ragged(h, q, k, v, o, lse, dev_ws, stream=None) -> None:
@@ -480,21 +484,22 @@ def add_key_weights(params: Params, kv_indptr, kv_indices, kv_last_page_len, q, 
     ``weights`` [num_pages, Hkv, P] float32.  No qo_indptr: one row per request.  ``kv_scales``: kv is the
     8-bit cache.  ``weighed_len`` [batch] int32: later keys' weights are set instead of added to."""
     batch = _table(kv_indptr, kv_indices, kv_last_page_len, qo_indptr, weighed_len, error)
-    rows, dtype = (q.shape[0], params.num_qo_heads), _STORED.get(params.dtype)
-    if q.shape != (*rows, params.head_dim) or q.dtype is not dtype or lse.shape != rows or lse.dtype is not torch.float32:
+    total_q, pool, hkv, page, dim = q.shape[0], kv.shape[0], params.num_kv_heads, params.page_size, params.head_dim
+    rows, dtype = (total_q, params.num_qo_heads), _STORED.get(params.dtype)
+    if q.shape != (*rows, dim) or q.dtype is not dtype or lse.shape != rows or lse.dtype is not torch.float32:
         raise ValueError("q must be [rows, num_qo_heads, head_dim] of the params' dtype, lse [rows, num_qo_heads] float32")
-    if (q.shape[0] != batch) if qo_indptr is None else (qo_indptr.numel() != batch + 1):
+    if (total_q != batch) if qo_indptr is None else (qo_indptr.numel() != batch + 1):
         raise ValueError("q must hold a row per request, or qo_indptr batch + 1 entries")
     if weighed_len is not None and weighed_len.numel() != batch:
         raise ValueError("weighed_len must have an entry per request")
     if kv_scales is not None:
         _kv8_tensors(params, kv, kv_scales)
-    elif kv.shape[1:] != (2, params.num_kv_heads, params.page_size, params.head_dim) or kv.dtype is not dtype:
+    elif kv.shape != (pool, 2, hkv, page, dim) or kv.dtype is not dtype:
         raise ValueError("kv must be [num_pages, 2, num_kv_heads, page_size, head_dim] of the params' dtype")
-    if weights.shape != (kv.shape[0], *kv.shape[2:4]) or weights.dtype is not torch.float32:
+    if weights.shape != (pool, hkv, page) or weights.dtype is not torch.float32:
         raise ValueError("weights must be [num_pages, num_kv_heads, page_size] float32")
     _check((_lib or load()).pkv_add_key_weights(
-        ctypes.byref(params), batch, q.shape[0], kv.shape[0], kv_indices.numel(),
+        ctypes.byref(params), batch, total_q, pool, kv_indices.numel(),
         *_ptrs((qo_indptr, kv_indptr, kv_indices, kv_last_page_len, weighed_len, q, kv, kv_scales, lse, weights)),
         decay, *_ptrs((error,)), _stream(stream)), "pkv_add_key_weights")
 
@@ -515,6 +520,12 @@ def select_keys(kv_indptr, kv_indices, kv_last_page_len, weights, budget, keep, 
         sink, window, keep.shape[2], *_ptrs((keep, kept_len, error)), _stream(stream)), "pkv_select_keys")
 
 
+@functools.lru_cache(maxsize=64)
+def _cache_params(hkv: int, dim: int, page: int) -> Params:
+    """A cache's sizes for the call that moves its rows (2 us of host time to make)."""
+    return Params(hkv, hkv, dim, page, PKV_F16, 1.0, 0.0, 0)
+
+
 def compact_paged_kv(kv_indptr, kv_indices, kv_last_page_len, keep, kept_len, kv, kv_scales=None, weights=None,
                      dst_indptr=None, dst_indices=None, error=None, stream=None) -> None:
     """Move the kept keys (``select_keys``) of the 16-bit cache ``kv``, or of the 8-bit one with its
@@ -525,7 +536,7 @@ def compact_paged_kv(kv_indptr, kv_indices, kv_last_page_len, keep, kept_len, kv
     pool, _, hkv, page, dim = kv.shape
     if kv_scales is None and kv.dtype not in (torch.float16, torch.bfloat16):
         raise ValueError("kv must be float16 or bfloat16, or come with its kv_scales")
-    params = Params(hkv, hkv, dim, page, PKV_F16, 1.0, 0.0, 0)
+    params = _cache_params(hkv, dim, page)
     if kv_scales is not None:
         _kv8_tensors(params, kv, kv_scales)
     if weights is not None and (weights.shape != (pool, hkv, page) or weights.dtype is not torch.float32):
