@@ -65,28 +65,8 @@ __device__ __forceinline__ bool keys_of(const Table& t, int b, int& page0, int& 
   return true;
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
-  uint32_t v;
-  asm volatile(
-      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
-      : "=r"(v)
-      : "r"(smem_addr(p)), "r"(rank)
-      : "memory");
-  return v;
-}
-
 // ---------------------------------------------------------------------------- select
 constexpr int kMaxHeld = 48 * 1024;  // weights in shared memory
-
 
 struct SelectArgs {
   Table t;

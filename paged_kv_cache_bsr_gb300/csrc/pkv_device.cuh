@@ -389,6 +389,27 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// All threads of a cluster's CTAs meet; what one wrote to its shared memory before, the others see.
+__device__ __forceinline__ void cluster_sync_all() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+// The word at p in the shared memory of the cluster's CTA `rank`.
+__device__ __forceinline__ uint32_t ld_cluster_u32(const void* p, uint32_t rank) {
+  uint32_t v;
+  asm volatile(
+      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.u32 %0, [r];\n\t}"
+      : "=r"(v)
+      : "r"(smem_addr(p)), "r"(rank)
+      : "memory");
+  return v;
+}
+
 // Shared-memory matrix descriptor of a 128B-swizzled operand tile whose
 // 1024-byte swizzle atoms (8 rows of 128 bytes) start at `addr`.
 //  K-major operand: rows are M (or N) at 128 B, 8-row groups `sbo` apart; lbo unused.

@@ -527,25 +527,6 @@ __device__ __forceinline__ bool keys_any(bool x) {
   return r != 0;
 }
 
-__device__ __forceinline__ void cluster_sync_all() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ float ld_cluster_f32(uint32_t addr, uint32_t rank) {
-  float v;
-  asm volatile(
-      "{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %1, %2;\n\tld.shared::cluster.f32 %0, [r];\n\t}"
-      : "=f"(v)
-      : "r"(addr), "r"(rank)
-      : "memory");
-  return v;
-}
-
 // The u-th key tile in the order of their places in their requests (all first tiles, then all
 // second ones, ...): under a causal mask the first tiles have the most columns, so the longest
 // work starts first.  By the whole warp; false past the last tile.
@@ -914,7 +895,7 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
     cluster_sync_all();
     if (at) {  // rank 0's keys
       total = 0.f;
-      for (int k = 0; k < share; ++k) total += ld_cluster_f32(smem_addr(&sh.sum[tid]), k);
+      for (int k = 0; k < share; ++k) total += __uint_as_float(ld_cluster_u32(&sh.sum[tid], k));
     }
     cluster_sync_all();  // a CTA's sums stay until they have been read
   }
