@@ -40,6 +40,7 @@
 #include <algorithm>
 #include <type_traits>
 
+#include "pkv_join.h"
 #include "prefill_kernel.cuh"
 
 namespace pkv {
@@ -890,14 +891,15 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
   __syncthreads();
   tc_fence_after();
   if (warp == 5) tmem_dealloc(tmem, kWTmemCols);
-  if (sh.abort) at = nullptr;  // sums that a wait left incomplete
+  // Where a wait ran out on any of the tile's CTAs its weights stay as they were.
   if (share > 1) {
     cluster_sync_all();
-    if (at) {  // rank 0's keys
-      total = 0.f;
-      for (int k = 0; k < share; ++k) total += __uint_as_float(ld_cluster_u32(&sh.sum[tid], k));
-    }
+    if (at && !join_ranks(share, [&](int k) { return __uint_as_float(ld_cluster_u32(&sh.sum[tid], k)); },
+                          [&](int k) { return ld_cluster_u32(&sh.abort, k) != 0u; }, total))
+      at = nullptr;      // (rank 0's keys)
     cluster_sync_all();  // a CTA's sums stay until they have been read
+  } else if (sh.abort) {
+    at = nullptr;
   }
   if (at) *at = old + total;
 }
