@@ -277,41 +277,60 @@ def add_key_weights(db: DeviceBatch, lse: torch.Tensor, weights: torch.Tensor, c
                         stream=stream)
 
 
+def _pages_listed_once(ids: torch.Tensor, what: str) -> None:
+    if ids.numel() and int(torch.bincount(ids).max()) > 1:
+        raise ValueError(what)
+
+
 def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[int]], sink: int = 0, window: int = 0,
-          cache: Optional[Kv8Cache] = None, error: Optional[torch.Tensor] = None, stream=None
-          ) -> Tuple[DeviceBatch, torch.Tensor]:
-    """Shorten each request's cache to ``budget`` keys (one number, or one a request) in place: for every kv
-    head the last ``window``, the first ``sink`` and the heaviest others.  No page may be listed by two requests.
-    Returns the batch with its shorter page tables, and the ids of the pages it no longer lists (on the host).
+          cache: Optional[Kv8Cache] = None, error: Optional[torch.Tensor] = None, stream=None,
+          pages: Union[None, Sequence[int], torch.Tensor] = None) -> Tuple[DeviceBatch, torch.Tensor]:
+    """Shorten each request's cache to ``budget`` keys (one number, or one a request): for every kv head the last
+    ``window``, the first ``sink`` and the heaviest others.  In place, which needs every page to be listed once (a
+    batch with shared pages is refused, and no other batch may list them), or into ``pages``: ids of free pages of the
+    pool on the host, of which the first ones are filled, for pages that requests share.
+    Returns the batch with its shorter page tables, and the ids of the pages it no longer lists (on the host; with
+    ``pages`` all it listed before, which other batches may still list).
     The key weights move with their keys; nothing is read back from the GPU."""
     b = db.host
     budgets = [int(budget)] * b.batch if isinstance(budget, int) else [int(x) for x in budget]
     if len(budgets) != b.batch or min(budgets, default=0) < 0:
         raise ValueError("budget must be a count of keys, or one for each request")
     kept = [min(n, x) for n, x in zip(b.kv_lens, budgets)]
+    used = [-(-n // b.page_size) for n in kept]
+    indptr = torch.zeros(b.batch + 1, dtype=torch.int32)
+    indptr[1:] = torch.tensor(used, dtype=torch.int32).cumsum(0)
+    first = [int(x) for x in b.kv_indptr]
+    source = b.kv_indices[first[0]:first[-1]]
+    none = source[:0]
+    if pages is None:
+        _pages_listed_once(source, "a page is listed twice: shared pages need others to move their keys to (pages)")
+        indices = torch.cat([none, *(b.kv_indices[s:s + n] for s, n in zip(first, used))])
+        freed = torch.cat([none, *(b.kv_indices[s + n:e] for s, n, e in zip(first, used, first[1:]))])
+    else:
+        given = torch.as_tensor(pages, dtype=torch.int32).cpu()
+        if given.dim() != 1 or given.numel() < int(indptr[-1]):
+            raise ValueError("pages must be a list of %d pages" % int(indptr[-1]))
+        indices, freed = given[:int(indptr[-1])].contiguous(), torch.unique(source)
+        if indices.numel() and not 0 <= int(indices.min()) <= int(indices.max()) < weights.shape[0]:
+            raise ValueError("pages must be pages of the pool")
+        _pages_listed_once(torch.cat([indices, freed]), "pages must be different ones that the batch does not list")
+    host = dataclasses.replace(b, kv_indptr=indptr, kv_indices=indices, kv_lens=kept,
+                               kv_last_page_len=torch.tensor([n - (p - 1) * b.page_size if n else 0 for n, p in zip(kept, used)],
+                                                             dtype=torch.int32))
     with _on(stream):
         host_budget = torch.tensor(budgets, dtype=torch.int32)
         keep = torch.empty(b.batch, b.num_kv_heads, max(kept, default=0), dtype=torch.int32, device=db.q.device)
         kept_len = torch.empty(b.batch, dtype=torch.int32, device=db.q.device)
+        tables = [t.to(db.q.device) for t in (host.kv_indptr, host.kv_indices, host.kv_last_page_len)]
         api.select_keys(db.kv_indptr, db.kv_indices, db.kv_last_page_len, weights, host_budget.to(db.q.device), keep, kept_len,
                         sink=sink, window=window, error=error, stream=stream)
         api.compact_paged_kv(db.kv_indptr, db.kv_indices, db.kv_last_page_len, keep, kept_len,
                              db.kv_data if cache is None else cache.codes, kv_scales=None if cache is None else cache.scales,
-                             weights=weights, error=error, stream=stream)
-        pages = [-(-n // b.page_size) for n in kept]
-        first = [int(x) for x in b.kv_indptr]
-        listed = [b.kv_indices[s:s + n] for s, n in zip(first, pages)]
-        freed = [b.kv_indices[s + n:e] for s, n, e in zip(first, pages, first[1:])]
-        none = b.kv_indices[:0]
-        indptr = torch.zeros(b.batch + 1, dtype=torch.int32)
-        indptr[1:] = torch.tensor(pages, dtype=torch.int32).cumsum(0)
-        host = dataclasses.replace(b, kv_indptr=indptr, kv_indices=torch.cat([none, *listed]), kv_lens=kept,
-                                   kv_last_page_len=torch.tensor([n - (p - 1) * b.page_size if n else 0 for n, p in zip(kept, pages)],
-                                                                 dtype=torch.int32))
-        tables = [t.to(db.q.device) for t in (host.kv_indptr, host.kv_indices, host.kv_last_page_len)]
+                             weights=weights, dst_indptr=None if pages is None else tables[0],
+                             dst_indices=None if pages is None else tables[1], error=error, stream=stream)
     _returned(stream, *tables)
-    return dataclasses.replace(db, host=host, kv_indptr=tables[0], kv_indices=tables[1], kv_last_page_len=tables[2]), \
-        torch.cat([none, *freed])
+    return dataclasses.replace(db, host=host, kv_indptr=tables[0], kv_indices=tables[1], kv_last_page_len=tables[2]), freed
 
 
 def mixed(db: DeviceBatch, plan: Optional[api.Plan] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:

@@ -1,0 +1,38 @@
+"""Which page tables the runner's eviction takes, without a GPU: what it refuses it refuses before any CUDA call."""
+import dataclasses
+
+import pytest
+import torch
+
+from paged_kv_cache_bsr_gb300 import runner, workloads as W
+
+
+def batch(shared=(), **kw):
+    """Two requests of 40 and 30 keys in pages of 16 (3 and 2 of a pool of 9); shared: places of the list that hold
+    the page of place 0."""
+    b = W.make_paged_batch(qo_lens=[1, 1], kv_lens=[40, 30], num_qo_heads=2, num_kv_heads=1, head_dim=64, page_size=16,
+                           dtype=torch.bfloat16, seed=1, pool_pages=9, identity_pages=True)
+    ids = b.kv_indices.clone()
+    for i in shared:
+        ids[i] = ids[0]
+    return type("HostOnly", (), {"host": dataclasses.replace(b, kv_indices=ids)})()
+
+
+WEIGHTS = torch.zeros(9, 1, 16)
+
+
+@pytest.mark.parametrize("shared", [[3], [1], [4, 3]])
+def test_shared_pages_are_not_shortened_in_place(shared):
+    with pytest.raises(ValueError, match="listed twice"):
+        runner.evict(batch(shared), WEIGHTS, 20)
+
+
+@pytest.mark.parametrize("pages,match", [([5, 6, 7], "4 pages"), ([[5, 6], [7, 8]], "4 pages"), ([5, 6, 7, 9], "of the pool"),
+                                         ([-1, 6, 7, 8], "of the pool"), ([5, 6, 7, 7], "different"), ([5, 6, 7, 4], "different"),
+                                         ([0, 6, 7, 8], "different")])
+def test_pages_to_fill_are_free_ones_of_the_pool(pages, match):
+    for shared in ([], [3]):
+        if shared and 4 in pages:
+            continue
+        with pytest.raises(ValueError, match=match):
+            runner.evict(batch(shared), WEIGHTS, 20, pages=pages)
