@@ -260,7 +260,7 @@ def cascade_kv8(prefix: DeviceBatch, suffix: DeviceBatch, cache: Kv8Cache, prefi
 
 
 def zero_key_weights(num_pages: int, num_kv_heads: int, page_size: int, device: str = "cuda") -> torch.Tensor:
-    """Key weights beside a cache of that many pages."""
+    """Key weights beside a cache of that many pages, as long as it holds no key that was weighed."""
     return torch.zeros(num_pages, num_kv_heads, page_size, dtype=torch.float32, device=device)
 
 
@@ -268,7 +268,11 @@ def add_key_weights(db: DeviceBatch, lse: torch.Tensor, weights: torch.Tensor, c
                     decay: float = 1.0, weighed_len: Optional[torch.Tensor] = None, error: Optional[torch.Tensor] = None,
                     stream=None) -> None:
     """Add to ``weights`` the probabilities that the batch's rows gave every key they see; ``lse`` from the
-    attention call (or merged from several) over the same keys.  ``cache``: the keys of the 8-bit cache."""
+    attention call (or merged from several) over the same keys.  ``cache``: the keys of the 8-bit cache.  A page may
+    be listed once.  A key's old weight is what its slot holds: 0 for a new key in a slot of ``zero_key_weights`` that
+    held none, or behind what ``evict`` kept; where a page comes back by another way (a request that ended, a prefix
+    that nothing lists any more), clear its weights, or give ``weighed_len`` [batch] int32, the keys of each request
+    that have weights already."""
     b = db.host
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale, b.logits_cap, b.causal)
     api.add_key_weights(params, db.kv_indptr, db.kv_indices, db.kv_last_page_len, db.q, lse,
@@ -291,7 +295,9 @@ def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[in
     pool on the host, of which the first ones are filled, for pages that requests share.
     Returns the batch with its shorter page tables, and the ids of the pages it no longer lists (on the host; with
     ``pages`` all it listed before, which other batches may still list).
-    The key weights move with their keys; nothing is read back from the GPU."""
+    The key weights move with their keys, and are 0 in the kept pages' slots behind them and, in place, in the pages
+    that are no longer listed, so that a key that comes to lie there starts from 0.  Nothing is read back from the
+    GPU."""
     b = db.host
     budgets = [int(budget)] * b.batch if isinstance(budget, int) else [int(x) for x in budget]
     if len(budgets) != b.batch or min(budgets, default=0) < 0:
@@ -329,6 +335,14 @@ def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[in
                              db.kv_data if cache is None else cache.codes, kv_scales=None if cache is None else cache.scales,
                              weights=weights, dst_indptr=None if pages is None else tables[0],
                              dst_indices=None if pages is None else tables[1], error=error, stream=stream)
+        # Slots that hold no key any more, and the last pages' behind the keys, weigh nothing.
+        ends = [(int(indices[e - 1]), last) for e, n, last in zip(indptr[1:], used, host.kv_last_page_len) if 0 < n and last < b.page_size]
+        if ends:
+            at, last = (torch.tensor(x).to(db.q.device) for x in zip(*ends))
+            behind = torch.arange(b.page_size, device=db.q.device) >= last.unsqueeze(1)
+            weights[at] = weights[at].masked_fill(behind.unsqueeze(1), 0)
+        if pages is None and freed.numel():
+            weights.index_fill_(0, freed.to(db.q.device, torch.int64), 0)
     _returned(stream, *tables)
     return dataclasses.replace(db, host=host, kv_indptr=tables[0], kv_indices=tables[1], kv_last_page_len=tables[2]), freed
 

@@ -93,3 +93,52 @@ def test_shared_pages_are_shortened_into_others(kv8, stream):
             assert torch.equal(new_w[h], old_w[h, keep])
             for t, t0 in zip(raw(db, cache), before):
                 assert torch.equal(rows(t, short.host, r)[:, h], rows(t0, db.host, r)[:, h][:, keep])
+
+
+@pytest.mark.parametrize("kv8", [False, True])
+@pytest.mark.parametrize("elsewhere", [False, True])
+def test_new_keys_do_not_inherit_an_evicted_keys_weight(kv8, elsewhere):
+    """Evict, append a token into a slot or a page that held an evicted key, weigh with the call's defaults: its
+    weight is its own probability (a row's probabilities over a head add up to 1)."""
+    lens, kept, pool = [70, 90, 33], [40, 32, 20], 40
+    db, cache = make(lens, 4, pool, kv8)
+    if not kv8:   # finite scores
+        db.kv_data.copy_(torch.randn(db.kv_data.shape, generator=torch.Generator("cuda").manual_seed(1), device="cuda"))
+    w = torch.rand(pool, HKV, P, device="cuda") * 100
+    free = sorted(set(range(pool)) - set(db.host.kv_indices.tolist()))
+    w[free] = 0
+    if elsewhere:
+        w[free[:3 + 2 + 2]] = 7   # the pages to fill: what their slots hold counts as nothing
+    short, freed = runner.evict(db, w, kept, sink=1, window=4, cache=cache, pages=free if elsewhere else None)
+    old = w.clone()
+    held = torch.zeros(pool, P, dtype=torch.bool)
+    for r, n in enumerate(kept):
+        i = torch.arange(n)
+        held[listed(short.host, r)[i // P], i % P] = True
+    if elsewhere:
+        held[db.host.kv_indices.long()] = True   # as they were
+    assert not w.cpu()[~held.unsqueeze(1).expand(pool, HKV, P)].any()
+    # a token more: the second request's in a page that was freed (or one more free one)
+    spare = free[int(short.host.kv_indptr[-1]):] if elsewhere else freed.tolist()
+    ids = [listed(short.host, r).tolist() for r in range(3)]
+    ids = [x if len(x) * P > n else x + [spare.pop()] for x, n in zip(ids, kept)]
+    one = dataclasses.replace(short.host, kv_lens=[n + 1 for n in kept], kv_indptr=torch.tensor(starts([len(x) for x in ids]), dtype=torch.int32),
+                              kv_indices=torch.tensor(sum(ids, []), dtype=torch.int32),
+                              kv_last_page_len=torch.tensor([n + 1 - (len(x) - 1) * P for x, n in zip(ids, kept)], dtype=torch.int32))
+    grown = dataclasses.replace(short, host=one, kv_indptr=one.kv_indptr.cuda(), kv_indices=one.kv_indices.cuda(),
+                                kv_last_page_len=one.kv_last_page_len.cuda())
+    new = [torch.randn(3, HKV, D, device="cuda").to(BF) for _ in range(2)]
+    if kv8:
+        runner.append_kv8(grown, cache, *new, rotate_q=False)
+        _, lse = runner.decode_kv8(grown, cache)
+    else:
+        runner.append_kv_axes(grown, *new, None, rotate_q=False)
+        _, lse = runner.decode(grown)
+    runner.add_key_weights(grown, lse, w, cache=cache)
+    for r, n in enumerate(kept):
+        page, slot = ids[r][n // P], n % P
+        # From 0 to HQ / HKV: the codes' logits differ by hundreds, and exp(-104) is below half the least fp32, 2^-150.
+        assert float(w[page, :, slot].min()) >= 0 and float(w[page, :, slot].max()) <= HQ // HKV + 1e-3
+        gained = (rows(w.unsqueeze(-1), one, r) - rows(old.unsqueeze(-1), one, r)).double().sum((-2, -1))
+        # A row's probabilities add up to 1: HQ / HKV rows a head, sums of 100 a key rounded in fp32 (n 100 2^-24).
+        assert bool(((gained - HQ // HKV).abs() < 1e-3).all())
