@@ -153,14 +153,22 @@ def cascade(prefix: DeviceBatch, suffix: DeviceBatch, prefix_plan: Optional[api.
     return o_p, l_p
 
 
+def _positions_by_slot(b) -> None:
+    if b.moved:
+        raise ValueError("after an eviction a token's slot is not its position: give its position (append_kv_axes, append_kv8)")
+
+
 def append_kv(db: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor, rope_theta: float = 0.0,
               q_out: Optional[torch.Tensor] = None, rotate_q: bool = True, error: Optional[torch.Tensor] = None,
               stream=None) -> Optional[torch.Tensor]:
     """Append stage: write the batch's new tokens (one per query row, rows by
     qo_indptr) into ``db.kv_data`` at the end of each request's page list, turning
     the keys (and the queries, into ``q_out`` or a new tensor) by RoPE when
-    rope_theta > 0.  Returns the rotated queries (None with rotate_q False)."""
+    rope_theta > 0 (by their slots: refused after ``evict``).  Returns the rotated queries (None with rotate_q
+    False)."""
     b = db.host
+    if rope_theta > 0:
+        _positions_by_slot(b)
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
     if rotate_q and q_out is None:
         with _on(stream):
@@ -177,8 +185,10 @@ def append_kv_axes(db: DeviceBatch, k_new: torch.Tensor, v_new: torch.Tensor, ro
                    error: Optional[torch.Tensor] = None, stream=None) -> Optional[torch.Tensor]:
     """``append_kv`` with positions on several axes: ``rope`` from ``api.make_rope_axes`` (None: no
     rotation), ``positions`` [num_axes, new tokens] int32 on the device (None: each token's place in its
-    request).  Returns the rotated queries (None with rotate_q False)."""
+    request, refused after ``evict``).  Returns the rotated queries (None with rotate_q False)."""
     b = db.host
+    if rope is not None and positions is None:
+        _positions_by_slot(b)
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
     if rotate_q and q_out is None:
         with _on(stream):
@@ -215,6 +225,8 @@ def append_kv8(db: DeviceBatch, cache: Kv8Cache, k_new: torch.Tensor, v_new: tor
                stream=None) -> Optional[torch.Tensor]:
     """``append_kv_axes`` into the 8-bit cache (``db.kv_data`` is not used)."""
     b = db.host
+    if rope is not None and positions is None:
+        _positions_by_slot(b)
     params = api.make_params(b.num_qo_heads, b.num_kv_heads, b.head_dim, b.page_size, b.dtype, b.sm_scale)
     if rotate_q and q_out is None:
         with _on(stream):
@@ -296,8 +308,9 @@ def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[in
     Returns the batch with its shorter page tables, and the ids of the pages it no longer lists (on the host; with
     ``pages`` all it listed before, which other batches may still list).
     The key weights move with their keys, and are 0 in the kept pages' slots behind them and, in place, in the pages
-    that are no longer listed, so that a key that comes to lie there starts from 0.  Nothing is read back from the
-    GPU."""
+    that are no longer listed, so that a key that comes to lie there starts from 0.  A new token's slot is no longer its
+    position, so later appends need it given (``append_kv_axes``, ``append_kv8``; its count in the whole sequence), and
+    those that would turn keys by their slots refuse the batch.  Nothing is read back from the GPU."""
     b = db.host
     budgets = [int(budget)] * b.batch if isinstance(budget, int) else [int(x) for x in budget]
     if len(budgets) != b.batch or min(budgets, default=0) < 0:
@@ -321,7 +334,7 @@ def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[in
         if indices.numel() and not 0 <= int(indices.min()) <= int(indices.max()) < weights.shape[0]:
             raise ValueError("pages must be pages of the pool")
         _pages_listed_once(torch.cat([indices, freed]), "pages must be different ones that the batch does not list")
-    host = dataclasses.replace(b, kv_indptr=indptr, kv_indices=indices, kv_lens=kept,
+    host = dataclasses.replace(b, kv_indptr=indptr, kv_indices=indices, kv_lens=kept, moved=b.moved or kept != list(b.kv_lens),
                                kv_last_page_len=torch.tensor([n - (p - 1) * b.page_size if n else 0 for n, p in zip(kept, used)],
                                                              dtype=torch.int32))
     with _on(stream):

@@ -72,6 +72,7 @@ class PagedBatch:
     logits_cap: float = 0.0
     causal: bool = False
     name: str = ""
+    moved: bool = False  # keys were evicted and the others moved up: a key's slot is not its position
 
     @property
     def batch(self) -> int:

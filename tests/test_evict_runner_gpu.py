@@ -142,3 +142,18 @@ def test_new_keys_do_not_inherit_an_evicted_keys_weight(kv8, elsewhere):
         gained = (rows(w.unsqueeze(-1), one, r) - rows(old.unsqueeze(-1), one, r)).double().sum((-2, -1))
         # A row's probabilities add up to 1: HQ / HKV rows a head, sums of 100 a key rounded in fp32 (n 100 2^-24).
         assert bool(((gained - HQ // HKV).abs() < 1e-3).all())
+
+
+def test_an_eviction_is_remembered_where_keys_moved():
+    db, _ = make([70, 90], 5, 20)
+    rope, rows_ = api.make_rope_axes(1e4, D, [D // 2]), torch.zeros(2, HKV, D, dtype=BF, device="cuda")
+    whole, freed = runner.evict(db, runner.zero_key_weights(20, HKV, P), [70, 200])
+    assert not whole.host.moved and not freed.numel() and whole.host.kv_lens == [70, 90]
+    short, _ = runner.evict(whole, runner.zero_key_weights(20, HKV, P), [70, 89])
+    again, _ = runner.evict(short, runner.zero_key_weights(20, HKV, P), 1000)
+    for x in (short, again):
+        with pytest.raises(ValueError, match="position"):
+            runner.append_kv_axes(x, rows_, rows_, rope)
+    q = runner.append_kv_axes(short, rows_, rows_, rope, positions=ints([[69, 90]]))
+    assert q.shape == db.q.shape
+    torch.cuda.synchronize()

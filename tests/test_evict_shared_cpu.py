@@ -4,7 +4,7 @@ import dataclasses
 import pytest
 import torch
 
-from paged_kv_cache_bsr_gb300 import runner, workloads as W
+from paged_kv_cache_bsr_gb300 import api, runner, workloads as W
 
 
 def batch(shared=(), **kw):
@@ -36,3 +36,26 @@ def test_pages_to_fill_are_free_ones_of_the_pool(pages, match):
             continue
         with pytest.raises(ValueError, match=match):
             runner.evict(batch(shared), WEIGHTS, 20, pages=pages)
+
+
+def evicted():
+    db = batch()
+    db.host = dataclasses.replace(db.host, moved=True)
+    return db
+
+
+def test_appends_by_slot_are_refused_after_an_eviction():
+    """Keys and queries would be turned by their slots; without a rotation, or with positions, the call goes on (to
+    the check of its tensors)."""
+    rope, rows, cache = api.make_rope_axes(1e4, 64, [32]), torch.zeros(2, 1, 64, dtype=torch.bfloat16), runner.Kv8Cache(None, None)
+    for call in (lambda: runner.append_kv(evicted(), rows, rows, rope_theta=1e4, rotate_q=False),
+                 lambda: runner.append_kv_axes(evicted(), rows, rows, rope, rotate_q=False),
+                 lambda: runner.append_kv8(evicted(), cache, rows, rows, rope, rotate_q=False)):
+        with pytest.raises(ValueError, match="position"):
+            call()
+    for call in (lambda: runner.append_kv(batch(), rows, rows, rope_theta=1e4, rotate_q=False),
+                 lambda: runner.append_kv(evicted(), rows, rows, rotate_q=False),
+                 lambda: runner.append_kv_axes(evicted(), rows, rows, None, rotate_q=False),
+                 lambda: runner.append_kv_axes(evicted(), rows, rows, rope, torch.zeros(1, 2, dtype=torch.int32), rotate_q=False)):
+        with pytest.raises(AttributeError, match="qo_indptr"):   # past the check: the batch has no tensors on a GPU
+            call()
