@@ -338,7 +338,7 @@ def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[in
                                kv_last_page_len=torch.tensor([n - (p - 1) * b.page_size if n else 0 for n, p in zip(kept, used)],
                                                              dtype=torch.int32))
     with _on(stream):
-        host_budget = torch.tensor(budgets, dtype=torch.int32)
+        host_budget = torch.tensor(kept, dtype=torch.int32)  # (what they asked for may not fit 32 bits)
         keep = torch.empty(b.batch, b.num_kv_heads, max(kept, default=0), dtype=torch.int32, device=db.q.device)
         kept_len = torch.empty(b.batch, dtype=torch.int32, device=db.q.device)
         tables = [t.to(db.q.device) for t in (host.kv_indptr, host.kv_indices, host.kv_last_page_len)]

@@ -157,3 +157,12 @@ def test_an_eviction_is_remembered_where_keys_moved():
     q = runner.append_kv_axes(short, rows_, rows_, rope, positions=ints([[69, 90]]))
     assert q.shape == db.q.shape
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("budget", [2 ** 31, [10 ** 12, 20]])
+def test_budgets_past_32_bits_keep_every_key(budget):
+    db, _ = make([70, 90], 6, 20)
+    short, freed = runner.evict(db, torch.rand(20, HKV, P, device="cuda"), budget, window=3)
+    assert short.host.kv_lens == ([70, 90] if isinstance(budget, int) else [70, 20])
+    assert sorted(short.host.kv_indices.tolist() + freed.tolist()) == sorted(db.host.kv_indices.tolist())
+    torch.cuda.synchronize()
