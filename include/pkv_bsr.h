@@ -703,7 +703,8 @@ pkv_status pkv_add_key_weights(const pkv_params* params, int batch, int64_t tota
  *    how many.
  *  - weights, kv_pages, the page table and error_d as in pkv_add_key_weights (a key in a page
  *    out of range counts as one of the lowest weight).  Pages may be shared here.
- * A request whose row pointers or last-page length do not fit keeps nothing (flagged).
+ * A request whose row pointers or last-page length do not fit, or of more than 2^31 - 1 - 2^21
+ * keys, keeps nothing (flagged).
  * Plan-free and graph-capturable.
  * Errors: PKV_ERR_INVALID_ARG (null or misaligned pointers, sizes out of range),
  * PKV_ERR_UNSUPPORTED (page size; batch * num_kv_heads past 2^25), PKV_ERR_CUDA.
@@ -732,8 +733,8 @@ pkv_status pkv_select_keys(int batch, int num_kv_heads, int page_size, int64_t n
  *    kv8_scales.  weights: NULL, or moved too.
  *  - Only the n slots are written; the slots and pages behind them keep what they held.
  *  - error_d as in pkv_add_key_weights; an index that is no key of the request leaves its
- *    place as it was (16), a request with n past its keys, max_keep or its pages is skipped
- *    whole (16).
+ *    place as it was (16), a request with n past its keys, max_keep or its pages, or of more
+ *    keys than pkv_select_keys takes, is skipped whole (16).
  * params: num_kv_heads, head_dim (64 or 128), page_size, dtype.  Plan-free, graph-capturable.
  * Errors: PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED (also a pool of 2^32 - 1 head rows or
  * more), PKV_ERR_CUDA.

@@ -37,6 +37,9 @@ namespace pkv {
 namespace {
 
 constexpr unsigned kFullMask = 0xffffffffu;
+// Keys of a request: indices are 32-bit and run ahead of the last key by up to a page (2^20 slots)
+// or a few thousand keys.
+constexpr int kMaxKeys = INT_MAX - (1 << 21);
 
 // Where the keys of a batch are.
 struct Table {
@@ -60,7 +63,7 @@ __device__ __forceinline__ bool keys_of(const Table& t, int b, int& page0, int& 
   if (p0 < 0 || p1 < p0 || p1 > t.kv_pages) return false;
   if (p1 == p0) return true;
   const int64_t n = static_cast<int64_t>(p1 - p0 - 1) * t.page_size + last;
-  if (last < 1 || last > t.page_size || n > INT_MAX - 256) return false;
+  if (last < 1 || last > t.page_size || n > kMaxKeys) return false;
   len = static_cast<int>(n);
   return true;
 }
@@ -207,9 +210,11 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) select_keys_kernel(co
   int32_t* out = a.keep + static_cast<int64_t>(list) * a.max_keep;
   if (h == 0 && rank == 0 && tid == 0) a.kept_len[b] = n;
   // The keys that stay anyway, and what is past the list.
-  for (int i = rank * THREADS + tid; i < a.max_keep; i += share * THREADS) {
+  const uint32_t step = share * THREADS;  // (unsigned: the last step may pass 2^31)
+  for (uint32_t at = rank * THREADS + tid; at < static_cast<uint32_t>(a.max_keep); at += step) {
+    const int i = static_cast<int>(at);
     if (i >= front && i < n - tail && pick < mid) {
-      i += (n - tail - 1 - i) / (share * THREADS) * (share * THREADS);  // the chosen ones are written below
+      at += (n - tail - 1 - i) / step * step;  // the chosen ones are written below
       continue;
     }
     out[i] = i >= n ? -1 : i >= n - tail ? len - (n - i) : i;
@@ -650,7 +655,7 @@ extern "C" pkv_status pkv_compact_paged_kv(const pkv_params* p, int batch, int64
   if (!dst_indptr_d) {
     while (a.split < row / 32 && lists * 2 * a.split < 2 * sms) a.split *= 2;
   } else {
-    const int64_t rounds = (max_keep + kCmpThreads * kSteps / (row / 16) - 1) / (kCmpThreads * kSteps / (row / 16));
+    const int per_round = kCmpThreads * kSteps / (row / 16), rounds = max_keep / per_round + (max_keep % per_round != 0);
     while (a.parts < 16 && a.parts * 2 <= rounds && lists * 2 * a.parts < 4 * sms) a.parts *= 2;
   }
   a.roles = 2 * a.split * a.parts + (kv8_scales || weights ? 1 : 0);
