@@ -669,8 +669,8 @@ pkv_status pkv_batch_prefill_ragged(const pkv_plan* plan, const void* q, int64_t
  *  - kv8_scales: NULL for the 16-bit cache, else kv holds the 8-bit cache's codes.
  *  - A row whose lse is -inf adds nothing, whatever its query holds (rows that saw no key,
  *    rows of a padded batch); a NaN lse makes the weights of the keys that the row sees NaN.
- *  - A page may be listed by one request only (a shared prefix is a request of its own, see
- *    above): two that list it would write its weights at the same time.
+ *  - A page may be listed once only (a shared prefix is a request of its own, see above):
+ *    where it is listed twice its weights would be written twice at the same time.
  *  - Only slots of keys are written.  Sums are fp32 and in an order fixed by the arguments:
  *    equal calls give equal bits.  Plan-free and graph-capturable: which kernel runs depends
  *    on total_q / batch, the group and head_dim, everything else on the device arrays.
@@ -679,7 +679,9 @@ pkv_status pkv_batch_prefill_ragged(const pkv_plan* plan, const void* q, int64_t
  *    to their row's largest element, as in pkv_batch_decode_paged_kv8.
  *  - error_d: device int32 or NULL, OR-ed with 1 (a page id out of range: such keys are
  *    skipped), 16 (a request whose row pointers, last-page length or rows do not fit: it is
- *    skipped whole) or 4 (a bounded wait ran out).  The caller clears it.
+ *    skipped whole, and where the row pointers do not ascend keys of other requests may be
+ *    skipped too) or 4 (a bounded wait ran out; the keys that it kept waiting keep their
+ *    weights).  The caller clears it.
  * params: num_qo_heads, num_kv_heads (group 1/2/4/8), head_dim 64 or 128, page_size, dtype
  * (of q, and of kv without scales), sm_scale, logits_cap, causal.
  * Errors: PKV_ERR_INVALID_ARG (null or misaligned pointers, sizes or decay out of range, no

@@ -135,6 +135,13 @@ __device__ __forceinline__ Request load_request(const WeightArgs& a, int b) {
   return r;
 }
 
+// Records request b if its arrays do not fit.  Every request is looked at by one thread: a tile finds
+// its request by a search that takes the row pointers to ascend, and where they do not it may meet
+// neither a request that does not fit nor one that does.
+__device__ __forceinline__ void check_request(const WeightArgs& a, int b) {
+  if (!load_request(a, b).ok) flag(a, kErrAppendLayout);
+}
+
 // ---------------------------------------------------------------------------- stream
 template <typename T>
 __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -237,6 +244,8 @@ __global__ void __launch_bounds__(StreamShape<D, KV8>::kWarps * 32, 1) key_weigh
   const int64_t listed = min(max(static_cast<int64_t>(__ldg(a.kv_indptr + a.batch)), int64_t{0}), a.kv_pages);
   const int64_t U = listed * P / K + a.batch;  // places of tiles per kv head
   const int64_t run = (U * a.hkv + workers - 1) / workers;
+  for (int64_t r = (workers - 1 - worker) * 32 + lane; r < a.batch; r += workers * 32)  // (the last workers have the least to do)
+    check_request(a, static_cast<int>(r));
   int64_t f = worker * run;
   const int64_t f_end = min(f + run, U * a.hkv);
   while (f < f_end) {
@@ -247,10 +256,7 @@ __global__ void __launch_bounds__(StreamShape<D, KV8>::kWarps * 32, 1) key_weigh
     const int64_t c0 = first_tile<K>(a, b), c1 = b + 1 < a.batch ? first_tile<K>(a, b + 1) : U;
     const int64_t stop = min(f_end, base + max(c1, u + 1));
     f = stop;
-    if (!rq.ok) {
-      if (lane == 0) flag(a, kErrAppendLayout);
-      continue;
-    }
+    if (!rq.ok) continue;
     const int n_tiles = (rq.kv_len - 1 + K) / K;
     const int t_end = static_cast<int>(min(static_cast<int64_t>(n_tiles), stop - base - c0));
     const int t_begin = static_cast<int>(max(u - c0, int64_t{0}));
@@ -603,18 +609,17 @@ __global__ void __launch_bounds__(kTileThreads, kTileCtas)
   const int h = static_cast<int>(item - u * a.hkv);
   int b = 0;
   int64_t tile = 0;
+  const uint32_t back = gridDim.x - 1 - blockIdx.x;  // the last CTAs have the least to do; there is one a request at least
+  if (back <= static_cast<uint32_t>(a.batch) / kTileThreads && back * kTileThreads + tid < static_cast<uint32_t>(a.batch))
+    check_request(a, back * kTileThreads + tid);
   if (a.by_level) {
-    if (blockIdx.x == 0 && tid < a.batch && !load_request(a, tid).ok) flag(a, kErrAppendLayout);
     if (!tile_by_level(a, u, lane, b, tile)) return;  // the same for all CTAs of a cluster
   } else {
     b = find_request<kTileKeys>(a, u, lane);
     tile = u - first_tile<kTileKeys>(a, b);
   }
   const Request rq = load_request(a, b);
-  if (!rq.ok || tile < 0 || tile * kTileKeys >= rq.kv_len) {  // the same for all CTAs of a cluster
-    if (!rq.ok && tid == 0) flag(a, kErrAppendLayout);
-    return;
-  }
+  if (!rq.ok || tile < 0 || tile * kTileKeys >= rq.kv_len) return;  // the same for all CTAs of a cluster
   const int k0 = static_cast<int>(tile) * kTileKeys;
   const int off = rq.kv_len - rq.rows;
   const int row_first = a.causal ? min(max(k0 - off, 0), rq.rows) : 0;  // the first row that sees key k0
