@@ -1014,9 +1014,13 @@ extern "C" pkv_status pkv_add_key_weights(const pkv_params* p, int batch, int64_
   a.lg = g == 1 ? 0 : g == 2 ? 1 : g == 4 ? 2 : 3;
   a.causal = p->causal != 0 && qo_indptr_d;
   // The tensor core cuts its partial sums off: of 400000 products over 128 dims, those within one standard
-  // deviation of 0 were 0.7e-7 of themselves nearer to 0 than the exact ones, those past three 1.4e-7, in a
-  // large logit (20) 2e-6 of its weight.  The tile kernel adds 1e-7, and what the rounding of the scale
-  // took, by a second product (3 us of those prompts' 65, an error of 6e-7 of the weights to 1.3e-7).
+  // deviation of 0 were 0.7e-7 of themselves nearer to 0 than the exact ones, those past three 1.4e-7.  The tile
+  // kernel adds 1e-7, and what the rounding of the scale took, by a second product (3 us of 65 on 10 prompts of
+  // 128 to 1500 rows).  What it brings and costs, as errors of the weights: prompts over keys of unlike sizes
+  // (logits to 20) 1.7e-7, without it 1.3e-6; sums that lose nothing (one nonzero element a row), where it is the
+  // error itself, 1.6e-6 at logits to 22 and 6.5e-6 at 90, without it 1e-7 and 3e-7.  Rows of queries and keys are
+  // dense, so the first counts, and the second is two roundings of the logit in fp32 (2^-24 each).  The branch for
+  // arguments past the cap's polynomial and the stream kernel do without.
   const double scale = static_cast<double>(p->sm_scale) * 1.4426950408889634;
   a.scale = static_cast<float>(scale);
   a.scale_lo = static_cast<float>(scale / a.scale * (1 + 1e-7) - 1);
