@@ -217,16 +217,26 @@ def _host_i32(t):
     return t.contiguous()
 
 
+def _plan_arrays(batch: int, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h):
+    """The host arrays of a batch as int32, none shorter than what is read of it."""
+    qo, ip, ix, la = _host_i32(qo_indptr_h), _host_i32(kv_indptr_h), _host_i32(kv_indices_h), _host_i32(kv_last_page_len_h)
+    if (qo is not None and qo.numel() <= batch) or (ip is not None and ip.numel() <= batch) or (la is not None and la.numel() < batch):
+        raise ValueError("qo_indptr and kv_indptr must have batch + 1 entries, kv_last_page_len batch")
+    if ix is not None and ip is not None and batch >= 0 and ix.numel() < ip[batch].item():
+        raise ValueError("kv_indices must have an entry for each of kv_indptr's pages")
+    return qo, ip, ix, la
+
+
 def plan_compute(h, batch: int, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h, num_pages: int,
                  host_ws: torch.Tensor) -> None:
-    qo, ip, ix, la = (_host_i32(x) for x in (qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h))
+    qo, ip, ix, la = _plan_arrays(int(batch), qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h)
     _check(load().pkv_plan_compute(h, int(batch), _ptr(qo), _ptr(ip), _ptr(ix), _ptr(la), int(num_pages),
                                    _ptr(host_ws), host_ws.numel() * host_ws.element_size()), "pkv_plan_compute")
 
 
 def plan_run(h, batch: int, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h, num_pages: int,
              dev_ws: torch.Tensor, host_ws: torch.Tensor, stream=None) -> None:
-    qo, ip, ix, la = (_host_i32(x) for x in (qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h))
+    qo, ip, ix, la = _plan_arrays(int(batch), qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_page_len_h)
     _check(load().pkv_plan_run(h, int(batch), _ptr(qo), _ptr(ip), _ptr(ix), _ptr(la), int(num_pages),
                                _ptr(dev_ws), dev_ws.numel() * dev_ws.element_size(), _ptr(host_ws),
                                host_ws.numel() * host_ws.element_size(), _stream(stream)), "pkv_plan_run")
