@@ -673,7 +673,10 @@ pkv_status pkv_batch_prefill_ragged(const pkv_plan* plan, const void* q, int64_t
  *    where it is listed twice its weights would be written twice at the same time.
  *  - Only slots of keys are written.  Sums are fp32 and in an order fixed by the arguments:
  *    equal calls give equal bits.  Plan-free and graph-capturable: which kernel runs depends
- *    on total_q / batch, the group and head_dim, everything else on the device arrays.
+ *    on total_q / batch, the group and head_dim, everything else on the device arrays.  (The
+ *    last bits of a weight go with the kernel.)  Up to 32 (row, head) pairs a request and kv
+ *    head on average, and at head_dim 64, the kernel for few rows runs, on which a request of
+ *    many rows is slow: weigh prompts in a call of their own, not beside decode rows.
  *  - Keys are 16-bit operands of the tensor cores with fp32 sums; from the 8-bit cache their
  *    codes are exact, and for few rows per request queries keep 11 significant bits relative
  *    to their row's largest element, as in pkv_batch_decode_paged_kv8.
@@ -707,6 +710,8 @@ pkv_status pkv_add_key_weights(const pkv_params* params, int batch, int64_t tota
  *    out of range counts as one of the lowest weight).  Pages may be shared here.
  * A request whose row pointers or last-page length do not fit, or of more than 2^31 - 1 - 2^21
  * keys, keeps nothing (flagged).
+ * Lists are laid out for the batch's average length (kv_pages * page_size / batch): one far
+ * longer than the rest is slow, and better chosen from in a call of its own.
  * Plan-free and graph-capturable.
  * Errors: PKV_ERR_INVALID_ARG (null or misaligned pointers, sizes out of range),
  * PKV_ERR_UNSUPPORTED (page size; batch * num_kv_heads past 2^25), PKV_ERR_CUDA.

@@ -9,19 +9,25 @@
 // ballots.  (The first digit holds the exponent and three bits of the mantissa.)  The weights
 // are read from global memory once and kept in shared memory as ordered 32-bit integers
 // (what does not fit is read again).  The CTAs of a cluster share a long list, each a
-// contiguous slice; they add their digit counts through distributed shared memory.  Bound
-// by latency: loops are unrolled over independent keys, and a digit is found by 64 threads
-// that each add up the counts above one (a chain of shuffles took 4800 of a list's 36000
-// cycles).  Measured, 8 kv heads: 64 requests of 512 to 4096 keys 15.2 us (20.7 us with
-// digits of 8 bits and a key at a time), 2 requests of 10^5 keys 25.4 us (50.3 us).
+// contiguous slice; they add their digit counts through distributed shared memory.  Each of
+// five passes looks at every key (issue slots 57 % busy on average, 74 % on the busiest SM,
+// on the batch below) and ends at a barrier; loops are unrolled over independent keys, and
+// a digit is found by 64 threads that each add up the counts above one (a chain of shuffles
+// took 4800 of a list's 36000 cycles).  Measured, 8 kv heads: 64 requests of 512 to 4096 keys 15.4 us (20.7 us with
+// digits of 8 bits and a key at a time), 2 requests of 10^5 keys 25.4 us (50.3 us).  CTAs
+// and shared memory a list go by the average length, which the host knows: one request of
+// 10^5 keys among 63 of 500 takes 1000 us, most of its keys being read again in each pass.
 //
 // Compact.  A kept key moves from its token index s to its place i <= s in the list of
 // kept keys.  In place, a CTA owns a column slice of one (request, kv head, K or V) and
 // moves the rows in order, 128 to 1024 at a time: every thread has read its part of a round before
 // any writes it, and what a round writes lies before everything later rounds read
 // (s >= i), so the next round is read ahead of the writes.  Slices of 32 bytes or more
-// give a single request enough CTAs; into other pages rounds are independent, and go to
-// as many CTAs as the chip holds.  HBM-bound: each kept row read once and written once.
+// give a list up to 16 CTAs (8 in the 8-bit cache at head_dim 128), and one more moves scales
+// and weights; into other pages rounds are independent, and go to as many CTAs as the chip
+// holds.  A batch is HBM-bound, each kept row read once and written once: 64 requests of 512
+// to 4096 keys, half kept, 118 us, 80 % of measured bandwidth.  One request alone is not: of
+// 10^5 keys, 8 kv heads, half kept, 237 us (8-bit cache 226) against 62 (32) for its bytes.
 #include <cuda_runtime.h>
 #include <limits.h>
 #include <math.h>

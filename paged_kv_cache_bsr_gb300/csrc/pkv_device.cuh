@@ -347,7 +347,7 @@ __device__ __forceinline__ void tmem_ld32_sync(uint32_t taddr, uint32_t (&r)[32]
       : "r"(taddr)
       : "memory");
 }
-// 128 consecutive fp32 columns of this thread's TMEM lane: four loads, one wait.
+// 64 consecutive fp32 columns of this thread's TMEM lane: two loads, one wait.
 __device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]) {
   asm volatile(
       "{\n\t.reg .b32 a1;\n\tadd.u32 a1, %64, 32;\n\t"
@@ -360,6 +360,7 @@ __device__ __forceinline__ void tmem_ld64_sync(uint32_t taddr, uint32_t (&r)[64]
       : "r"(taddr)
       : "memory");
 }
+// 128 consecutive columns: four loads, one wait.
 __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, uint32_t (&r)[128]) {
   asm volatile(
       "{\n\t.reg .b32 a1, a2, a3;\n\t"
@@ -380,9 +381,8 @@ __device__ __forceinline__ void tmem_ld128_sync(uint32_t taddr, uint32_t (&r)[12
 }
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// True in one lane of a converged warp.  A branch on it tells the compiler that a single thread is
-// inside: in a branch on the lane number every tcgen05.mma is issued with a check that its operands
-// are alike across the lanes, 125 cycles a product where 64 would do.
+// True in one lane of a converged warp.  The products are issued in a branch on it: by clocks around
+// them a tcgen05.mma of 128 x 128 x 16 takes 64 cycles there, and 125 in a branch on the lane number.
 __device__ __forceinline__ bool elect_one() {
   uint32_t one;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));

@@ -24,10 +24,17 @@
 //    exponentials over the columns in registers.  Four CTAs share an SM, so that one's
 //    start and waits are another's products.  Many columns before few keys are shared by
 //    the CTAs of a cluster, which add their sums in rank order through distributed shared
-//    memory.  Prompts are bound by L2 (each key tile streams its request's queries): 10 of
-//    128 to 1500 rows, 8 kv heads, group 4, 64 us, 456 MB at 7.1 TB/s, where boxes of
-//    128-byte rows come at about 9 on all SMs.  Few columns are bound by a tile's start:
-//    the last 32 to 64 rows of 7 prompts of 2000 to 9000 keys, group 2, capped, 40 us.
+//    memory.  10 prompts of 128 to 1500 rows, 8 kv heads, group 4, take 64 us: 18064 column
+//    tiles, 1100 cycles each on an SM, where the product takes 432, the exponentials 256 and
+//    the queries' copies (296 MB) half of what TMA brings from L2.  No unit is the limit;
+//    what is left (counted, not timed apart) is what the key warps do around a tile: its lse
+//    through shared memory, their barrier, the wait for the one S.  Few columns pay for a key
+//    tile's start (tensor memory, page ids, staging): the last 32 to 64 rows of 7 prompts of
+//    2000 to 9000 keys, group 2, capped, 40 us.
+// The choice between them goes by the batch's average rows, which the host knows: a request
+// of many rows among few-row ones is right but slow on the stream kernel, whose warps share
+// keys and never columns (63 decode rows over 2000 keys beside a prompt of 400 rows, 8 kv
+// heads, group 4: 1290 us in one call, 75 us in two).
 // Both find their work from the device's row pointers alone: request b's tiles start at
 //     first(b) = floor(kv_indptr[b] P / K) + b        (K keys a tile),
 // which leaves each request room for its ceil(len / K) tiles and at most one unused
