@@ -633,6 +633,8 @@ pkv_status pkv_batch_prefill_paged_kv8(const pkv_plan* plan, const void* q, cons
  *    stream is captured).
  *  - Built for head_dim 128 and groups 1/2/4/8.  Causal or not (params->causal), rows and
  *    keys of a request counted apart: a row that sees no key gets o = 0, lse = -inf.
+ *  - Probabilities are rounded to params->dtype as operands of P V, as in
+ *    pkv_batch_prefill_paged; sums, maxima and o before its rounding are fp32.
  *  - Rows of k and v of other requests have no part in a request's result, NaN or not.  A
  *    value that is NaN or infinite may make NaN also of rows of its request that share its
  *    128-key block and do not see it (0 times it); a key's does not.
