@@ -322,6 +322,8 @@ def evict(db: DeviceBatch, weights: torch.Tensor, budget: Union[int, Sequence[in
     first = [int(x) for x in b.kv_indptr]
     source = b.kv_indices[first[0]:first[-1]]
     none = source[:0]
+    if source.numel() and not 0 <= int(source.min()) <= int(source.max()) < weights.shape[0]:
+        raise ValueError("kv_indices must be pages of the pool")
     if pages is None:
         _pages_listed_once(source, "a page is listed twice: shared pages need others to move their keys to (pages)")
         indices = torch.cat([none, *(b.kv_indices[s:s + n] for s, n in zip(first, used))])

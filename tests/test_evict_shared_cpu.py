@@ -38,6 +38,15 @@ def test_pages_to_fill_are_free_ones_of_the_pool(pages, match):
             runner.evict(batch(shared), WEIGHTS, 20, pages=pages)
 
 
+@pytest.mark.parametrize("page", [-1, 9, 2 ** 31 - 1])
+@pytest.mark.parametrize("pages", [None, [5, 6, 7, 8]])
+def test_tables_past_the_pool_are_refused(page, pages):
+    db = batch()
+    db.host.kv_indices[1] = page
+    with pytest.raises(ValueError, match="of the pool"):
+        runner.evict(db, WEIGHTS, 20, pages=pages)
+
+
 def evicted():
     db = batch()
     db.host = dataclasses.replace(db.host, moved=True)
