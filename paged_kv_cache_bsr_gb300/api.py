@@ -222,7 +222,7 @@ def _plan_arrays(batch: int, qo_indptr_h, kv_indptr_h, kv_indices_h, kv_last_pag
     qo, ip, ix, la = _host_i32(qo_indptr_h), _host_i32(kv_indptr_h), _host_i32(kv_indices_h), _host_i32(kv_last_page_len_h)
     if (qo is not None and qo.numel() <= batch) or (ip is not None and ip.numel() <= batch) or (la is not None and la.numel() < batch):
         raise ValueError("qo_indptr and kv_indptr must have batch + 1 entries, kv_last_page_len batch")
-    if ix is not None and ip is not None and batch >= 0 and ix.numel() < ip[batch].item():
+    if ix is not None and ip is not None and batch >= 0 and ix.numel() < ctypes.c_int32.from_address(ip.data_ptr() + 4 * batch).value:
         raise ValueError("kv_indices must have an entry for each of kv_indptr's pages")
     return qo, ip, ix, la
 
